@@ -79,6 +79,21 @@ def _declare(lib):
     lib.kda_chunk_prefill_segmented_workspace_size.restype = sz
     lib.kda_chunk_prefill_auto_segments.argtypes = [i32, i64, i32, i32, i32, i32, i32]
     lib.kda_chunk_prefill_auto_segments.restype = i32
+    f32 = ctypes.c_float
+    lib.kda_rotary.argtypes = [vp, i64, vp, i64, i32, vp, i64, vp, i64, i32, vp, vp, f32, i64, i32,
+                               i32, i32, i32, vp]
+    lib.kda_rotary.restype = i32
+    lib.kda_cache_write.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i32, vp, vp, i32, i64, i32,
+                                    i32, i64, i32, i32, vp]
+    lib.kda_cache_write.restype = i32
+    lib.kda_cache_read.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, i32, i64, i32, i32, i64, i32, vp,
+                                   vp, i32, vp]
+    lib.kda_cache_read.restype = i32
+    lib.kda_cache_attention.argtypes = [vp, i64, vp, vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32,
+                                        i32, i32, i64, i32, f32, i64, i32, i32, vp, sz, vp]
+    lib.kda_cache_attention.restype = i32
+    lib.kda_cache_attention_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+    lib.kda_cache_attention_workspace_size.restype = sz
     lib.kda_static_workspace_status.argtypes = [vp, vp]
     lib.kda_static_workspace_status.restype = i32
     return lib

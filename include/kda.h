@@ -375,6 +375,126 @@ kda_status kda_spec_commit(const void *k, const void *v, const void *z, const vo
                            int H, int d_k, int d_v, kda_dtype dtype, cudaStream_t stream);
 
 /*
+ * ---- The global-attention layer beside the recurrent ones ----
+ *
+ * The same page that defines the gate interleaves three of these recurrent
+ * layers with one layer of global attention ("How Kimi K3 is built", section
+ * "Sequence: three KDA to one global MLA"), and its section "How to serve two
+ * different caches" sets the recurrent state beside the attention layer's
+ * cache.  The pages give no formulas for positions or for a cache in 8 bits;
+ * the definitions below are this library's own.  The operators are those a step
+ * of such a layer needs around its projections: kda_rotary, kda_cache_write,
+ * kda_cache_attention, and kda_cache_read to take cached tokens out again.
+ *
+ * Token strides.  Where an argument x has a companion x_stride, x is
+ * [tokens, H, d] with H * d dense elements for each token and x_stride
+ * elements from one token to the next, a multiple of 16 bytes; so q, k and v may be
+ * views of one projection's output.
+ *
+ * The cache is a pool of pages of `page` tokens (16, 32, 64, 128 or 256),
+ * owned by the caller, d a multiple of 16 up to 128:
+ *   k_codes, v_codes  [n_pages, H_kv, page, d] e4m3 (1 sign, 4 exponent, 3
+ *                     fraction bits; largest 448; no infinities)
+ *   k_scale, v_scale  [n_pages, H_kv] fp32: x = code * scale
+ *   block_table       device int32 [n_seqs, table_pages]: the pages of each
+ *                     sequence, in order.  An entry outside [0, n_pages) is a page
+ *                     that is not held: what would be written there is
+ *                     dropped, reading it gives zeros, and attention does not
+ *                     see its tokens.  So are positions past the table.
+ * A scale is the least power of two, at least 2^-100, that brings every finite
+ * value of the page's tokens to 448 or less.  Pages start out with any
+ * contents; writing a page's first token starts its scale anew.
+ */
+
+/* Which channels of a head make a pair: (i, i + rot/2) or (2i, 2i + 1). */
+typedef enum { KDA_ROTARY_HALF = 0, KDA_ROTARY_INTERLEAVED = 1 } kda_rotary_layout;
+
+/*
+ * kda_rotary -- rotary positions on a step's queries and keys, in one launch.
+ * With a = positions[t] * freq[i], for each pair (x, y) of the first rot
+ * channels of every head:
+ *   (x, y) <- amplitude * (x cos a - y sin a, y cos a + x sin a)
+ * and the channels past rot are copied.  Scaling for long contexts is a matter of
+ * freq and amplitude alone.  The angle is reduced in 64 bits, so that far
+ * positions lose nothing; x, cos and sin are fp32, rounded once to dtype.
+ *   q, k       [n_tokens, H, d] with token strides; H_k may be 0 (k unused)
+ *   q_out, k_out  likewise (written); may be q and k with the same strides,
+ *              and must not overlap them otherwise
+ *   positions  device int32 [n_tokens] (negative ones turn the other way)
+ *   freq       device fp64 [rot / 2], radians a position
+ *   rot        even, 2 .. d;  d at most 256, whole 16-byte vectors
+ */
+kda_status kda_rotary(const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride, int H_q,
+                      const void *k, int64_t k_stride, void *k_out, int64_t k_out_stride, int H_k,
+                      const int32_t *positions, const double *freq, float amplitude,
+                      int64_t n_tokens, int d, int rot, kda_rotary_layout layout, kda_dtype dtype,
+                      cudaStream_t stream);
+
+/*
+ * kda_cache_write -- quantises new keys and values into the cache.
+ * Sequence n brings T tokens (cu_seqlens == NULL; k and v are [n_seqs * T, H_kv,
+ * d]) or those of rows cu_seqlens[n] .. cu_seqlens[n + 1] (device int32
+ * [n_seqs + 1]; k and v are [T, H_kv, d], T all rows), for its positions from
+ * start[n] on (device int32 [n_seqs]).
+ * A page that already holds tokens of the sequence keeps the larger of its
+ * scale and the new tokens' own; where that grows it, the older codes are
+ * rounded again to the new scale, which is exact but for values below
+ * 2^-6 of it.  code = e4m3(x / scale), nearest, ties to even; infinities
+ * become 448, NaN stays NaN, and neither counts for the scale.
+ * No two sequences may write to the same page in one call.  Malformed
+ * cu_seqlens are clamped into [0, T]: results are then unspecified, but no
+ * access leaves the buffers.
+ */
+kda_status kda_cache_write(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                           void *k_codes, void *v_codes, float *k_scale, float *v_scale,
+                           const int32_t *block_table, int table_pages, const int32_t *start,
+                           const int32_t *cu_seqlens, int n_seqs, int64_t T, int H_kv, int d,
+                           int64_t n_pages, int page, kda_dtype dtype, cudaStream_t stream);
+
+/*
+ * kda_cache_read -- cached tokens as dense rows: k and v (written) are laid out
+ * as the inputs of kda_cache_write with dense rows, x = code * scale rounded
+ * once to dtype.  Arguments as there.
+ */
+kda_status kda_cache_read(const void *k_codes, const void *v_codes, const float *k_scale,
+                          const float *v_scale, const int32_t *block_table, int table_pages,
+                          const int32_t *start, const int32_t *cu_seqlens, int n_seqs, int64_t T,
+                          int H_kv, int d, int64_t n_pages, int page, void *k, void *v,
+                          kda_dtype dtype, cudaStream_t stream);
+
+/*
+ * kda_cache_attention -- attention of the T_q newest tokens of each sequence
+ * over its cached tokens, their own included.  With p = lengths[b] - T_q + i the
+ * position of query i, and head h reading the keys of head h / (H_q / H_kv):
+ *   sees(t)  = t <= p, and (window == 0 or t > p - window or t < sinks), and t's
+ *              page is held
+ *   o[b, i, h] = sum_t w_t v_t,  w = softmax over the seen t of scale * q . k_t
+ *   lse[b, i, h] = log sum_t exp(scale * q . k_t)
+ * A row that sees no token, or whose scores are all -inf, gives o = 0 and
+ * lse = -inf.  What lies in tokens that a row does not see (NaN included) does
+ * not reach it.
+ *   q          [B * T_q, H_q, d] with a token stride
+ *   lengths    device int32 [B], tokens of each sequence with the T_q newest;
+ *              clamped into [0, table_pages * page]
+ *   o          [B, T_q, H_q, d] in dtype (written)
+ *   lse        nullable; fp32 [B, T_q, H_q] (written)
+ *   workspace  kda_cache_attention_workspace_size() bytes, 256-byte aligned;
+ *              contents on entry are ignored
+ * Scores, sums and outputs are fp32 until the one rounding to dtype.
+ */
+kda_status kda_cache_attention(const void *q, int64_t q_stride, const void *k_codes,
+                               const void *v_codes, const float *k_scale, const float *v_scale,
+                               const int32_t *block_table, int table_pages, const int32_t *lengths,
+                               void *o, float *lse, int B, int T_q, int H_q, int H_kv, int d,
+                               int64_t n_pages, int page, float scale, int64_t window, int sinks,
+                               kda_dtype dtype, void *workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
+
+/* Workspace bytes of kda_cache_attention (0 for sizes it does not take). */
+size_t kda_cache_attention_workspace_size(int B, int T_q, int H_q, int H_kv, int d, int page,
+                                          int table_pages);
+
+/*
  * Instrumentation (not part of the layer's arithmetic).  While `events` is
  * non-NULL, every later prefill, decode or speculative call made on this
  * thread records events[0] on its stream before its first kernel and
