@@ -81,13 +81,15 @@ class Cache:
 
 
 def attention(q, cache, table, lengths, scale, window=0, sinks=0):
-    """o, lse, and for each row the bound-giving sum of w |v| and largest sum of |q k| scale; 64 bits."""
+    """o, lse, and what bounds a row's error: sum of w |v|, the largest sum of |q k| scale, and the largest w times
+    its page's scale of v, times the sum of |v| / scale.  64 bits."""
     q = q.cpu().double()
     B, t_q, h_q, d = q.shape
     group = h_q // cache.heads
     o, weight = torch.zeros(q.shape, dtype=F64), torch.zeros(q.shape, dtype=F64)
     lse = torch.full((B, t_q, h_q), -math.inf, dtype=F64)
     size = torch.zeros((B, t_q, h_q), dtype=F64)
+    floor = torch.zeros(q.shape, dtype=F64)
     for b in range(B):
         length = max(0, min(int(lengths[b]), table.shape[1] * cache.page))
         if length == 0:
@@ -98,6 +100,7 @@ def attention(q, cache, table, lengths, scale, window=0, sinks=0):
             continue
         at = torch.tensor([g[0] for g in got])
         k, v = torch.stack([g[1] for g in got]), torch.stack([g[2] for g in got])   # [t, H_kv, d]
+        of_page = torch.stack([cache.scale["v"][cache.page_of(table, b, g[0])] for g in got])   # [t, H_kv]
         for i in range(t_q):
             p = length - t_q + i
             sees = at <= p
@@ -115,5 +118,7 @@ def attention(q, cache, table, lengths, scale, window=0, sinks=0):
                 w = torch.exp(s - lse[b, i, h])
                 o[b, i, h] = (w[:, None] * vv).sum(0)
                 weight[b, i, h] = (w[:, None] * vv.abs()).sum(0)
+                vs = of_page[sees, h // group]
+                floor[b, i, h] = (w * vs).max() * (vv.abs() / vs[:, None]).sum(0)
                 size[b, i, h] = abs(scale) * (kk * q[b, i, h]).abs().sum(-1).max()
-    return o, lse, weight, size
+    return o, lse, weight, size, floor

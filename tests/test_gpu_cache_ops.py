@@ -226,17 +226,19 @@ def _check_attention(q, cache, table, lengths, got_o, got_lse, scale=None, windo
     scalings; its exponential adds 2^-21.  Weights go to the product with the values in fp16 (half a step
     2^-11) for bf16 outputs, in two fp16 pieces (2^-21) for fp32 ones; sums of n terms in 32 bits add
     2^-24 (n / 16 + 64).  All of it counts on sum w |v|, twice for the division by the sum; then
-    half a step of the output's type.
+    half a step of the output's type.  The half step of an fp16 weight is relative only down to fp16's least
+    normal number; below, it is half of 2^-24, with the largest weight (times its page's scale) at 2^12: an error of
+    2^-37 of the largest for each token.
     fp16 queries hold their row's largest value to 2^-25, an error of the score of d 2^-25 S at most."""
     table, lengths = table.cpu(), lengths.cpu()
     d = q.shape[-1]
     scale = 1 / math.sqrt(d) if scale is None else scale
     c = ref.Cache(cache)
-    o, lse, weight, size = ref.attention(q, c, table, lengths, scale, window, sinks)
+    o, lse, weight, size, floor = ref.attention(q, c, table, lengths, scale, window, sinks)
     n = int(lengths.max())
     score = 2.0 ** -24 * (2 * d + 8) * size
     step = (2.0 ** -11 if q.dtype == BF16 else 2.0 ** -21) + 2.0 ** -21 + 2.0 ** -24 * (n / 16 + 64)
-    tol = HALF_STEP[q.dtype] * o.abs() + 2 * (score + step)[..., None] * weight + 1e-30
+    tol = HALF_STEP[q.dtype] * o.abs() + 2 * (score + step)[..., None] * weight + 2.0 ** -37 * floor + 1e-30
     err = (got_o.cpu().double() - o).abs()
     finite = torch.isfinite(o)
     assert torch.equal(torch.isnan(got_o.cpu()), torch.isnan(o))
