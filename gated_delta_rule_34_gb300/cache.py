@@ -6,7 +6,7 @@ layout, and their data pointers plus the current CUDA stream are handed to ``lib
 """
 from __future__ import annotations
 
-import contextlib
+import functools
 import math
 from typing import NamedTuple
 
@@ -15,22 +15,30 @@ import torch
 from .api import _check, _dtype_code, lib
 
 LAYOUTS = {"half": 0, "interleaved": 1}
-_NO_SWITCH = contextlib.nullcontext()
+E4M3, F32, F64, I32 = torch.float8_e4m3fn, torch.float32, torch.float64, torch.int32
+
+# A decode step's kernels take a few microseconds, so the checks below cost as much as
+# they do: one plain condition decides that all is well, and what is wrong is looked for
+# only where it is not.
 
 
-def _on(device):
-    """Makes ``device`` current for a call, unless it already is."""
-    return _NO_SWITCH if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _call(index: int, fn, *args) -> None:
+    """fn(*args, stream) with device ``index`` current, on its current stream."""
+    if index == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        _check(status)
 
 
-def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-def _tensor(name, t, dtype, shape, device):
-    """A dense CUDA tensor of this dtype and shape (-1: any size)."""
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+def _tensor(name, t, dtype, shape, index):
+    """A dense CUDA tensor of this dtype and shape (-1: any size) on device ``index``."""
+    if t.dtype is dtype and t.get_device() == index >= 0 and t.is_contiguous() and t.shape == shape:
+        return
+    if index < 0 or t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor" + (f" on cuda:{index}" if index >= 0 else ""))
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != len(shape) or any(n >= 0 and n != m for n, m in zip(shape, t.shape)):
@@ -39,17 +47,20 @@ def _tensor(name, t, dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _rows(name, t, like=None):
+def _rows(name, t, dtype, index):
     """The token stride, in elements, of [..., tokens, H, d] whose [H, d] are dense and whose
     leading dimensions, if any, are token runs one after another."""
-    if not t.is_cuda or (like is not None and t.device != like.device):
-        raise ValueError(f"{name} must be a CUDA tensor" + ("" if like is None else f" on {like.device}"))
-    if like is not None and t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    shape, strides = t.shape, t.stride()
-    h, d = shape[-2], shape[-1]
-    if t.numel() == 0:
+    if index < 0 or t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor" + (f" on cuda:{index}" if index >= 0 else ""))
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) < 3:
+        raise ValueError(f"{name} must be [..., tokens, H, d], got {tuple(shape)}")
+    h, d = shape[-2:]
+    if t.is_contiguous():
         return h * d
+    strides = t.stride()
     if (d > 1 and strides[-1] != 1) or (h > 1 and strides[-2] != d):
         raise ValueError(f"{name}: the heads of a token must be dense")
     stride, span = 0, 0                  # tokens of the inner dimensions, once there are two or more
@@ -100,36 +111,39 @@ def rotary(q, k, positions, freq, layout: str = "half", amplitude: float = 1.0, 
     positions: int32, one a token; freq: fp64 [rot / 2] (rotary_frequencies); layout "half" or
     "interleaved".  Returns (q_out, k_out), allocated dense unless given; they may be q and k.
     """
-    device, d = q.device, q.shape[-1]
-    h_q, n = q.shape[-2], math.prod(q.shape[:-2])
-    qs = _rows("q", q)
+    shape, dtype, index = q.shape, q.dtype, q.get_device()
+    qs = _rows("q", q, dtype, index)
+    h_q, d = shape[-2:]
+    n = q.numel() // (h_q * d) if h_q * d else 0
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
-    qos = _rows("q_out", q_out, q)
-    if q_out.shape != q.shape:
-        raise ValueError("q_out must have q's shape")
+        q_out, qos = torch.empty(shape, dtype=dtype, device=q.device), h_q * d
+    else:
+        qos = _rows("q_out", q_out, dtype, index)
+        if q_out.shape != shape:
+            raise ValueError("q_out must have q's shape")
     ks, kos, h_k, k_ptr, ko_ptr = 0, 0, 0, 0, 0
     if k is not None:
-        if k.shape[:-2] != q.shape[:-2] or k.shape[-1] != d:
-            raise ValueError(f"k must be [..., H_k, d] of q's tokens, got {tuple(k.shape)} beside {tuple(q.shape)}")
+        ks, h_k = _rows("k", k, dtype, index), k.shape[-2]
+        if k.shape[:-2] != shape[:-2] or k.shape[-1] != d:
+            raise ValueError(f"k must be [..., H_k, d] of q's tokens, got {tuple(k.shape)} beside {tuple(shape)}")
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=device)
-        if k_out.shape != k.shape:
-            raise ValueError("k_out must have k's shape")
-        h_k, ks, kos = k.shape[-2], _rows("k", k, q), _rows("k_out", k_out, q)
+            k_out, kos = torch.empty(k.shape, dtype=dtype, device=q.device), h_k * d
+        else:
+            kos = _rows("k_out", k_out, dtype, index)
+            if k_out.shape != k.shape:
+                raise ValueError("k_out must have k's shape")
         k_ptr, ko_ptr = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
     if positions.numel() != n:
         raise ValueError(f"{n} tokens but {positions.numel()} positions")
-    _tensor("positions", positions, torch.int32, positions.shape, device)
-    _tensor("freq", freq, torch.float64, (-1,), device)
-    if layout not in LAYOUTS:
+    _tensor("positions", positions, I32, positions.shape, index)
+    _tensor("freq", freq, F64, (-1,) if freq.dim() != 1 else freq.shape, index)
+    code = LAYOUTS.get(layout)
+    if code is None:
         raise ValueError(f"layout must be half or interleaved, got {layout!r}")
-    with _on(device):
-        _check(lib().kda_rotary(q.data_ptr(), qs, q_out.data_ptr(), qos, h_q, k_ptr, ks, ko_ptr, kos, h_k,
-                                positions.data_ptr(), freq.data_ptr(), amplitude, n, d, 2 * freq.numel(),
-                                LAYOUTS[layout], _dtype_code(q.dtype), _stream(device)))
+    _call(index, lib().kda_rotary, q.data_ptr(), qs, q_out.data_ptr(), qos, h_q, k_ptr, ks, ko_ptr, kos, h_k,
+          positions.data_ptr(), freq.data_ptr(), amplitude, n, d, 2 * freq.numel(), code, _dtype_code(dtype))
     return q_out, k_out
 
 
@@ -150,14 +164,34 @@ def cache_new(n_pages: int, H_kv: int, page: int, d: int, device="cuda") -> Page
     return PagedCache(*codes, *scales)
 
 
-def _pool(cache: PagedCache, device):
+def _pool(cache: PagedCache, index):
     """Checks the pool; returns n_pages, H_kv, page, d."""
-    shape = cache.k.shape
-    _tensor("cache.k", cache.k, torch.float8_e4m3fn, (-1, -1, -1, -1), device)
-    _tensor("cache.v", cache.v, torch.float8_e4m3fn, shape, device)
-    _tensor("cache.k_scale", cache.k_scale, torch.float32, shape[:2], device)
-    _tensor("cache.v_scale", cache.v_scale, torch.float32, shape[:2], device)
+    k, v, k_scale, v_scale = cache
+    shape = k.shape
+    blocks = shape[:2]
+    if not (k.dtype is E4M3 and v.dtype is E4M3 and k_scale.dtype is F32 and v_scale.dtype is F32
+            and k.get_device() == v.get_device() == k_scale.get_device() == v_scale.get_device() == index >= 0
+            and len(shape) == 4 and v.shape == shape and k_scale.shape == blocks and v_scale.shape == blocks
+            and k.is_contiguous() and v.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous()):
+        _tensor("cache.k", k, E4M3, (-1, -1, -1, -1), index)
+        _tensor("cache.v", v, E4M3, shape, index)
+        _tensor("cache.k_scale", k_scale, F32, blocks, index)
+        _tensor("cache.v_scale", v_scale, F32, blocks, index)
     return shape
+
+
+def _sequences(batch, cu_seqlens, block_table, start, index) -> int:
+    n = batch
+    if cu_seqlens is not None:
+        if batch != 1:
+            raise ValueError(f"cu_seqlens requires B == 1 (got {batch})")
+        n = cu_seqlens.numel() - 1
+        if n < 0:
+            raise ValueError("cu_seqlens must not be empty")
+        _tensor("cu_seqlens", cu_seqlens, I32, (n + 1,), index)
+    _tensor("block_table", block_table, I32, (n, block_table.shape[-1]), index)
+    _tensor("start", start, I32, (n,), index)
+    return n
 
 
 def cache_write(cache: PagedCache, k, v, block_table, start, cu_seqlens=None) -> PagedCache:
@@ -167,33 +201,17 @@ def cache_write(cache: PagedCache, k, v, block_table, start, cu_seqlens=None) ->
     bf16, tokens evenly spaced, heads dense); block_table: int32 [N, table_pages];
     start: int32 [N], the position of each sequence's first new token.
     """
-    device = k.device
-    ks, vs = _rows("k", k), _rows("v", v, k)
-    n_pages, h, page, d = _pool(cache, device)
-    if k.dim() != 4 or v.shape != k.shape or k.shape[2:] != (h, d):
-        raise ValueError(f"k and v must be [B, T, {h}, {d}], got {tuple(k.shape)} and {tuple(v.shape)}")
-    n = _sequences(k.shape[0], cu_seqlens, block_table, start, device)
-    with _on(device):
-        _check(lib().kda_cache_write(
-            k.data_ptr(), ks, v.data_ptr(), vs, cache.k.data_ptr(), cache.v.data_ptr(),
-            cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), block_table.data_ptr(), block_table.shape[1],
-            start.data_ptr(), 0 if cu_seqlens is None else cu_seqlens.data_ptr(), n, k.shape[1], h, d, n_pages,
-            page, _dtype_code(k.dtype), _stream(device)))
+    shape, dtype, index = k.shape, k.dtype, k.get_device()
+    ks, vs = _rows("k", k, dtype, index), _rows("v", v, dtype, index)
+    n_pages, h, page, d = _pool(cache, index)
+    if len(shape) != 4 or v.shape != shape or shape[2] != h or shape[3] != d:
+        raise ValueError(f"k and v must be [B, T, {h}, {d}], got {tuple(shape)} and {tuple(v.shape)}")
+    n = _sequences(shape[0], cu_seqlens, block_table, start, index)
+    _call(index, lib().kda_cache_write, k.data_ptr(), ks, v.data_ptr(), vs, cache.k.data_ptr(), cache.v.data_ptr(),
+          cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+          start.data_ptr(), 0 if cu_seqlens is None else cu_seqlens.data_ptr(), n, shape[1], h, d, n_pages, page,
+          _dtype_code(dtype))
     return cache
-
-
-def _sequences(batch, cu_seqlens, block_table, start, device) -> int:
-    n = batch
-    if cu_seqlens is not None:
-        if batch != 1:
-            raise ValueError(f"cu_seqlens requires B == 1 (got {batch})")
-        _tensor("cu_seqlens", cu_seqlens, torch.int32, (-1,), device)
-        n = cu_seqlens.numel() - 1
-        if n < 0:
-            raise ValueError("cu_seqlens must not be empty")
-    _tensor("block_table", block_table, torch.int32, (n, -1), device)
-    _tensor("start", start, torch.int32, (n,), device)
-    return n
 
 
 def cache_read(cache: PagedCache, block_table, start, T: int, cu_seqlens=None, dtype=torch.bfloat16,
@@ -202,20 +220,27 @@ def cache_read(cache: PagedCache, block_table, start, T: int, cu_seqlens=None, d
     position start[n] on ([N, T, H_kv, d]), or with cu_seqlens those of its packed rows, T rows in
     all ([1, T, H_kv, d]).  Returns (k, v), allocated unless given."""
     device = cache.k.device
-    n_pages, h, page, d = _pool(cache, device)
-    n = _sequences(block_table.shape[0] if cu_seqlens is None else 1, cu_seqlens, block_table, start, device)
+    index = cache.k.get_device()
+    n_pages, h, page, d = _pool(cache, index)
+    n = _sequences(block_table.shape[0] if cu_seqlens is None else 1, cu_seqlens, block_table, start, index)
     shape = (n if cu_seqlens is None else 1, T, h, d)
     k = torch.empty(shape, dtype=dtype, device=device) if k_out is None else k_out
     v = torch.empty(shape, dtype=dtype, device=device) if v_out is None else v_out
-    _tensor("k_out", k, dtype, shape, device)
-    _tensor("v_out", v, dtype, shape, device)
-    with _on(device):
-        _check(lib().kda_cache_read(
-            cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(),
-            block_table.data_ptr(), block_table.shape[1], start.data_ptr(),
-            0 if cu_seqlens is None else cu_seqlens.data_ptr(), n, T, h, d, n_pages, page, k.data_ptr(), v.data_ptr(),
-            _dtype_code(dtype), _stream(device)))
+    if k_out is not None:
+        _tensor("k_out", k, dtype, shape, index)
+    if v_out is not None:
+        _tensor("v_out", v, dtype, shape, index)
+    _call(index, lib().kda_cache_read, cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
+          cache.v_scale.data_ptr(), block_table.data_ptr(), block_table.shape[1], start.data_ptr(),
+          0 if cu_seqlens is None else cu_seqlens.data_ptr(), n, T, h, d, n_pages, page, k.data_ptr(), v.data_ptr(),
+          _dtype_code(dtype))
     return k, v
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_need(index, *sizes) -> int:
+    """The library's answer for the current device, which is ``index``: a function of sizes alone."""
+    return int(lib().kda_cache_attention_workspace_size(*sizes))
 
 
 def cache_attention_workspace_size(B: int, T_q: int, H_q: int, H_kv: int, d: int, page: int,
@@ -234,35 +259,40 @@ def cache_attention(q, cache: PagedCache, block_table, lengths, scale: float | N
     ``sinks`` tokens besides.  Returns o [B, T_q, H_q, d], or with return_lse (o, lse) where
     lse is fp32 [B, T_q, H_q].  A workspace of the required size is allocated with torch if none is given.
     """
+    shape, dtype, index = q.shape, q.dtype, q.get_device()
+    qs = _rows("q", q, dtype, index)
+    n_pages, h, page, d = _pool(cache, index)
+    if len(shape) != 4 or shape[3] != d:
+        raise ValueError(f"q must be [B, T_q, H_q, {d}], got {tuple(shape)}")
+    B, t_q, h_q, _ = shape
+    wide = block_table.shape[-1]
+    _tensor("block_table", block_table, I32, (B, wide), index)
+    _tensor("lengths", lengths, I32, (B,), index)
     device = q.device
-    qs = _rows("q", q)
-    n_pages, h, page, d = _pool(cache, device)
-    if q.dim() != 4 or q.shape[3] != d:
-        raise ValueError(f"q must be [B, T_q, H_q, {d}], got {tuple(q.shape)}")
-    B, t_q, h_q, _ = q.shape
-    _tensor("block_table", block_table, torch.int32, (B, -1), device)
-    _tensor("lengths", lengths, torch.int32, (B,), device)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=device)
+        out = torch.empty(shape, dtype=dtype, device=device)
     else:
-        _tensor("out", out, q.dtype, q.shape, device)
+        _tensor("out", out, dtype, shape, index)
     if lse is not None:
-        _tensor("lse", lse, torch.float32, (B, t_q, h_q), device)
+        _tensor("lse", lse, F32, (B, t_q, h_q), index)
     elif return_lse:
-        lse = torch.empty((B, t_q, h_q), dtype=torch.float32, device=device)
-    wide = block_table.shape[1]
-    with _on(device):
-        if workspace is None:
-            need = cache_attention_workspace_size(B, t_q, h_q, h, d, page, wide)
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        lse = torch.empty((B, t_q, h_q), dtype=F32, device=device)
+    ws, ws_bytes = 0, 0
+    if workspace is None:
+        if index == torch.cuda.current_device():
+            need = _workspace_need(index, B, t_q, h_q, h, d, page, wide)
+        else:
+            with torch.cuda.device(index):
+                need = _workspace_need(index, B, t_q, h_q, h, d, page, wide)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            ws, ws_bytes = workspace.data_ptr(), need
+    else:
+        if workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
-        ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-        _check(lib().kda_cache_attention(
-            q.data_ptr(), qs, cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
-            cache.v_scale.data_ptr(), block_table.data_ptr(), wide, lengths.data_ptr(), out.data_ptr(),
-            0 if lse is None else lse.data_ptr(), B, t_q, h_q, h, d, n_pages, page,
-            1.0 / math.sqrt(d) if scale is None else scale, window, sinks, _dtype_code(q.dtype), ws, ws_bytes,
-            _stream(device)))
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _call(index, lib().kda_cache_attention, q.data_ptr(), qs, cache.k.data_ptr(), cache.v.data_ptr(),
+          cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), block_table.data_ptr(), wide, lengths.data_ptr(),
+          out.data_ptr(), 0 if lse is None else lse.data_ptr(), B, t_q, h_q, h, d, n_pages, page,
+          1.0 / math.sqrt(d) if scale is None else scale, window, sinks, _dtype_code(dtype), ws, ws_bytes)
     return (out, lse) if return_lse else out
