@@ -12,24 +12,31 @@
 // What bounds it: reading the codes, as long as the rows that share a head's
 // keys (T_q times H_q / H_kv) are few; the products' rate beyond some 32 rows.
 //
-// The tile.  16 rows x 16 tokens a step, on m16n8k16 products of fp16 with fp32
-// sums: e4m3 codes are exact in fp16, and so are a page's scale (applied to
-// the scores after the product, to the weights before it) and bf16 queries, once a
-// power of two has brought their row under fp16's largest value.  fp32 queries
-// and their weights go as two fp16 pieces (22 bits), two products instead of one.
-// No operand passes through shared memory to change hands: the pairing of a
-// product's k index with channels, of its n index with channels of v, is free, so
+// The tile.  16 tokens a step against NT tiles of 8 rows, on m16n8k16 products of
+// fp16 with fp32 sums, tokens and then channels of v on the side of 16: a decode
+// step has few rows a head, and 8 waste less than 16.  e4m3 codes are exact in
+// fp16, and so are a page's scale (applied to the scores after the product,
+// to the weights before it) and bf16 queries, once a power of two has brought
+// their row under fp16's largest value.  fp32 queries and their weights go as
+// two fp16 pieces (22 bits), two products instead of one.
+// No code passes through shared memory to change hands: the pairing of a
+// product's k index with channels, of its m index with channels of v, is free, so
 // each lane reads its own 16 consecutive bytes of a token's row, as they lie
-// in the cache, and its words are the fragments; the scores' fragments are the
-// weights' fragments.  Every lane copies what it will read itself (16-byte
-// asynchronous copies into its own slots, three steps ahead), so a warp runs
-// without a barrier; with more than 16 rows, MT warps share one ring of slots and
-// one barrier a step.
+// in the cache, and its words are the fragments; the scores become the weights'
+// fragments by a transposition of 8 x 8 within the warp.  Every lane copies what
+// it will read itself (16-byte asynchronous copies into its own slots, some steps
+// ahead), so a warp runs without a barrier; with more rows than one warp takes,
+// MT warps share one ring of slots and one barrier a step.
+//
+// The maximum is not brought up to date at every step: as long as no score is
+// above the last one by more than a factor of 4, sums keep their reference, and a
+// vote of the warp is all that a step spends on it.
 //
 // The work.  The lengths are on the device, so the host cannot cut the work up.
 // All steps of all (sequence, row tile, head) items are one list, cut into equal
 // shares, one for each of a fixed number of CTAs; each finds its place by
-// summing the lengths.  An item that lies within one share is finished there; pieces of
+// summing the lengths.  An item counts some steps more than it has, for what its
+// start and end cost.  An item that lies within one share is finished there; pieces of
 // the others are left in the workspace (fp32 sums with their maxima), at most
 // two a CTA, and a second small kernel joins them in a fixed order, so that
 // the same call gives the same bits.  Where one CTA takes any item whole
@@ -38,7 +45,7 @@
 // V's scale.  The weights are e^(s - m) times the page's scale of v, whose range
 // is far beyond fp16's.  So the sums of v have a reference of their own, mo = max(s
 // + log2 scale), beside the maximum m that the sum of weights has; weights go
-// to fp16 as 2^(s + log2 scale - mo + 12), at most 2^13, with full precision down to
+// to fp16 as 2^(s + log2 scale - mo + 12), at most 2^15, with full precision down to
 // 2^-26 of the largest.
 //
 // NaN that a row does not see.  0 times NaN is NaN, so tokens past the last that
@@ -59,15 +66,18 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 16;             // tokens of a step
 constexpr int kMinShare = 8;          // steps below which no item is cut further
+constexpr int kItemCost = 6;          // what an item's start and end cost, in steps
 constexpr int kJoinThreads = 256;
 constexpr int kMaxScan = 8192;        // (sequence, row tile) pairs that every CTA sums up
 constexpr float kWeightBits = 12.0f;
+constexpr float kSlack = 2.0f;        // log2 of how far scores may pass the reference
+constexpr float kLowest = -3.402823466e38f;   // the reference before any score
 
 struct Plan {
     int group;          // query heads of a head of keys
     int rows;           // T_q * group
     int row_tiles;
-    int stored;         // rows of a tile that exist: min(rows, 16 MT)
+    int stored;         // rows of a tile that exist
     float* sums;        // [grid][2][stored][D]
     float4* stats;      // [grid][2][stored]: m, mo, l
     int4* joins;        // [grid]: pair (sequence, row tile), head, last CTA, slot; pair < 0: none
@@ -122,11 +132,17 @@ __device__ __forceinline__ float quad_max(float x) {
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
     return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
 }
-__device__ __forceinline__ float quad_sum(float x) {
-    x += __shfl_xor_sync(0xffffffffu, x, 1);
-    return x + __shfl_xor_sync(0xffffffffu, x, 2);
+// Over the eight lanes of one c.
+__device__ __forceinline__ float column_max(float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
 }
-__device__ __forceinline__ float or_zero(float m) { return m == -INFINITY ? 0.0f : m; }
+__device__ __forceinline__ float column_sum(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 4);
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
 
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -146,14 +162,21 @@ __device__ __forceinline__ void word_to_half2x2(uint32_t w, uint32_t& lo, uint32
         : "r"(w));
 }
 
-// c += a b: a is 16 x 16 (rows g and g + 8; k 2c, 2c + 1, then 8 more), b 16 x 8
-// (n = g), c 16 x 8 (rows g and g + 8, n 2c and 2c + 1), of lane 4 g + c.
+// c += a b: a is 16 x 16 (m = g and g + 8; k = 2c, 2c + 1, then 8 more), b 16 x 8
+// (n = g), c 16 x 8 (m = g and g + 8, n = 2c and 2c + 1), of lane 4 g + c.
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// An 8 x 8 matrix of 16-bit values, a row a quad, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 template <int BYTES>
@@ -176,33 +199,96 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
     return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
 
-// The sizes that go together: MT warps share the tokens of their 16 MT rows,
-// NG groups of them take steps in turn, each with a ring of STAGES steps.
-template <typename T, int D, int MT>
+// The sizes that go together: a warp takes NT tiles of 8 rows; MT warps share
+// the tokens of their 8 NT MT rows; NG groups of them take steps in turn, each with a
+// ring of STAGES steps.  The more rows a warp has, the fewer warps' registers an SM holds.
+template <typename T, int D, int NT_, int MT_>
 struct Shape {
+    static constexpr int NT = NT_, MT = MT_;
+    static constexpr int PIECES = sizeof(T) == 4 ? 2 : 1;   // fp16 pieces of a query and a weight
     static constexpr int NG = kWarps / MT;
-    static constexpr int ROWS = 16 * MT;
-    static constexpr int STAGES = MT == 1 ? 4 : MT == 2 ? 6 : 8;
+    static constexpr int ROWS = 8 * NT * MT;
+    static constexpr int CTAS = PIECES == 1 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2) : (NT == 1 ? 3 : 2);   // resident a SM
+    static constexpr int STAGES = MT == 1 ? (CTAS == 4 ? 3 : 4) : MT == 2 ? 6 : 8;
+    static constexpr bool Q_HELD = NT <= 2;           // queries in registers, or read again at every step
     static constexpr int KC = D / 64;                 // 16-byte pieces of a key that a lane reads
     static constexpr int VB = D / 8;                  // bytes of a value that a lane reads
+    static constexpr int TILES = VB / 2;              // of 16 channels of v
     static constexpr int K_BYTES = 2 * KC * 512;      // of a step: 16 keys
     static constexpr int STAGE = K_BYTES + 4 * 32 * VB + 16;   // + the two scales
     static constexpr int RING = NG * STAGES * STAGE;
     static constexpr int JOIN = NG * ROWS * (D + 4) * 4 + NG * ROWS * 16;
-    static constexpr int SMEM = RING > JOIN ? RING : JOIN;
-    static constexpr int PIECES = sizeof(T) == 4 ? 2 : 1;   // fp16 pieces of a query and a weight
-    static constexpr int CTAS = PIECES == 1 ? 3 : 2;        // resident a SM
+    static constexpr int Q_AT = RING > JOIN ? RING : JOIN;
+    static constexpr int Q_BYTES = ROWS * D * 2;      // of one piece
+    static constexpr int FACTOR_AT = Q_AT + PIECES * Q_BYTES;
+    static constexpr int SMEM = FACTOR_AT + ROWS * 4;
 };
 
 // One piece of an item: steps [from, to) of a tile's `steps`.
-template <typename T, int D, int MT>
+template <typename T, int D, int NT, int MT>
 struct Piece {
-    using S = Shape<T, D, MT>;
+    using S = Shape<T, D, NT, MT>;
     const CacheAttention& a;
     const Plan& plan;
     uint8_t* smem;
     int b, hk, rt, from, to;
     Tile tile;
+
+    // The tile's queries, as the fragments that the score products read: for 8 rows
+    // and 64 channels, two 16-byte words of each lane (row g, channels 16 c ..).
+    __device__ __forceinline__ void load_queries() {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int g = lane >> 2, c = lane & 3;
+        uint4* to_s = reinterpret_cast<uint4*>(smem + S::Q_AT);
+        float* factor_s = reinterpret_cast<float*>(smem + S::FACTOR_AT);
+        for (int rows8 = warp; rows8 < S::ROWS / 8; rows8 += kWarps) {
+            const int row = rt * S::ROWS + 8 * rows8 + g;
+            const bool real = row < plan.rows;
+            const int i = real ? row / plan.group : 0;
+            const T* q = static_cast<const T*>(a.q) + ((int64_t)b * a.T_q + i) * a.q_stride +
+                         (int64_t)(hk * plan.group + (real ? row - i * plan.group : 0)) * a.d;
+            uint4 raw[S::KC][sizeof(T)];
+            float amax = 0.0f;
+#pragma unroll
+            for (int j = 0; j < S::KC; ++j) {
+                const bool in = real && 64 * j + 16 * c < a.d;
+#pragma unroll
+                for (int w = 0; w < (int)sizeof(T); ++w)
+                    raw[j][w] = in ? __ldg(reinterpret_cast<const uint4*>(q + 64 * j + 16 * c) + w)
+                                   : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < S::KC; ++j)
+#pragma unroll
+                for (int w = 0; w < 16; ++w)
+                    amax = fmaxf(amax, finite_abs(to_f32(reinterpret_cast<const T*>(raw[j])[w])));
+            amax = quad_max(amax);
+            // 2^ex <= amax < 2^(ex + 1): times 2^(14 - ex), under fp16's largest value
+            int ex = (int)(__float_as_uint(amax) >> 23) - 127;
+            ex = ex < -112 ? -112 : ex;
+            const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+            if (c == 0)
+                factor_s[8 * rows8 + g] =
+                    a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + ex - 14) << 23);
+#pragma unroll
+            for (int j = 0; j < S::KC; ++j)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t bits[4], rest[4];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const T* e = reinterpret_cast<const T*>(raw[j]) + 8 * half + 2 * w;
+                        const float lo = to_f32(e[0]) * up, hi = to_f32(e[1]) * up;
+                        bits[w] = half2_bits(lo, hi);
+                        rest[w] = half2_rest(lo, hi, bits[w]);
+                    }
+                    const int at = ((rows8 * S::KC + j) * 2 + half) * 32 + lane;
+                    to_s[at] = make_uint4(bits[0], bits[1], bits[2], bits[3]);
+                    if constexpr (S::PIECES == 2)
+                        to_s[S::Q_BYTES / 16 + at] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+                }
+        }
+    }
 
     __device__ __forceinline__ void run(int cta, int slot, bool whole) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -213,6 +299,7 @@ struct Piece {
         const int d = a.d;
         const int32_t* table = a.table + (int64_t)b * a.table_pages;
         const int page_mask = (1 << a.page_shift) - 1;
+        const int k_lane = g * d + 16 * c, v_lane = 2 * c * d + S::VB * g;   // of this lane's bytes in a step
 
         auto page_at = [&](int s) -> int {
             const int t = tile.token(s);
@@ -227,25 +314,35 @@ struct Piece {
                 const int t0 = tile.token(s);
                 const int64_t block = (int64_t)pg * a.H_kv + hk;
                 const int64_t at = ((block << a.page_shift) + (t0 & page_mask)) * d;
-                const uint8_t* k = a.k_codes + at;
-                const uint8_t* v = a.v_codes + at;
+                const uint8_t* k = a.k_codes + at + k_lane;
+                const uint8_t* v = a.v_codes + at + v_lane;
                 const int n = tile.end - t0;               // tokens of the step that exist
+                const uint32_t k_to = stage + lane * 16, v_to = stage + S::K_BYTES + lane * S::VB;
+                if (d == D && n >= kStep) {
 #pragma unroll
-                for (int i = 0; i < 2 * S::KC; ++i)
-                    if (MT == 1 || i % MT == wt) {
-                        const int token = 8 * (i / S::KC) + g, byte = 64 * (i % S::KC) + 16 * c;
-                        const bool real = token < n && byte < d;
-                        copy_async<16>(stage + i * 512 + lane * 16, real ? k + token * d + byte : a.k_codes,
-                                       real);
-                    }
+                    for (int i = 0; i < 2 * S::KC; ++i)
+                        if (MT == 1 || i % MT == wt)
+                            copy_async<16>(k_to + i * 512, k + 8 * (i / S::KC) * D + 64 * (i % S::KC), true);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (MT == 1 || i % MT == wt) {
-                        const int token = 8 * (i / 2) + 2 * c + (i & 1), byte = S::VB * g;
-                        const bool real = token < n && byte < d;
-                        copy_async<S::VB>(stage + S::K_BYTES + i * 32 * S::VB + lane * S::VB,
-                                          real ? v + token * d + byte : a.v_codes, real);
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        if (MT == 1 || i % MT == wt)
+                            copy_async<S::VB>(v_to + i * 32 * S::VB, v + (8 * (i / 2) + (i & 1)) * D, true);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2 * S::KC; ++i)
+                        if (MT == 1 || i % MT == wt) {
+                            const int up = 8 * (i / S::KC), byte = 64 * (i % S::KC);
+                            const bool real = up + g < n && byte + 16 * c < d;
+                            copy_async<16>(k_to + i * 512, real ? k + up * d + byte : a.k_codes, real);
+                        }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (MT == 1 || i % MT == wt) {
+                            const int up = 8 * (i / 2) + (i & 1);
+                            const bool real = up + 2 * c < n && S::VB * g < d;
+                            copy_async<S::VB>(v_to + i * 32 * S::VB, real ? v + up * d : a.v_codes, real);
+                        }
+                }
                 if (wt == 0 && lane < 2)
                     copy_async<4>(scales + 4 * lane, (lane ? a.v_scale : a.k_scale) + block, true);
             } else if (wt == 0 && lane < 2) {
@@ -264,61 +361,36 @@ struct Piece {
         }
         int next_page = page_at(s0 + (S::STAGES - 1) * S::NG);
 
-        // Queries: rows ra and rb of this lane, 16 channels from 64 j + 16 c on.
-        const int r_local[2] = {wt * 16 + g, wt * 16 + g + 8};
-        uint32_t qf[S::PIECES][4 * S::KC][4];
-        float factor[2];
-        int pos[2];
+        load_queries();
+        __syncthreads();
+        const uint4* q_s = reinterpret_cast<const uint4*>(smem + S::Q_AT) + wt * NT * S::KC * 64 + lane;
+        const float* factor_s = reinterpret_cast<const float*>(smem + S::FACTOR_AT) + wt * NT * 8 + 2 * c;
+        uint4 qh[S::Q_HELD ? S::PIECES : 1][S::Q_HELD ? NT : 1][S::KC][2];
+        float factor[NT][2], m[NT][2], mo[NT][2], l[NT][2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = rt * S::ROWS + r_local[r];
-            const bool real = row < plan.rows;
-            const int i = real ? row / plan.group : 0;
-            pos[r] = real ? tile.p0 - rt * S::ROWS / plan.group + i : -1;
-            const T* q = static_cast<const T*>(a.q) + ((int64_t)b * a.T_q + i) * a.q_stride +
-                         (int64_t)(hk * plan.group + (real ? row - i * plan.group : 0)) * d;
-            float x[S::KC][16];
-            float amax = 0.0f;
+        for (int n = 0; n < NT; ++n) {
+            if constexpr (S::Q_HELD)
 #pragma unroll
-            for (int j = 0; j < S::KC; ++j) {
-                uint4 raw[sizeof(T)];
-                const bool in = real && 64 * j + 16 * c < d;
+                for (int pc = 0; pc < S::PIECES; ++pc)
 #pragma unroll
-                for (int w = 0; w < (int)sizeof(T); ++w)
-                    raw[w] = in ? __ldg(reinterpret_cast<const uint4*>(q + 64 * j + 16 * c) + w)
-                                : make_uint4(0, 0, 0, 0);
-                const T* e = reinterpret_cast<const T*>(raw);
+                    for (int j = 0; j < S::KC; ++j)
 #pragma unroll
-                for (int w = 0; w < 16; ++w) {
-                    x[j][w] = to_f32(e[w]);
-                    amax = fmaxf(amax, finite_abs(x[j][w]));
-                }
+                        for (int h = 0; h < 2; ++h)
+                            qh[pc][n][j][h] = q_s[pc * (S::Q_BYTES / 16) + ((n * S::KC + j) * 2 + h) * 32];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                factor[n][r] = factor_s[8 * n + r];
+                m[n][r] = mo[n][r] = kLowest;
+                l[n][r] = 0.0f;
             }
-            amax = quad_max(amax);
-            // 2^ex <= amax < 2^(ex + 1): times 2^(14 - ex), under fp16's largest value
-            int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-            ex = ex < -112 ? -112 : ex;
-            const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
-            factor[r] = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + ex - 14) << 23);
-#pragma unroll
-            for (int j = 0; j < S::KC; ++j)
-#pragma unroll
-                for (int w = 0; w < 4; ++w)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float lo = x[j][4 * w + 2 * h] * up, hi = x[j][4 * w + 2 * h + 1] * up;
-                        const uint32_t bits = half2_bits(lo, hi);
-                        qf[0][4 * j + w][2 * h + r] = bits;
-                        if constexpr (S::PIECES == 2) qf[1][4 * j + w][2 * h + r] = half2_rest(lo, hi, bits);
-                    }
         }
-
-        float acc[S::VB][4];
+        float acc[S::TILES][NT][4];
 #pragma unroll
-        for (int n = 0; n < S::VB; ++n)
+        for (int x = 0; x < S::TILES; ++x)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) acc[n][w] = 0.0f;
-        float m[2] = {-INFINITY, -INFINITY}, mo[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) acc[x][n][w] = 0.0f;
 
         int st = 0;
         for (int s = s0; s < to; s += S::NG) {
@@ -336,166 +408,193 @@ struct Piece {
             st = st == S::STAGES - 1 ? 0 : st + 1;
             if (scales.y == 0.0f) continue;                // a page that is not held
 
-            float sc[2][4];
+            // Scores of tokens g and g + 8 with rows 2 c and 2 c + 1 of each tile.
+            float sc[NT][4];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int w = 0; w < 4; ++w) sc[t][w] = 0.0f;
+                for (int w = 0; w < 4; ++w) sc[n][w] = 0.0f;
 #pragma unroll
-                for (int j = 0; j < S::KC; ++j) {
-                    const uint4 raw = *reinterpret_cast<const uint4*>(stage + (t * S::KC + j) * 512 + lane * 16);
-                    const uint32_t word[4] = {raw.x, raw.y, raw.z, raw.w};
+            for (int j = 0; j < S::KC; ++j) {
+                const uint4 k0 = *reinterpret_cast<const uint4*>(stage + j * 512 + lane * 16);
+                const uint4 k1 = *reinterpret_cast<const uint4*>(stage + (S::KC + j) * 512 + lane * 16);
+                const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        uint32_t b0, b1;
-                        word_to_half2x2(word[w], b0, b1);
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t f[2][4];
 #pragma unroll
-                        for (int pc = 0; pc < S::PIECES; ++pc) mma16816(sc[t], qf[pc][4 * j + w], b0, b1);
+                    for (int w = 0; w < 2; ++w) {
+                        word_to_half2x2(w0[2 * h + w], f[w][0], f[w][2]);
+                        word_to_half2x2(w1[2 * h + w], f[w][1], f[w][3]);
                     }
-                }
-            }
-            const float f0 = factor[0] * scales.x, f1 = factor[1] * scales.x;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                sc[t][0] *= f0;
-                sc[t][1] *= f0;
-                sc[t][2] *= f1;
-                sc[t][3] *= f1;
+                    for (int pc = 0; pc < S::PIECES; ++pc)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const uint4 q = S::Q_HELD ? qh[S::Q_HELD ? pc : 0][S::Q_HELD ? n : 0][j][h]
+                                                      : q_s[pc * (S::Q_BYTES / 16) + ((n * S::KC + j) * 2 + h) * 32];
+                            mma16816(sc[n], f[0], q.x, q.y);
+                            mma16816(sc[n], f[1], q.z, q.w);
+                        }
+                }
             }
             const int t0 = tile.token(s);
             const bool partly = t0 + kStep - 1 > tile.p0 ||
                                 (a.window > 0 && t0 <= tile.p1 - a.window && t0 + kStep - 1 >= a.sinks);
-            uint32_t sight = 0xffu;                        // bit 4 t + w: sc[t][w] is seen
+            uint32_t sight = 0xffffffffu;                  // bit 4 n + w: sc[n][w] is seen
             if (partly) {
                 sight = 0;
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const int at = t0 + 8 * t + 2 * c + (w & 1), p = pos[w >> 1];
-                        const bool sees = at <= p && (a.window == 0 || at > p - a.window || at < a.sinks);
-                        if (sees) sight |= 1u << (4 * t + w);
-                        else sc[t][w] = -INFINITY;
+                    for (int r = 0; r < 2; ++r) {
+                        const int row = rt * S::ROWS + (wt * NT + n) * 8 + 2 * c + r;
+                        const int p = tile.p0 - rt * S::ROWS / plan.group + row / plan.group;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int at = t0 + 8 * h + g;
+                            if (at <= p && (a.window == 0 || at > p - a.window || at < a.sinks))
+                                sight |= 1u << (4 * n + 2 * h + r);
+                        }
                     }
             }
             // log2 of v's scale: its exponent, and what remains (1 for these pages' powers of two)
             const float e = (float)((int)(__float_as_uint(scales.y) >> 23) - 127);
             const float mantissa = __uint_as_float((__float_as_uint(scales.y) & 0x7fffffu) | 0x3f800000u);
-            uint32_t pf[S::PIECES][4];
-            float keep[2];
-            bool moved = false;
+            // x = score - m, in powers of two
+            float x[NT][4];
+            bool above = false;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float top = quad_max(fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]),
-                                                 fmaxf(sc[1][2 * r], sc[1][2 * r + 1])));
-                const float m_new = fmaxf(m[r], top), mo_new = fmaxf(mo[r], top + e);
-                const float ref = or_zero(m_new), oref = or_zero(mo_new);
-                keep[r] = ex2(mo[r] - oref);
-                moved |= mo_new > mo[r];
-                const float lift = ex2(fminf(ref + e - oref + kWeightBits, 126.0f)) * mantissa;
-                float p[4];
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int w = 0; w < 4; ++w) p[w] = ex2(sc[w >> 1][2 * r + (w & 1)] - ref);
-                l[r] = l[r] * ex2(m[r] - ref) + ((p[0] + p[1]) + (p[2] + p[3]));
-                m[r] = m_new;
-                mo[r] = mo_new;
+                for (int r = 0; r < 2; ++r) {
+                    const float f = factor[n][r] * scales.x;
+                    const float most = fminf(kSlack, kSlack - (m[n][r] + e - mo[n][r]));
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const float lo = p[2 * t] * lift, hi = p[2 * t + 1] * lift;
+                    for (int h = 0; h < 2; ++h) {
+                        const int w = 2 * h + r;
+                        x[n][w] = fmaf(sc[n][w], f, -m[n][r]);
+                        if (partly && !(sight >> (4 * n + w) & 1)) x[n][w] = -INFINITY;
+                        above |= x[n][w] > most;
+                    }
+                }
+            if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float keep[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float f = factor[n][r] * scales.x;
+                        const bool seen[2] = {(sight >> (4 * n + r) & 1) != 0, (sight >> (4 * n + 2 + r) & 1) != 0};
+                        const float top = column_max(fmaxf(seen[0] ? sc[n][r] * f : -INFINITY,
+                                                           seen[1] ? sc[n][2 + r] * f : -INFINITY));
+                        const float m_new = fmaxf(m[n][r], top), mo_new = fmaxf(mo[n][r], top + e);
+                        keep[r] = ex2(mo[n][r] - mo_new);
+                        l[n][r] *= ex2(m[n][r] - m_new);
+                        m[n][r] = m_new;
+                        mo[n][r] = mo_new;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            x[n][2 * h + r] = seen[h] ? fmaf(sc[n][2 * h + r], f, -m_new) : -INFINITY;
+                    }
+#pragma unroll
+                    for (int y = 0; y < S::TILES; ++y)
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) acc[y][n][w] *= keep[w & 1];
+                }
+            }
+            uint32_t pf[S::PIECES][NT][2];                 // weights: tokens 2 c .. of row g, then 8 more
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float lift[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    lift[r] = ex2(fminf(m[n][r] + e - mo[n][r] + kWeightBits, 126.0f)) * mantissa;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float p0 = ex2(x[n][2 * h]), p1 = ex2(x[n][2 * h + 1]);
+                    l[n][0] += p0;
+                    l[n][1] += p1;
+                    const float lo = p0 * lift[0], hi = p1 * lift[1];
                     const uint32_t bits = half2_bits(lo, hi);
-                    pf[0][2 * t + r] = bits;
-                    if constexpr (S::PIECES == 2) pf[1][2 * t + r] = half2_rest(lo, hi, bits);
+                    pf[0][n][h] = transposed(bits);
+                    if constexpr (S::PIECES == 2) pf[1][n][h] = transposed(half2_rest(lo, hi, bits));
                 }
             }
-            if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-                for (int n = 0; n < S::VB; ++n) {
-                    acc[n][0] *= keep[0];
-                    acc[n][1] *= keep[0];
-                    acc[n][2] *= keep[1];
-                    acc[n][3] *= keep[1];
-                }
-            }
-            // Values: four tokens' words; a product's b pairs two tokens of one channel.
+            // Values: four tokens' words; a product's a pairs two tokens of one channel.
             const uint8_t* vs = stage + S::K_BYTES + lane * S::VB;
-            bool nan_here = false;
+            uint32_t v[4][S::VB / 4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int w = 0; w < S::VB / 4; w += 2) {
+                    const uint2 two = *reinterpret_cast<const uint2*>(vs + i * 32 * S::VB + 4 * w);
+                    v[i][w] = two.x;
+                    v[i][w + 1] = two.y;
+                }
             if (partly) {
+                uint32_t any = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int w = 0; w < S::VB / 4; ++w)
-                        nan_here |= nan_bytes(*reinterpret_cast<const uint32_t*>(vs + i * 32 * S::VB + 4 * w)) != 0;
-                nan_here = __any_sync(0xffffffffu, nan_here);
-            }
-            if (!nan_here) {
+                    for (int w = 0; w < S::VB / 4; ++w) any |= nan_bytes(v[i][w]);
+                if (__any_sync(0xffffffffu, any != 0)) {
+                    uint32_t ones[1][NT][2];               // the rows' sight as weights of 1
 #pragma unroll
-                for (int w = 0; w < S::VB / 4; w += 2) {
-                    uint2 two[4];
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        two[i] = *reinterpret_cast<const uint2*>(vs + i * 32 * S::VB + 4 * w);
+                        for (int h = 0; h < 2; ++h)
+                            ones[0][n][h] = transposed((sight >> (4 * n + 2 * h) & 1 ? 0x3c00u : 0u) |
+                                                       (sight >> (4 * n + 2 * h + 1) & 1 ? 0x3c000000u : 0u));
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const uint32_t v0 = x ? two[0].y : two[0].x, v1 = x ? two[1].y : two[1].x;
-                        const uint32_t v2 = x ? two[2].y : two[2].x, v3 = x ? two[3].y : two[3].x;
-                        add_values(acc, 4 * (w + x), pf, v0, v1, v2, v3);
+                    for (int w = 0; w < S::VB / 4; ++w) {
+                        uint32_t bad[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            bad[i] = nan_bytes(v[i][w]);
+                            v[i][w] &= ~bad[i];
+                            bad[i] &= 0x38383838u;         // 1 in e4m3
+                        }
+                        float hit[2][NT][4] = {};
+                        add_values<2, 1>(hit, 0, ones, bad[0], bad[1], bad[2], bad[3]);
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int z = 0; z < 4; ++z)
+                                    if (hit[y][n][z] > 0.0f) acc[2 * w + y][n][z] = NAN;
                     }
                 }
-            } else {
-                uint32_t seen[4];                          // the rows' sight as a fragment of ones
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        seen[2 * t + r] = (sight >> (4 * t + 2 * r) & 1 ? 0x3c00u : 0u) |
-                                          (sight >> (4 * t + 2 * r + 1) & 1 ? 0x3c000000u : 0u);
-#pragma unroll
-                for (int w = 0; w < S::VB / 4; ++w) {
-                    uint32_t v[4], bad[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        v[i] = *reinterpret_cast<const uint32_t*>(vs + i * 32 * S::VB + 4 * w);
-                        bad[i] = nan_bytes(v[i]);
-                        v[i] &= ~bad[i];
-                        bad[i] &= 0x38383838u;             // 1 in e4m3
-                    }
-                    add_values(acc, 4 * w, pf, v[0], v[1], v[2], v[3]);
-                    float hit[4][4] = {};
-                    uint32_t ones[1][4] = {{seen[0], seen[1], seen[2], seen[3]}};
-                    add_values<4, 1>(hit, 0, ones, bad[0], bad[1], bad[2], bad[3]);
-#pragma unroll
-                    for (int n = 0; n < 4; ++n)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            if (hit[n][x] > 0.0f) acc[4 * w + n][x] = NAN;
-                }
             }
+#pragma unroll
+            for (int w = 0; w < S::VB / 4; ++w) add_values(acc, 2 * w, pf, v[0][w], v[1][w], v[2][w], v[3][w]);
         }
         copy_wait<0>();
         __syncthreads();                                   // the ring becomes the place to join in
 
-        // Join the groups.  Lane (g, c) holds channels [2 c VB, 2 (c + 1) VB) of its rows.
+        // Join the groups.  Lane (g, c) holds channels VB g .. of rows 2 c and 2 c + 1.
         float* o_s = reinterpret_cast<float*>(smem);
         float4* stat_s = reinterpret_cast<float4*>(smem + S::NG * S::ROWS * (D + 4) * 4);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            l[r] = quad_sum(l[r]);
-            if (r_local[r] >= plan.stored) continue;
-            float* to_s = o_s + (grp * S::ROWS + r_local[r]) * (D + 4) + 2 * c * S::VB;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int r = 0; r < 2; ++r) {
+                const int row = (wt * NT + n) * 8 + 2 * c + r;
+                l[n][r] = column_sum(l[n][r]);
+                if (row >= plan.stored) continue;
+                float* to_s = o_s + (grp * S::ROWS + row) * (D + 4) + S::VB * g;
 #pragma unroll
-                for (int n = 0; n < S::VB; n += 4)
-                    *reinterpret_cast<float4*>(to_s + h * S::VB + n) =
-                        make_float4(acc[n][2 * r + h], acc[n + 1][2 * r + h], acc[n + 2][2 * r + h],
-                                    acc[n + 3][2 * r + h]);
-            if (c == 0) stat_s[grp * S::ROWS + r_local[r]] = make_float4(m[r], mo[r], l[r], 0.0f);
-        }
+                for (int y = 0; y < S::TILES; y += 2)
+                    *reinterpret_cast<float4*>(to_s + 2 * y) =
+                        make_float4(acc[y][n][r], acc[y][n][2 + r], acc[y + 1][n][r], acc[y + 1][n][2 + r]);
+                if (g == 0) stat_s[grp * S::ROWS + row] = make_float4(m[n][r], mo[n][r], l[n][r], 0.0f);
+            }
         __syncthreads();
         const int rows_here = plan.rows - rt * S::ROWS < S::ROWS ? plan.rows - rt * S::ROWS : S::ROWS;
         for (int u = threadIdx.x; u < rows_here * (D / 4); u += kThreads) {
             const int r = u / (D / 4), ch = u % (D / 4) * 4;
-            float M = -INFINITY, MO = -INFINITY, L = 0.0f;
+            float M = kLowest, MO = kLowest, L = 0.0f;
             float4 stat[S::NG];
 #pragma unroll
             for (int i = 0; i < S::NG; ++i) {
@@ -506,8 +605,8 @@ struct Piece {
             float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int i = 0; i < S::NG; ++i) {
-                L += stat[i].z * ex2(stat[i].x - or_zero(M));
-                const float f = ex2(stat[i].y - or_zero(MO));
+                L += stat[i].z * ex2(stat[i].x - M);
+                const float f = ex2(stat[i].y - MO);
                 const float4 x = *reinterpret_cast<const float4*>(o_s + (i * S::ROWS + r) * (D + 4) + ch);
                 o.x += f * x.x;
                 o.y += f * x.y;
@@ -527,25 +626,27 @@ struct Piece {
         __syncthreads();
     }
 
-    // acc[n0 + x] += weights x channels n0 + x of four tokens, x = 0 .. 3.
+    // acc[y0], acc[y0 + 1] += four channels of four tokens x weights.
     template <int N, int PCS>
-    static __device__ __forceinline__ void add_values(float (&acc)[N][4], int n0, const uint32_t (&pf)[PCS][4],
+    static __device__ __forceinline__ void add_values(float (&acc)[N][NT][4], int y0, const uint32_t (&pf)[PCS][NT][2],
                                                       uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3) {
-        uint32_t b0[4], b1[4];
-        word_to_half2x2(__byte_perm(v0, v1, 0x5140), b0[0], b0[1]);
-        word_to_half2x2(__byte_perm(v0, v1, 0x7362), b0[2], b0[3]);
-        word_to_half2x2(__byte_perm(v2, v3, 0x5140), b1[0], b1[1]);
-        word_to_half2x2(__byte_perm(v2, v3, 0x7362), b1[2], b1[3]);
+        uint32_t f[2][4];
+        word_to_half2x2(__byte_perm(v0, v1, 0x5140), f[0][0], f[0][1]);
+        word_to_half2x2(__byte_perm(v0, v1, 0x7362), f[1][0], f[1][1]);
+        word_to_half2x2(__byte_perm(v2, v3, 0x5140), f[0][2], f[0][3]);
+        word_to_half2x2(__byte_perm(v2, v3, 0x7362), f[1][2], f[1][3]);
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+        for (int y = 0; y < 2; ++y)
 #pragma unroll
-            for (int pc = 0; pc < PCS; ++pc) mma16816(acc[n0 + x], pf[pc], b0[x], b1[x]);
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int pc = 0; pc < PCS; ++pc) mma16816(acc[y0 + y][n], f[y], pf[pc][n][0], pf[pc][n][1]);
     }
 
     template <typename U>
     static __device__ __forceinline__ void write_row(const CacheAttention& a, int64_t row, int ch, float4 o,
                                                      float M, float MO, float L) {
-        const float f = L == 0.0f ? 0.0f : ex2(or_zero(MO) - or_zero(M) - kWeightBits) / L;
+        const float f = L == 0.0f ? 0.0f : ex2(MO - M - kWeightBits) / L;
         if (L == 0.0f) o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (ch < a.d) {
             U* to = static_cast<U*>(a.o) + row * a.d + ch;
@@ -561,33 +662,33 @@ struct Piece {
 };
 
 // Every CTA one item: (sequence, row tile, head), heads innermost.
-template <typename T, int D, int MT>
-__global__ void __launch_bounds__(kThreads, Shape<T, D, MT>::CTAS)
+template <typename T, int D, int NT, int MT>
+__global__ void __launch_bounds__(kThreads, Shape<T, D, NT, MT>::CTAS)
 attention_whole_kernel(const CacheAttention a, const Plan plan) {
     extern __shared__ __align__(16) uint8_t smem[];
     const int pair = blockIdx.x / a.H_kv, hk = blockIdx.x % a.H_kv;
     const int b = pair / plan.row_tiles, rt = pair % plan.row_tiles;
-    const Tile tile = make_tile<16 * MT>(a, plan, length_of(a, b), rt);
-    Piece<T, D, MT> piece{a, plan, smem, b, hk, rt, 0, tile.steps, tile};
+    const Tile tile = make_tile<8 * NT * MT>(a, plan, length_of(a, b), rt);
+    Piece<T, D, NT, MT> piece{a, plan, smem, b, hk, rt, 0, tile.steps, tile};
     piece.run(0, 0, true);
 }
 
 // Every CTA an equal share of all items' steps.
-template <typename T, int D, int MT>
-__global__ void __launch_bounds__(kThreads, Shape<T, D, MT>::CTAS)
+template <typename T, int D, int NT, int MT>
+__global__ void __launch_bounds__(kThreads, Shape<T, D, NT, MT>::CTAS)
 attention_share_kernel(const CacheAttention a, const Plan plan) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int64_t warp_sum_s[kWarps];
     __shared__ int64_t found_base;
     __shared__ int found_pair;
     asm volatile("griddepcontrol.launch_dependents;");
-    constexpr int ROWS = 16 * MT;
+    constexpr int ROWS = 8 * NT * MT;
     const int pairs = a.B * plan.row_tiles;
     const int each = (pairs + kThreads - 1) / kThreads;
     const int q0 = threadIdx.x * each;
     int64_t mine = 0;
     for (int q = q0; q < q0 + each && q < pairs; ++q)
-        mine += make_tile<ROWS>(a, plan, length_of(a, q / plan.row_tiles), q % plan.row_tiles).steps;
+        mine += make_tile<ROWS>(a, plan, length_of(a, q / plan.row_tiles), q % plan.row_tiles).steps + kItemCost;
     int64_t before = mine;                                 // steps of one head, up to this thread's end
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) {
@@ -612,8 +713,8 @@ attention_share_kernel(const CacheAttention a, const Plan plan) {
     if (begin >= before && begin < before + mine * a.H_kv) {
         int64_t base = before;
         for (int q = q0; q < pairs; ++q) {
-            const int64_t w = (int64_t)a.H_kv *
-                make_tile<ROWS>(a, plan, length_of(a, q / plan.row_tiles), q % plan.row_tiles).steps;
+            const int64_t w = (int64_t)a.H_kv * (
+                make_tile<ROWS>(a, plan, length_of(a, q / plan.row_tiles), q % plan.row_tiles).steps + kItemCost);
             if (begin < base + w) {
                 found_pair = q;
                 found_base = base;
@@ -628,23 +729,29 @@ attention_share_kernel(const CacheAttention a, const Plan plan) {
     if (pair >= 0) {
         int64_t base = found_base, at = begin;
         Tile tile = make_tile<ROWS>(a, plan, length_of(a, pair / plan.row_tiles), pair % plan.row_tiles);
-        int hk = (int)((begin - base) / tile.steps);
-        base += (int64_t)hk * tile.steps;                  // where the item begins in the list
+        int span = tile.steps + kItemCost;                 // of an item in the list, its cost first
+        int hk = (int)((begin - base) / span);
+        base += (int64_t)hk * span;                        // where the item begins
         while (at < end) {
-            const int64_t item_end = base + tile.steps;
+            const int64_t item_end = base + span;
             const int64_t stop = item_end < end ? item_end : end;
-            const bool whole = at == base && stop == item_end;
-            const int slot = at == begin ? 0 : 1;
-            Piece<T, D, MT> piece{a, plan, smem, pair / plan.row_tiles, hk, pair % plan.row_tiles,
-                                  (int)(at - base), (int)(stop - base), tile};
-            piece.run(blockIdx.x, slot, whole);
-            if (!whole && at == base) join = make_int4(pair, hk, (int)((item_end - 1) / share), slot);
+            const int from = at - base > kItemCost ? (int)(at - base) - kItemCost : 0;
+            const int to = stop - base > kItemCost ? (int)(stop - base) - kItemCost : 0;
+            if (from < to) {
+                const bool whole = from == 0 && to == tile.steps;
+                const int slot = at == begin ? 0 : 1;
+                Piece<T, D, NT, MT> piece{a, plan, smem, pair / plan.row_tiles, hk, pair % plan.row_tiles, from, to,
+                                          tile};
+                piece.run(blockIdx.x, slot, whole);
+                if (!whole && from == 0) join = make_int4(pair, hk, (int)((item_end - 1) / share), slot);
+            }
             at = stop;
             base = item_end;
             if (++hk == a.H_kv && at < end) {
                 hk = 0;
                 ++pair;
                 tile = make_tile<ROWS>(a, plan, length_of(a, pair / plan.row_tiles), pair % plan.row_tiles);
+                span = tile.steps + kItemCost;
             }
         }
     }
@@ -654,10 +761,10 @@ attention_share_kernel(const CacheAttention a, const Plan plan) {
 // The pieces of the item that begins in CTA blockIdx.x's share and ends in a later
 // one, joined in order: the first from its slot, the later ones from slot 0.  A
 // row a CTA at a time; eight warps take pieces in turn.
-template <typename T, int D, int MT>
+template <typename T, int D, int NT, int MT>
 __global__ void __launch_bounds__(kJoinThreads)
 attention_join_kernel(const CacheAttention a, const Plan plan) {
-    constexpr int WARPS = kJoinThreads / 32, PER = D / 32;
+    constexpr int WARPS = kJoinThreads / 32, PER = D / 32, ROWS = 8 * NT * MT;
     __shared__ float o_s[WARPS][D];
     __shared__ float l_s[WARPS];
     __shared__ float2 top_s[WARPS];
@@ -667,12 +774,12 @@ attention_join_kernel(const CacheAttention a, const Plan plan) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int first = blockIdx.x, n = join.z - first + 1;
     const int b = join.x / plan.row_tiles, rt = join.x % plan.row_tiles;
-    const int rows_here = plan.rows - rt * 16 * MT < 16 * MT ? plan.rows - rt * 16 * MT : 16 * MT;
+    const int rows_here = plan.rows - rt * ROWS < ROWS ? plan.rows - rt * ROWS : ROWS;
     for (int r = blockIdx.y; r < rows_here; r += gridDim.y) {
         auto place = [&](int i) -> int64_t {
             return ((int64_t)(first + i) * 2 + (i == 0 ? join.w : 0)) * plan.stored + r;
         };
-        float M = -INFINITY, MO = -INFINITY;
+        float M = kLowest, MO = kLowest;
         for (int i = threadIdx.x; i < n; i += kJoinThreads) {
             const float4 s = plan.stats[place(i)];
             M = fmaxf(M, s.x);
@@ -695,8 +802,8 @@ attention_join_kernel(const CacheAttention a, const Plan plan) {
         for (int i = warp; i < n; i += WARPS) {
             const int64_t at = place(i);
             const float4 s = plan.stats[at];
-            const float f = ex2(s.y - or_zero(MO));
-            L += s.z * ex2(s.x - or_zero(M));
+            const float f = ex2(s.y - MO);
+            L += s.z * ex2(s.x - M);
 #pragma unroll
             for (int x = 0; x < PER; ++x) o[x] += f * plan.sums[at * D + 32 * x + lane];
         }
@@ -716,8 +823,8 @@ attention_join_kernel(const CacheAttention a, const Plan plan) {
                 sum.w += x.w;
                 L += l_s[w];
             }
-            const int row = rt * 16 * MT + r, i = row / plan.group;
-            Piece<T, D, MT>::template write_row<T>(
+            const int row = rt * ROWS + r, i = row / plan.group;
+            Piece<T, D, NT, MT>::template write_row<T>(
                 a, ((int64_t)b * a.T_q + i) * a.H_q + join.y * plan.group + row - i * plan.group,
                 4 * threadIdx.x, sum, M, MO, L);
         }
@@ -726,46 +833,61 @@ attention_join_kernel(const CacheAttention a, const Plan plan) {
 }
 
 int rows_of(const CacheAttention& a) { return a.T_q * (a.H_q / a.H_kv); }
-// Row tiles of 16, of 32 (two warps share the tokens) or of 64 rows (four).
-int tile_warps(const CacheAttention& a) { return rows_of(a) <= 16 ? 1 : rows_of(a) <= 32 ? 2 : 4; }
 int padded_d(const CacheAttention& a) { return a.d <= 64 ? 64 : 128; }
 
+// Calls f with the shape for these queries: as many rows a warp as registers allow
+// before warps have to share tokens.
+template <typename T, int D, typename F>
+auto by_rows(const CacheAttention& a, F f) {
+    constexpr int MOST = sizeof(T) == 4 ? 2 : 4;
+    const int rows = rows_of(a);
+    if (rows <= 8) return f(Shape<T, D, 1, 1>{});
+    if (rows <= 16) return f(Shape<T, D, 2, 1>{});
+    if (rows <= 32) return f(Shape<T, D, MOST, 4 / MOST>{});
+    return f(Shape<T, D, MOST, 8 / MOST>{});
+}
+template <typename F>
+auto by_shape(const CacheAttention& a, bool bf16, F f) {
+    if (bf16) return padded_d(a) == 64 ? by_rows<__nv_bfloat16, 64>(a, f) : by_rows<__nv_bfloat16, 128>(a, f);
+    return padded_d(a) == 64 ? by_rows<float, 64>(a, f) : by_rows<float, 128>(a, f);
+}
+
 // CTAs of the shared-out form; 0 where each item is one CTA's.
-int64_t share_grid(const CacheAttention& a, int num_sms, int ctas) {
-    const int mt = tile_warps(a);
-    const int64_t row_tiles = (rows_of(a) + 16 * mt - 1) / (16 * mt);
+template <typename S>
+int64_t share_grid(const CacheAttention& a, int num_sms) {
+    const int64_t row_tiles = (rows_of(a) + S::ROWS - 1) / S::ROWS;
     const int64_t cap = ((int64_t)a.table_pages << a.page_shift) / kStep;
     if (cap <= kMinShare || a.B * row_tiles > kMaxScan) return 0;
-    const int64_t all = a.B * row_tiles * a.H_kv * cap;
-    const int64_t most = (int64_t)num_sms * ctas, useful = (all + kMinShare - 1) / kMinShare;
+    const int64_t all = a.B * row_tiles * a.H_kv * (cap + kItemCost);
+    const int64_t most = (int64_t)num_sms * S::CTAS, useful = (all + kMinShare - 1) / kMinShare;
     return useful < most ? useful : most;
 }
 
-template <typename T, int D, int MT>
+template <typename T, int D, int NT, int MT>
 cudaError_t launch(const CacheAttention& a, void* workspace, cudaStream_t stream, int num_sms) {
-    using S = Shape<T, D, MT>;
+    using S = Shape<T, D, NT, MT>;
     Plan plan = {};
     plan.group = a.H_q / a.H_kv;
     plan.rows = rows_of(a);
     plan.row_tiles = (plan.rows + S::ROWS - 1) / S::ROWS;
     plan.stored = plan.rows < S::ROWS ? plan.rows : S::ROWS;
-    const int64_t grid = share_grid(a, num_sms, S::CTAS);
+    const int64_t grid = share_grid<S>(a, num_sms);
     if (grid == 0) {
         const int64_t items = (int64_t)a.B * plan.row_tiles * a.H_kv;
-        cudaError_t e = cudaFuncSetAttribute(attention_whole_kernel<T, D, MT>,
+        cudaError_t e = cudaFuncSetAttribute(attention_whole_kernel<T, D, NT, MT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
         if (e != cudaSuccess) return e;
-        attention_whole_kernel<T, D, MT><<<(unsigned)items, kThreads, S::SMEM, stream>>>(a, plan);
+        attention_whole_kernel<T, D, NT, MT><<<(unsigned)items, kThreads, S::SMEM, stream>>>(a, plan);
         return cudaGetLastError();
     }
     const int64_t slots = grid * 2 * plan.stored;
     plan.joins = static_cast<int4*>(workspace);
     plan.stats = reinterpret_cast<float4*>(plan.joins + grid);
     plan.sums = reinterpret_cast<float*>(plan.stats + slots);
-    cudaError_t e = cudaFuncSetAttribute(attention_share_kernel<T, D, MT>,
+    cudaError_t e = cudaFuncSetAttribute(attention_share_kernel<T, D, NT, MT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
-    attention_share_kernel<T, D, MT><<<(unsigned)grid, kThreads, S::SMEM, stream>>>(a, plan);
+    attention_share_kernel<T, D, NT, MT><<<(unsigned)grid, kThreads, S::SMEM, stream>>>(a, plan);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // The second kernel's CTAs come up while the first ends, and wait for it.
@@ -778,38 +900,33 @@ cudaError_t launch(const CacheAttention& a, void* workspace, cudaStream_t stream
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, D, MT>, a, plan);
+    return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, D, NT, MT>, a, plan);
 }
 
-template <typename T, int D>
-cudaError_t by_rows(const CacheAttention& a, void* ws, cudaStream_t stream, int num_sms) {
-    switch (tile_warps(a)) {
-        case 1: return launch<T, D, 1>(a, ws, stream, num_sms);
-        case 2: return launch<T, D, 2>(a, ws, stream, num_sms);
-        default: return launch<T, D, 4>(a, ws, stream, num_sms);
-    }
-}
-
-template <typename T>
-cudaError_t by_d(const CacheAttention& a, void* ws, cudaStream_t stream, int num_sms) {
-    return padded_d(a) == 64 ? by_rows<T, 64>(a, ws, stream, num_sms)
-                             : by_rows<T, 128>(a, ws, stream, num_sms);
+template <typename T, int D, int NT, int MT>
+cudaError_t launch(Shape<T, D, NT, MT>, const CacheAttention& a, void* ws, cudaStream_t stream, int num_sms) {
+    return launch<T, D, NT, MT>(a, ws, stream, num_sms);
 }
 
 }  // namespace
 
 size_t cache_attention_workspace_bytes(const CacheAttention& a, int num_sms) {
-    const int mt = tile_warps(a);
-    const int64_t stored = rows_of(a) < 16 * mt ? rows_of(a) : 16 * mt;
-    // 3 CTAs a SM: the larger of what the two types of query run
-    const int64_t grid = share_grid(a, num_sms, 3);
-    return (size_t)grid * (16 + 2 * stored * (16 + padded_d(a) * 4));
+    // the larger of what the two types of query need
+    size_t most = 0;
+    for (int bf16 = 0; bf16 < 2; ++bf16) {
+        const size_t need = by_shape(a, bf16 != 0, [&](auto shape) -> size_t {
+            using S = decltype(shape);
+            const int64_t stored = rows_of(a) < S::ROWS ? rows_of(a) : S::ROWS;
+            return (size_t)share_grid<S>(a, num_sms) * (16 + 2 * stored * (16 + padded_d(a) * 4));
+        });
+        most = need > most ? need : most;
+    }
+    return most;
 }
 
 cudaError_t run_cache_attention(const CacheAttention& a, bool bf16, void* workspace, cudaStream_t stream,
                                 int num_sms) {
-    return bf16 ? by_d<__nv_bfloat16>(a, workspace, stream, num_sms)
-                : by_d<float>(a, workspace, stream, num_sms);
+    return by_shape(a, bf16, [&](auto shape) { return launch(shape, a, workspace, stream, num_sms); });
 }
 
 }  // namespace kda
