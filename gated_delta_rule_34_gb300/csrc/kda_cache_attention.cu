@@ -23,10 +23,13 @@
 // product's k index with channels, of its m index with channels of v, is free, so
 // each lane reads its own 16 consecutive bytes of a token's row, as they lie
 // in the cache, and its words are the fragments; the scores become the weights'
-// fragments by a transposition of 8 x 8 within the warp.  Every lane copies what
-// it will read itself (16-byte asynchronous copies into its own slots, some steps
-// ahead), so a warp runs without a barrier; with more rows than one warp takes,
-// MT warps share one ring of slots and one barrier a step.
+// fragments by a transposition of 8 x 8 within the warp.  A warp copies its steps
+// itself, 16 bytes a lane, some steps ahead, so it runs without a barrier; with
+// more rows than one warp takes, MT warps share one ring and one barrier a step.
+// The copies go along the rows, whole lines at a time (a million tokens of 8 heads took 448
+// us without any arithmetic when every lane fetched the bytes that it reads, half a
+// line a row, and 334 us so), and each lane puts its 16 bytes where the reading
+// lane's load meets no other's bank.
 //
 // The maximum is not brought up to date at every step: as long as no score is
 // above the last one by more than a factor of 4, sums keep their reference, and a
@@ -165,8 +168,7 @@ __device__ __forceinline__ void word_to_half2x2(uint32_t w, uint32_t& lo, uint32
 // c += a b: a is 16 x 16 (m = g and g + 8; k = 2c, 2c + 1, then 8 more), b 16 x 8
 // (n = g), c 16 x 8 (m = g and g + 8, n = 2c and 2c + 1), of lane 4 g + c.
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -175,18 +177,17 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // An 8 x 8 matrix of 16-bit values, a row a quad, transposed.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 
-template <int BYTES>
+// 16 bytes, zeros unless real.
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool real) {
-    const uint32_t n = real ? BYTES : 0;
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n)
-                     : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16u : 0u)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
@@ -214,8 +215,10 @@ struct Shape {
     static constexpr int KC = D / 64;                 // 16-byte pieces of a key that a lane reads
     static constexpr int VB = D / 8;                  // bytes of a value that a lane reads
     static constexpr int TILES = VB / 2;              // of 16 channels of v
-    static constexpr int K_BYTES = 2 * KC * 512;      // of a step: 16 keys
-    static constexpr int STAGE = K_BYTES + 4 * 32 * VB + 16;   // + the two scales
+    static constexpr int COPIES = D / 32;             // a warp's, of 16 rows of keys or of values
+    static constexpr int ROW_LANES = D / 16;          // lanes that copy one row
+    static constexpr int K_BYTES = kStep * D;         // of a step
+    static constexpr int STAGE = 2 * K_BYTES + 16;    // + the two scales
     static constexpr int RING = NG * STAGES * STAGE;
     static constexpr int JOIN = NG * ROWS * (D + 4) * 4 + NG * ROWS * 16;
     static constexpr int Q_AT = RING > JOIN ? RING : JOIN;
@@ -299,7 +302,23 @@ struct Piece {
         const int d = a.d;
         const int32_t* table = a.table + (int64_t)b * a.table_pages;
         const int page_mask = (1 << a.page_shift) - 1;
-        const int k_lane = g * d + 16 * c, v_lane = 2 * c * d + S::VB * g;   // of this lane's bytes in a step
+        // What this lane copies: 16-byte piece `piece` of row `row` (and of every 32 / ROW_LANES rows
+        // on), to where lane (g, c) will read it.  Keys: word j = piece / 4 of token g (or g + 8) is at
+        // [token / 8][j][4 g + c, its bit 2 turned for j = 1].  Values: token 8 (q / 2) + 2 c + q % 2
+        // is at [q][c], its pieces turned by c, so that the eight lanes of two g and four c differ.
+        const int row = lane / S::ROW_LANES, piece = lane % S::ROW_LANES;
+        const int from_lane = row * d + 16 * piece;
+        uint32_t k_to_lane, v_to_lane[2];
+        if constexpr (D == 128) {
+            k_to_lane = (piece >> 2) * 512 + ((4 * row + (piece & 3)) ^ (piece & 4)) * 16;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                v_to_lane[i] = (row & 1) * 512 + (2 * i + (row >> 1)) * 128 + (piece ^ (2 * (2 * i + (row >> 1)))) * 16;
+        } else {
+            k_to_lane = lane * 16;
+            v_to_lane[0] = v_to_lane[1] =
+                (row & 1) * 256 + ((row >> 1) ^ (row & 1)) * 64 + (piece ^ ((row >> 1) & 2)) * 16;
+        }
 
         auto page_at = [&](int s) -> int {
             const int t = tile.token(s);
@@ -314,37 +333,36 @@ struct Piece {
                 const int t0 = tile.token(s);
                 const int64_t block = (int64_t)pg * a.H_kv + hk;
                 const int64_t at = ((block << a.page_shift) + (t0 & page_mask)) * d;
-                const uint8_t* k = a.k_codes + at + k_lane;
-                const uint8_t* v = a.v_codes + at + v_lane;
+                const uint8_t* k = a.k_codes + at + from_lane;
+                const uint8_t* v = a.v_codes + at + from_lane;
                 const int n = tile.end - t0;               // tokens of the step that exist
-                const uint32_t k_to = stage + lane * 16, v_to = stage + S::K_BYTES + lane * S::VB;
+                const uint32_t k_to = stage + k_to_lane, v_to = stage + S::K_BYTES;
+                constexpr int ROWS_A_COPY = 32 / S::ROW_LANES;
+                // copy i of a warp's 16 rows starts at row i ROWS_A_COPY
+                auto k_at = [&](int i) { return k_to + (D == 128 ? (i >> 1) * 1024 + (i & 1) * 256 : i * 512); };
+                auto v_at = [&](int i) {
+                    return v_to + v_to_lane[D == 128 ? i & 1 : 0] + (D == 128 ? (i >> 1) * 1024 : i * 512);
+                };
                 if (d == D && n >= kStep) {
 #pragma unroll
-                    for (int i = 0; i < 2 * S::KC; ++i)
-                        if (MT == 1 || i % MT == wt)
-                            copy_async<16>(k_to + i * 512, k + 8 * (i / S::KC) * D + 64 * (i % S::KC), true);
+                    for (int i = 0; i < S::COPIES; ++i)
+                        if (MT == 1 || i % MT == wt) copy_async(k_at(i), k + i * 512, true);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (MT == 1 || i % MT == wt)
-                            copy_async<S::VB>(v_to + i * 32 * S::VB, v + (8 * (i / 2) + (i & 1)) * D, true);
+                    for (int i = 0; i < S::COPIES; ++i)
+                        if (MT == 1 || (i + S::COPIES) % MT == wt) copy_async(v_at(i), v + i * 512, true);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 2 * S::KC; ++i)
-                        if (MT == 1 || i % MT == wt) {
-                            const int up = 8 * (i / S::KC), byte = 64 * (i % S::KC);
-                            const bool real = up + g < n && byte + 16 * c < d;
-                            copy_async<16>(k_to + i * 512, real ? k + up * d + byte : a.k_codes, real);
-                        }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (MT == 1 || i % MT == wt) {
-                            const int up = 8 * (i / 2) + (i & 1);
-                            const bool real = up + 2 * c < n && S::VB * g < d;
-                            copy_async<S::VB>(v_to + i * 32 * S::VB, real ? v + up * d : a.v_codes, real);
-                        }
+                    for (int i = 0; i < S::COPIES; ++i) {
+                        const int up = i * ROWS_A_COPY;
+                        const bool real = up + row < n && 16 * piece < d;
+                        if (MT == 1 || i % MT == wt)
+                            copy_async(k_at(i), real ? k + up * d : a.k_codes, real);
+                        if (MT == 1 || (i + S::COPIES) % MT == wt)
+                            copy_async(v_at(i), real ? v + up * d : a.v_codes, real);
+                    }
                 }
                 if (wt == 0 && lane < 2)
-                    copy_async<4>(scales + 4 * lane, (lane ? a.v_scale : a.k_scale) + block, true);
+                    copy_async4(scales + 4 * lane, (lane ? a.v_scale : a.k_scale) + block);
             } else if (wt == 0 && lane < 2) {
                 asm volatile("st.shared.b32 [%0], %1;" ::"r"(scales + 4 * lane), "r"(0) : "memory");
             }
@@ -416,8 +434,8 @@ struct Piece {
                 for (int w = 0; w < 4; ++w) sc[n][w] = 0.0f;
 #pragma unroll
             for (int j = 0; j < S::KC; ++j) {
-                const uint4 k0 = *reinterpret_cast<const uint4*>(stage + j * 512 + lane * 16);
-                const uint4 k1 = *reinterpret_cast<const uint4*>(stage + (S::KC + j) * 512 + lane * 16);
+                const uint4 k0 = *reinterpret_cast<const uint4*>(stage + j * 512 + (lane ^ 4 * j) * 16);
+                const uint4 k1 = *reinterpret_cast<const uint4*>(stage + (S::KC + j) * 512 + (lane ^ 4 * j) * 16);
                 const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -522,15 +540,20 @@ struct Piece {
                 }
             }
             // Values: four tokens' words; a product's a pairs two tokens of one channel.
-            const uint8_t* vs = stage + S::K_BYTES + lane * S::VB;
+            const uint8_t* vs = stage + S::K_BYTES;
             uint32_t v[4][S::VB / 4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int w = 0; w < S::VB / 4; w += 2) {
-                    const uint2 two = *reinterpret_cast<const uint2*>(vs + i * 32 * S::VB + 4 * w);
-                    v[i][w] = two.x;
-                    v[i][w + 1] = two.y;
+                {
+                    if constexpr (D == 128) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(vs + i * 512 + c * 128 + (g ^ 2 * c) * 16);
+                        v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+                    } else {
+                        const uint2 x = *reinterpret_cast<const uint2*>(
+                            vs + i * 256 + (c ^ (i & 1)) * 64 + ((g >> 1) ^ (c & 2)) * 16 + (g & 1) * 8);
+                        v[i][0] = x.x, v[i][1] = x.y;
+                    }
                 }
             if (partly) {
                 uint32_t any = 0;
