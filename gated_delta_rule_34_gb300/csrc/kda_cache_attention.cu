@@ -782,28 +782,33 @@ attention_share_kernel(const CacheAttention a, const Plan plan) {
 }
 
 // The pieces of the item that begins in CTA blockIdx.x's share and ends in a later
-// one, joined in order: the first from its slot, the later ones from slot 0.  A
-// row a CTA at a time; eight warps take pieces in turn.
+// one, joined in order: the first from its slot, the later ones from slot 0.  Few
+// pieces: a warp a row, without a barrier; many: eight warps a row, each every
+// eighth piece, their sums joined in shared memory.
+constexpr int kJoinFew = 8;
 template <typename T, int D, int NT, int MT>
 __global__ void __launch_bounds__(kJoinThreads)
 attention_join_kernel(const CacheAttention a, const Plan plan) {
     constexpr int WARPS = kJoinThreads / 32, PER = D / 32, ROWS = 8 * NT * MT;
-    __shared__ float o_s[WARPS][D];
+    __shared__ float4 o_s[WARPS][D / PER];
     __shared__ float l_s[WARPS];
-    __shared__ float2 top_s[WARPS];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 join = plan.joins[blockIdx.x];
     if (join.x < 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int first = blockIdx.x, n = join.z - first + 1;
+    const int n = join.z - (int)blockIdx.x + 1;
     const int b = join.x / plan.row_tiles, rt = join.x % plan.row_tiles;
     const int rows_here = plan.rows - rt * ROWS < ROWS ? plan.rows - rt * ROWS : ROWS;
-    for (int r = blockIdx.y; r < rows_here; r += gridDim.y) {
+    const bool few = n <= kJoinFew;
+    const int at_once = few ? WARPS : 1, part = few ? 0 : warp, parts = few ? 1 : WARPS;
+    for (int r0 = blockIdx.y * at_once; r0 < rows_here; r0 += gridDim.y * at_once) {
+        const int r = r0 + (few ? warp : 0);
+        if (r >= rows_here) return;                        // only where no barrier follows
         auto place = [&](int i) -> int64_t {
-            return ((int64_t)(first + i) * 2 + (i == 0 ? join.w : 0)) * plan.stored + r;
+            return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? join.w : 0)) * plan.stored + r;
         };
         float M = kLowest, MO = kLowest;
-        for (int i = threadIdx.x; i < n; i += kJoinThreads) {
+        for (int i = lane; i < n; i += 32) {
             const float4 s = plan.stats[place(i)];
             M = fmaxf(M, s.x);
             MO = fmaxf(MO, s.y);
@@ -813,45 +818,48 @@ attention_join_kernel(const CacheAttention a, const Plan plan) {
             M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
             MO = fmaxf(MO, __shfl_xor_sync(0xffffffffu, MO, w));
         }
-        if (lane == 0) top_s[warp] = make_float2(M, MO);
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            M = fmaxf(M, top_s[w].x);
-            MO = fmaxf(MO, top_s[w].y);
-        }
-        float o[PER] = {}, L = 0.0f;
-#pragma unroll 4
-        for (int i = warp; i < n; i += WARPS) {
+        float o[4] = {}, L = 0.0f;
+#pragma unroll 8
+        for (int i = part; i < n; i += parts) {
             const int64_t at = place(i);
             const float4 s = plan.stats[at];
             const float f = ex2(s.y - MO);
             L += s.z * ex2(s.x - M);
-#pragma unroll
-            for (int x = 0; x < PER; ++x) o[x] += f * plan.sums[at * D + 32 * x + lane];
-        }
-#pragma unroll
-        for (int x = 0; x < PER; ++x) o_s[warp][32 * x + lane] = o[x];
-        if (lane == 0) l_s[warp] = L;
-        __syncthreads();
-        if (threadIdx.x < D / 4) {
-            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            L = 0.0f;
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                const float4 x = *reinterpret_cast<const float4*>(&o_s[w][4 * threadIdx.x]);
-                sum.x += x.x;
-                sum.y += x.y;
-                sum.z += x.z;
-                sum.w += x.w;
-                L += l_s[w];
+            const float* from = plan.sums + at * D + PER * lane;
+            if constexpr (PER == 4) {
+                const float4 x = *reinterpret_cast<const float4*>(from);
+                o[0] += f * x.x, o[1] += f * x.y, o[2] += f * x.z, o[3] += f * x.w;
+            } else {
+                const float2 x = *reinterpret_cast<const float2*>(from);
+                o[0] += f * x.x, o[1] += f * x.y;
             }
-            const int row = rt * ROWS + r, i = row / plan.group;
-            Piece<T, D, NT, MT>::template write_row<T>(
-                a, ((int64_t)b * a.T_q + i) * a.H_q + join.y * plan.group + row - i * plan.group,
-                4 * threadIdx.x, sum, M, MO, L);
         }
-        __syncthreads();
+        if (!few) {
+            o_s[warp][lane] = make_float4(o[0], o[1], o[2], o[3]);
+            if (lane == 0) l_s[warp] = L;
+            __syncthreads();
+            if (warp == 0) {
+                L = 0.0f;
+                o[0] = o[1] = o[2] = o[3] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w) {
+                    const float4 x = o_s[w][lane];
+                    o[0] += x.x, o[1] += x.y, o[2] += x.z, o[3] += x.w;
+                    L += l_s[w];
+                }
+            }
+            __syncthreads();
+            if (warp != 0) continue;
+        }
+        if constexpr (PER == 2) {                          // four channels a lane from here on
+            o[2] = __shfl_down_sync(0xffffffffu, o[0], 1);
+            o[3] = __shfl_down_sync(0xffffffffu, o[1], 1);
+            if (lane & 1) continue;
+        }
+        const int row = rt * ROWS + r, i = row / plan.group;
+        Piece<T, D, NT, MT>::template write_row<T>(
+            a, ((int64_t)b * a.T_q + i) * a.H_q + join.y * plan.group + row - i * plan.group, PER * lane,
+            make_float4(o[0], o[1], o[2], o[3]), M, MO, L);
     }
 }
 
@@ -913,9 +921,11 @@ cudaError_t launch(const CacheAttention& a, void* workspace, cudaStream_t stream
     attention_share_kernel<T, D, NT, MT><<<(unsigned)grid, kThreads, S::SMEM, stream>>>(a, plan);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // The second kernel's CTAs come up while the first ends, and wait for it.
+    // The second kernel's CTAs come up while the first ends, and wait for it.  A
+    // row a CTA where the items are so few that each ends in many pieces.
+    const bool many = grid > kJoinFew * (int64_t)a.B * plan.row_tiles * a.H_kv;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)(plan.stored < 8 ? plan.stored : 8));
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)(many ? plan.stored : (plan.stored + 7) / 8));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
