@@ -47,8 +47,8 @@
 //
 // V's scale.  The weights are e^(s - m) times the page's scale of v, whose range
 // is far beyond fp16's.  So the sums of v have a reference of their own, mo = max(s
-// + log2 scale), beside the maximum m that the sum of weights has; weights go
-// to fp16 as 2^(s + log2 scale - mo + 12), at most 2^15, with full precision down to
+// + log2 scale), beside the maximum m that the sum of weights has (kept as dm = m -
+// mo, which is small where m is large); weights go to fp16 as 2^(s + log2 scale - mo + 12), at most 2^15, with full precision down to
 // 2^-26 of the largest.
 //
 // NaN that a row does not see.  0 times NaN is NaN, so tokens past the last that
@@ -69,7 +69,6 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 16;             // tokens of a step
 constexpr int kMinShare = 8;          // steps below which no item is cut further
-constexpr int kItemCost = 6;          // what an item's start and end cost, in steps
 constexpr int kJoinThreads = 256;
 constexpr int kMaxScan = 8192;        // (sequence, row tile) pairs that every CTA sums up
 constexpr float kWeightBits = 12.0f;
@@ -82,7 +81,7 @@ struct Plan {
     int row_tiles;
     int stored;         // rows of a tile that exist
     float* sums;        // [grid][2][stored][D]
-    float4* stats;      // [grid][2][stored]: m, mo, l
+    float4* stats;      // [grid][2][stored]: m, dm, l
     int4* joins;        // [grid]: pair (sequence, row tile), head, last CTA, slot; pair < 0: none
 };
 
@@ -210,7 +209,8 @@ struct Shape {
     static constexpr int NG = kWarps / MT;
     static constexpr int ROWS = 8 * NT * MT;
     static constexpr int CTAS = PIECES == 1 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2) : (NT == 1 ? 3 : 2);   // resident a SM
-    static constexpr int STAGES = MT == 1 ? (CTAS == 4 ? 3 : 4) : MT == 2 ? 6 : 8;
+    static constexpr int STAGES = MT == 1 ? (CTAS == 4 ? 3 : NT == 4 ? 6 : 4) : MT == 2 ? 6 : 8;
+    static constexpr int ITEM_COST = NT == 4 ? 32 : 12;     // what an item's start and end cost, in steps
     static constexpr bool Q_HELD = NT <= 2;           // queries in registers, or read again at every step
     static constexpr int KC = D / 64;                 // 16-byte pieces of a key that a lane reads
     static constexpr int VB = D / 8;                  // bytes of a value that a lane reads
@@ -384,7 +384,7 @@ struct Piece {
         const uint4* q_s = reinterpret_cast<const uint4*>(smem + S::Q_AT) + wt * NT * S::KC * 64 + lane;
         const float* factor_s = reinterpret_cast<const float*>(smem + S::FACTOR_AT) + wt * NT * 8 + 2 * c;
         uint4 qh[S::Q_HELD ? S::PIECES : 1][S::Q_HELD ? NT : 1][S::KC][2];
-        float factor[NT][2], m[NT][2], mo[NT][2], l[NT][2];
+        float factor[NT][2], m[NT][2], dm[NT][2], l[NT][2];   // dm = m - mo
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             if constexpr (S::Q_HELD)
@@ -398,8 +398,8 @@ struct Piece {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 factor[n][r] = factor_s[8 * n + r];
-                m[n][r] = mo[n][r] = kLowest;
-                l[n][r] = 0.0f;
+                m[n][r] = kLowest;
+                dm[n][r] = l[n][r] = 0.0f;
             }
         }
         float acc[S::TILES][NT][4];
@@ -410,24 +410,8 @@ struct Piece {
 #pragma unroll
                 for (int w = 0; w < 4; ++w) acc[x][n][w] = 0.0f;
 
-        int st = 0;
-        for (int s = s0; s < to; s += S::NG) {
-            copy_wait<S::STAGES - 2>();
-            if constexpr (MT == 1) __syncwarp();
-            else tc::named_bar_sync(1 + grp, 32 * MT);
-            const uint8_t* stage = ring + st * S::STAGE;
-            const float2 scales = *reinterpret_cast<const float2*>(stage + S::STAGE - 16);
-            {
-                const int ahead = s + (S::STAGES - 1) * S::NG;
-                const int into = st == 0 ? S::STAGES - 1 : st - 1;
-                issue(ahead, next_page, into);
-                next_page = page_at(ahead + S::NG);
-            }
-            st = st == S::STAGES - 1 ? 0 : st + 1;
-            if (scales.y == 0.0f) continue;                // a page that is not held
-
-            // Scores of tokens g and g + 8 with rows 2 c and 2 c + 1 of each tile.
-            float sc[NT][4];
+        // Scores of a step's tokens g and g + 8 with rows 2 c and 2 c + 1 of each tile.
+        auto scores = [&](const uint8_t* stage, float (&sc)[NT][4]) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -456,6 +440,28 @@ struct Piece {
                         }
                 }
             }
+        };
+        auto meet = [&]() {
+            if constexpr (MT == 1) __syncwarp();
+            else tc::named_bar_sync(1 + grp, 32 * MT);
+        };
+
+        int st = 0;
+        for (int s = s0; s < to; s += S::NG) {
+            copy_wait<S::STAGES - 2>();
+            meet();
+            const uint8_t* stage = ring + st * S::STAGE;
+            const float2 scales = *reinterpret_cast<const float2*>(stage + S::STAGE - 16);
+            {
+                const int ahead = s + (S::STAGES - 1) * S::NG;
+                const int into = st == 0 ? S::STAGES - 1 : st - 1;
+                issue(ahead, next_page, into);
+                next_page = page_at(ahead + S::NG);
+            }
+            st = st == S::STAGES - 1 ? 0 : st + 1;
+            if (scales.y == 0.0f) continue;                // a page that is not held
+            float sc[NT][4];
+            scores(stage, sc);
             const int t0 = tile.token(s);
             const bool partly = t0 + kStep - 1 > tile.p0 ||
                                 (a.window > 0 && t0 <= tile.p1 - a.window && t0 + kStep - 1 >= a.sinks);
@@ -476,27 +482,32 @@ struct Piece {
                         }
                     }
             }
-            // log2 of v's scale: its exponent, and what remains (1 for these pages' powers of two)
-            const float e = (float)((int)(__float_as_uint(scales.y) >> 23) - 127);
-            const float mantissa = __uint_as_float((__float_as_uint(scales.y) & 0x7fffffu) | 0x3f800000u);
+            const float e = (float)((int)(__float_as_uint(scales.y) >> 23) - 127);   // log2 of v's scale
             // x = score - m, in powers of two
             float x[NT][4];
-            bool above = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const float f = factor[n][r] * scales.x;
-                    const float most = fminf(kSlack, kSlack - (m[n][r] + e - mo[n][r]));
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int w = 2 * h + r;
-                        x[n][w] = fmaf(sc[n][w], f, -m[n][r]);
-                        if (partly && !(sight >> (4 * n + w) & 1)) x[n][w] = -INFINITY;
-                        above |= x[n][w] > most;
-                    }
+                    x[n][r] = fmaf(sc[n][r], f, -m[n][r]);
+                    x[n][2 + r] = fmaf(sc[n][2 + r], f, -m[n][r]);
                 }
-            if (__any_sync(0xffffffffu, above)) {
+            if (partly) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        if (!(sight >> (4 * n + w) & 1)) x[n][w] = -INFINITY;
+            }
+            // Beyond m, or beyond mo with this page's scale: by how much, at most?
+            float beyond = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    beyond = fmaxf(beyond, fmaxf(x[n][r], x[n][2 + r]) + fmaxf(dm[n][r] + e, 0.0f));
+            if (__any_sync(0xffffffffu, beyond > kSlack)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float keep[2];
@@ -506,11 +517,12 @@ struct Piece {
                         const bool seen[2] = {(sight >> (4 * n + r) & 1) != 0, (sight >> (4 * n + 2 + r) & 1) != 0};
                         const float top = column_max(fmaxf(seen[0] ? sc[n][r] * f : -INFINITY,
                                                            seen[1] ? sc[n][2 + r] * f : -INFINITY));
-                        const float m_new = fmaxf(m[n][r], top), mo_new = fmaxf(mo[n][r], top + e);
-                        keep[r] = ex2(mo[n][r] - mo_new);
+                        const float m_new = fmaxf(m[n][r], top);
+                        const float dm_new = m_new - fmaxf(m[n][r] - dm[n][r], top + e);
+                        keep[r] = ex2(m[n][r] - m_new + (dm_new - dm[n][r]));
                         l[n][r] *= ex2(m[n][r] - m_new);
                         m[n][r] = m_new;
-                        mo[n][r] = mo_new;
+                        dm[n][r] = dm_new;
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
                             x[n][2 * h + r] = seen[h] ? fmaf(sc[n][2 * h + r], f, -m_new) : -INFINITY;
@@ -526,8 +538,7 @@ struct Piece {
             for (int n = 0; n < NT; ++n) {
                 float lift[2];
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    lift[r] = ex2(fminf(m[n][r] + e - mo[n][r] + kWeightBits, 126.0f)) * mantissa;
+                for (int r = 0; r < 2; ++r) lift[r] = ex2(fminf(dm[n][r] + (e + kWeightBits), 126.0f));
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float p0 = ex2(x[n][2 * h]), p1 = ex2(x[n][2 * h + 1]);
@@ -611,7 +622,7 @@ struct Piece {
                 for (int y = 0; y < S::TILES; y += 2)
                     *reinterpret_cast<float4*>(to_s + 2 * y) =
                         make_float4(acc[y][n][r], acc[y][n][2 + r], acc[y + 1][n][r], acc[y + 1][n][2 + r]);
-                if (g == 0) stat_s[grp * S::ROWS + row] = make_float4(m[n][r], mo[n][r], l[n][r], 0.0f);
+                if (g == 0) stat_s[grp * S::ROWS + row] = make_float4(m[n][r], dm[n][r], l[n][r], 0.0f);
             }
         __syncthreads();
         const int rows_here = plan.rows - rt * S::ROWS < S::ROWS ? plan.rows - rt * S::ROWS : S::ROWS;
@@ -623,13 +634,14 @@ struct Piece {
             for (int i = 0; i < S::NG; ++i) {
                 stat[i] = stat_s[i * S::ROWS + r];
                 M = fmaxf(M, stat[i].x);
-                MO = fmaxf(MO, stat[i].y);
+                MO = fmaxf(MO, stat[i].x - stat[i].y);
             }
+            const float DM = M - MO;
             float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int i = 0; i < S::NG; ++i) {
                 L += stat[i].z * ex2(stat[i].x - M);
-                const float f = ex2(stat[i].y - MO);
+                const float f = ex2(stat[i].x - M + (DM - stat[i].y));
                 const float4 x = *reinterpret_cast<const float4*>(o_s + (i * S::ROWS + r) * (D + 4) + ch);
                 o.x += f * x.x;
                 o.y += f * x.y;
@@ -639,11 +651,11 @@ struct Piece {
             if (whole) {
                 const int row = rt * S::ROWS + r, i = row / plan.group;
                 write_row<T>(a, ((int64_t)b * a.T_q + i) * a.H_q + hk * plan.group + row - i * plan.group, ch, o,
-                             M, MO, L);
+                             M, DM, L);
             } else {
                 const int64_t at = ((int64_t)cta * 2 + slot) * plan.stored + r;
                 *reinterpret_cast<float4*>(plan.sums + at * D + ch) = o;
-                if (ch == 0) plan.stats[at] = make_float4(M, MO, L, 0.0f);
+                if (ch == 0) plan.stats[at] = make_float4(M, DM, L, 0.0f);
             }
         }
         __syncthreads();
@@ -668,8 +680,8 @@ struct Piece {
 
     template <typename U>
     static __device__ __forceinline__ void write_row(const CacheAttention& a, int64_t row, int ch, float4 o,
-                                                     float M, float MO, float L) {
-        const float f = L == 0.0f ? 0.0f : ex2(MO - M - kWeightBits) / L;
+                                                     float M, float DM, float L) {
+        const float f = L == 0.0f ? 0.0f : ex2(-DM - kWeightBits) / L;
         if (L == 0.0f) o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (ch < a.d) {
             U* to = static_cast<U*>(a.o) + row * a.d + ch;
@@ -705,13 +717,13 @@ attention_share_kernel(const CacheAttention a, const Plan plan) {
     __shared__ int64_t found_base;
     __shared__ int found_pair;
     asm volatile("griddepcontrol.launch_dependents;");
-    constexpr int ROWS = 8 * NT * MT;
+    constexpr int ROWS = 8 * NT * MT, COST = Shape<T, D, NT, MT>::ITEM_COST;
     const int pairs = a.B * plan.row_tiles;
     const int each = (pairs + kThreads - 1) / kThreads;
     const int q0 = threadIdx.x * each;
     int64_t mine = 0;
     for (int q = q0; q < q0 + each && q < pairs; ++q)
-        mine += make_tile<ROWS>(a, plan, length_of(a, q / plan.row_tiles), q % plan.row_tiles).steps + kItemCost;
+        mine += make_tile<ROWS>(a, plan, length_of(a, q / plan.row_tiles), q % plan.row_tiles).steps + COST;
     int64_t before = mine;                                 // steps of one head, up to this thread's end
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) {
@@ -737,7 +749,7 @@ attention_share_kernel(const CacheAttention a, const Plan plan) {
         int64_t base = before;
         for (int q = q0; q < pairs; ++q) {
             const int64_t w = (int64_t)a.H_kv * (
-                make_tile<ROWS>(a, plan, length_of(a, q / plan.row_tiles), q % plan.row_tiles).steps + kItemCost);
+                make_tile<ROWS>(a, plan, length_of(a, q / plan.row_tiles), q % plan.row_tiles).steps + COST);
             if (begin < base + w) {
                 found_pair = q;
                 found_base = base;
@@ -752,14 +764,14 @@ attention_share_kernel(const CacheAttention a, const Plan plan) {
     if (pair >= 0) {
         int64_t base = found_base, at = begin;
         Tile tile = make_tile<ROWS>(a, plan, length_of(a, pair / plan.row_tiles), pair % plan.row_tiles);
-        int span = tile.steps + kItemCost;                 // of an item in the list, its cost first
+        int span = tile.steps + COST;                 // of an item in the list, its cost first
         int hk = (int)((begin - base) / span);
         base += (int64_t)hk * span;                        // where the item begins
         while (at < end) {
             const int64_t item_end = base + span;
             const int64_t stop = item_end < end ? item_end : end;
-            const int from = at - base > kItemCost ? (int)(at - base) - kItemCost : 0;
-            const int to = stop - base > kItemCost ? (int)(stop - base) - kItemCost : 0;
+            const int from = at - base > COST ? (int)(at - base) - COST : 0;
+            const int to = stop - base > COST ? (int)(stop - base) - COST : 0;
             if (from < to) {
                 const bool whole = from == 0 && to == tile.steps;
                 const int slot = at == begin ? 0 : 1;
@@ -774,7 +786,7 @@ attention_share_kernel(const CacheAttention a, const Plan plan) {
                 hk = 0;
                 ++pair;
                 tile = make_tile<ROWS>(a, plan, length_of(a, pair / plan.row_tiles), pair % plan.row_tiles);
-                span = tile.steps + kItemCost;
+                span = tile.steps + COST;
             }
         }
     }
@@ -811,19 +823,20 @@ attention_join_kernel(const CacheAttention a, const Plan plan) {
         for (int i = lane; i < n; i += 32) {
             const float4 s = plan.stats[place(i)];
             M = fmaxf(M, s.x);
-            MO = fmaxf(MO, s.y);
+            MO = fmaxf(MO, s.x - s.y);
         }
 #pragma unroll
         for (int w = 16; w > 0; w >>= 1) {
             M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
             MO = fmaxf(MO, __shfl_xor_sync(0xffffffffu, MO, w));
         }
+        const float DM = M - MO;
         float o[4] = {}, L = 0.0f;
 #pragma unroll 8
         for (int i = part; i < n; i += parts) {
             const int64_t at = place(i);
             const float4 s = plan.stats[at];
-            const float f = ex2(s.y - MO);
+            const float f = ex2(s.x - M + (DM - s.y));
             L += s.z * ex2(s.x - M);
             const float* from = plan.sums + at * D + PER * lane;
             if constexpr (PER == 4) {
@@ -859,7 +872,7 @@ attention_join_kernel(const CacheAttention a, const Plan plan) {
         const int row = rt * ROWS + r, i = row / plan.group;
         Piece<T, D, NT, MT>::template write_row<T>(
             a, ((int64_t)b * a.T_q + i) * a.H_q + join.y * plan.group + row - i * plan.group, PER * lane,
-            make_float4(o[0], o[1], o[2], o[3]), M, MO, L);
+            make_float4(o[0], o[1], o[2], o[3]), M, DM, L);
     }
 }
 
@@ -889,7 +902,7 @@ int64_t share_grid(const CacheAttention& a, int num_sms) {
     const int64_t row_tiles = (rows_of(a) + S::ROWS - 1) / S::ROWS;
     const int64_t cap = ((int64_t)a.table_pages << a.page_shift) / kStep;
     if (cap <= kMinShare || a.B * row_tiles > kMaxScan) return 0;
-    const int64_t all = a.B * row_tiles * a.H_kv * (cap + kItemCost);
+    const int64_t all = a.B * row_tiles * a.H_kv * (cap + S::ITEM_COST);
     const int64_t most = (int64_t)num_sms * S::CTAS, useful = (all + kMinShare - 1) / kMinShare;
     return useful < most ? useful : most;
 }
