@@ -101,14 +101,34 @@ __device__ __forceinline__ void load_unit(const T* p, uint4 (&raw)[sizeof(T)]) {
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T); ++i) raw[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
 }
+// The largest |x| of a unit and m, an infinity among them; NaN does not count.
 template <typename T>
-__device__ __forceinline__ float unit_amax(const uint4 (&raw)[sizeof(T)]) {
-    float f[16], m = 0.0f;
+__device__ __forceinline__ float unit_amax(const uint4 (&raw)[sizeof(T)], float m) {
+    if constexpr (sizeof(T) == 2) {
+        const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(raw);
+        __nv_bfloat162 top = __habs2(e[0]);
+#pragma unroll
+        for (int i = 1; i < 8; ++i) top = __hmax2(top, __habs2(e[i]));
+        return fmaxf(m, fmaxf(__low2float(top), __high2float(top)));
+    } else {
+        const float* e = reinterpret_cast<const float*>(raw);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(e[i]));
+        return m;
+    }
+}
+// The same of its finite values alone.
+template <typename T>
+__device__ __forceinline__ float unit_finite_amax(const uint4 (&raw)[sizeof(T)], float m) {
+    float f[16];
     unpack_unit<T>(raw, f);
 #pragma unroll
     for (int i = 0; i < 16; ++i) m = fmaxf(m, finite_abs(f[i]));
     return m;
 }
+// u / per_row for u < 2048 and per_row <= 8, from the reciprocal 65536 / per_row
+// rounded up: its excess below 1 adds less than 2048 / 65536 < 1 / 8.
+__device__ __forceinline__ int row_of(int u, int reciprocal) { return u * reciprocal >> 16; }
 template <typename T>
 __device__ __forceinline__ void round_unit(const uint4 (&raw)[sizeof(T)], float inv, uint8_t* to) {
     float f[16];
@@ -151,32 +171,44 @@ cache_write_kernel(CacheSpan w, const T* __restrict__ k, int64_t k_stride, const
     uint8_t* fresh = codes + offset * w.d;
     const float old = offset > 0 ? valid_scale(*scale) : 0.0f;
 
-    const int per_row = w.d / 16, units = run.n * per_row;
+    const int per_row = w.d / 16, units = run.n * per_row, reciprocal = (65536 + per_row - 1) / per_row;
+    auto unit = [&](int u) {
+        const int r = row_of(u, reciprocal);
+        return x + r * stride + (u - r * per_row) * 16;
+    };
     uint4 held[kHeld][sizeof(T)];
-    float amax = 0.0f;
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
         const int u = tid + j * THREADS;
-        if (u < units) load_unit(x + (u / per_row) * stride + u % per_row * 16, held[j]);
+        if (u < units) load_unit(unit(u), held[j]);
     }
+    auto over_all = [&](auto of_unit) {
+        float amax = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j)
-        if (tid + j * THREADS < units) amax = fmaxf(amax, unit_amax<T>(held[j]));
-    for (int u = tid + kHeld * THREADS; u < units; u += THREADS) {
-        uint4 raw[sizeof(T)];
-        load_unit(x + (u / per_row) * stride + u % per_row * 16, raw);
-        amax = fmaxf(amax, unit_amax<T>(raw));
-    }
+        for (int j = 0; j < kHeld; ++j)
+            if (tid + j * THREADS < units) amax = of_unit(held[j], amax);
+        for (int u = tid + kHeld * THREADS; u < units; u += THREADS) {
+            uint4 raw[sizeof(T)];
+            load_unit(unit(u), raw);
+            amax = of_unit(raw, amax);
+        }
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-    if constexpr (GROUP > 1) {
-        if (threadIdx.x % 32 == 0) warp_max[threadIdx.x / 32] = amax;
-        __syncthreads();                                   // also: `old` is read before it is written
-        amax = warp_max[0];
+        for (int m = 16; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+        if constexpr (GROUP > 1) {
+            if (threadIdx.x % 32 == 0) warp_max[threadIdx.x / 32] = amax;
+            __syncthreads();                               // also: `old` is read before it is written
+            amax = warp_max[0];
 #pragma unroll
-        for (int i = 1; i < GROUP; ++i) amax = fmaxf(amax, warp_max[i]);
-    } else {
-        __syncwarp();
+            for (int i = 1; i < GROUP; ++i) amax = fmaxf(amax, warp_max[i]);
+        } else {
+            __syncwarp();
+        }
+        return amax;
+    };
+    float amax = over_all([](const uint4 (&raw)[sizeof(T)], float m) { return unit_amax<T>(raw, m); });
+    if (amax > 3.402823466e38f) {                          // an infinity: once more without it
+        if constexpr (GROUP > 1) __syncthreads();
+        amax = over_all([](const uint4 (&raw)[sizeof(T)], float m) { return unit_finite_amax<T>(raw, m); });
     }
     const float s = fmaxf(page_scale(amax), old);
     const float inv = pow2_inverse(s);
@@ -187,7 +219,7 @@ cache_write_kernel(CacheSpan w, const T* __restrict__ k, int64_t k_stride, const
     }
     for (int u = tid + kHeld * THREADS; u < units; u += THREADS) {
         uint4 raw[sizeof(T)];
-        load_unit(x + (u / per_row) * stride + u % per_row * 16, raw);
+        load_unit(unit(u), raw);
         round_unit<T>(raw, inv, fresh + u * 16);
     }
     if (old > 0.0f && s > old) {
@@ -226,7 +258,7 @@ cache_read_kernel(CacheSpan w, const uint8_t* __restrict__ k_codes,
     const float s = is_held ? (is_v ? v_scale : k_scale)[block] : 0.0f;
     const uint8_t* codes = (is_v ? v_codes : k_codes) +
                            ((block << w.page_shift) + (run.at & ((1 << w.page_shift) - 1))) * w.d;
-    const int per_row = w.d / 16, units = run.n * per_row;
+    const int per_row = w.d / 16, units = run.n * per_row, reciprocal = (65536 + per_row - 1) / per_row;
     const int64_t row_stride = (int64_t)w.H * w.d;
     for (int u0 = threadIdx.x; u0 < units; u0 += kHeld * kCacheThreads) {
         uint4 c[kHeld];
@@ -249,7 +281,8 @@ cache_read_kernel(CacheSpan w, const uint8_t* __restrict__ k_codes,
             T* e = reinterpret_cast<T*>(out);
 #pragma unroll
             for (int i = 0; i < 16; ++i) e[i] = from_f32<T>(f[i] * s);
-            uint4* to = reinterpret_cast<uint4*>(y + (u / per_row) * row_stride + u % per_row * 16);
+            const int r = row_of(u, reciprocal);
+            uint4* to = reinterpret_cast<uint4*>(y + r * row_stride + (u - r * per_row) * 16);
 #pragma unroll
             for (int i = 0; i < (int)sizeof(T); ++i) __stcs(to + i, out[i]);
         }
