@@ -13,10 +13,13 @@
 // most 2^-32 turns plus p 2^-53.
 //
 // The split.  Bound by memory: every element is read and written once.  A CTA
-// takes a few tokens with all their heads, works out their rot / 2 angles once
-// into shared memory, and then gives every thread one (head, 16-byte vector)
-// place for all its tokens, so that the place is worked out once and the
-// loads of four tokens are in flight together.
+// takes a few tokens with all their heads and works out their rot / 2 angles once
+// into shared memory, in the order in which a warp's lanes read them together.  A thread
+// then has one vector's place in the head, of up to four heads of a token: their
+// loads are in flight together, and the angles are read once for the four.  (One head
+// and four tokens a thread: 70% of the copy rate at 40 heads of 128 channels, all
+// turned, 16384 tokens; 80% so.)  The vector is 16 bytes where rot allows it (rot / 2 whole
+// vectors in the half layout, rot in the interleaved one), else 8, 4 or 2.
 #include "kda_common.cuh"
 #include "kda_internal.h"
 
@@ -30,8 +33,10 @@ struct RotarySide {
 };
 
 constexpr int kRotaryThreads = 256;
-constexpr int kRotaryBatch = 4;               // tokens whose loads a thread has in flight
-constexpr int kRotaryRowBytes = 16 * 1024;    // of one pass of the ragged kernel (twice in shared memory)
+// Heads of one thread: four, or more of the interleaved layout's narrower
+// vectors (40 heads of 128 channels, 50 of them turned: 110 us with 4, 84 us with 16; in the half
+// layout, with two vectors a head, more than four gained nothing).
+constexpr int rotary_heads(bool half, int bytes) { return half || bytes > 8 ? 4 : 64 / bytes; }
 
 __device__ __forceinline__ float2 rotary_angle(double turns_per_position, int32_t position) {
     const double frac = turns_per_position - floor(turns_per_position);
@@ -42,190 +47,181 @@ __device__ __forceinline__ float2 rotary_angle(double turns_per_position, int32_
     return make_float2(c, s);
 }
 
-template <typename T>
-__device__ __forceinline__ void unpack16(const uint4& raw, float* f) {
+// A vector of N elements of T as one load or store.
+template <int BYTES>
+struct RawOf;
+template <>
+struct RawOf<16> { using type = uint4; };
+template <>
+struct RawOf<8> { using type = uint2; };
+template <>
+struct RawOf<4> { using type = uint32_t; };
+template <>
+struct RawOf<2> { using type = unsigned short; };
+
+template <typename T, int V>
+__device__ __forceinline__ void unpack_raw(const typename RawOf<V * sizeof(T)>::type& raw, float (&f)[V]) {
     const T* e = reinterpret_cast<const T*>(&raw);
 #pragma unroll
-    for (int i = 0; i < (int)(16 / sizeof(T)); ++i) f[i] = to_f32(e[i]);
+    for (int i = 0; i < V; ++i) f[i] = to_f32(e[i]);
 }
-template <typename T>
-__device__ __forceinline__ uint4 pack16(const float* f) {
-    uint4 raw;
+template <typename T, int V>
+__device__ __forceinline__ typename RawOf<V * sizeof(T)>::type pack_raw(const float (&f)[V]) {
+    typename RawOf<V * sizeof(T)>::type raw;
     T* e = reinterpret_cast<T*>(&raw);
 #pragma unroll
-    for (int i = 0; i < (int)(16 / sizeof(T)); ++i) e[i] = from_f32<T>(f[i]);
+    for (int i = 0; i < V; ++i) e[i] = from_f32<T>(f[i]);
     return raw;
 }
 
-// cos and sin of the CTA's tokens, [tokens][rot / 2].
-__device__ __forceinline__ void rotary_table(float2* cs, const int32_t* positions,
-                                             const double* freq, float amplitude, int64_t t0, int nt,
-                                             int half) {
-    for (int i = threadIdx.x; i < nt * half; i += kRotaryThreads) {
-        const int t = i / half;
-        const float2 a = rotary_angle(freq[i - t * half] * 0.15915494309189535,   // 1 / 2 pi
-                                      positions[t0 + t]);
-        cs[i] = make_float2(a.x * amplitude, a.y * amplitude);
-    }
-    __syncthreads();
-}
-
-// Whole 16-byte vectors of pairs: in the half layout rot / 2 is a multiple of
-// the vector, in the interleaved one rot is.  A unit is the vector (or, in the
-// half layout, the two) that one thread turns; the last units of a head are
-// vectors past rot, copied.
-template <typename T, bool HALF>
+// A unit is the vector (or, in the half layout, the two) that one thread turns.
+// A head's last units, past rot, are copied.  Where vectors are single bf16 values,
+// those from the next 16 bytes on are copied apart, 16 bytes at a time, and not at
+// all where the output is the input (50 of 128 channels turned: 174 us without, 117 us
+// so; wider vectors lose by it, as two passes then write the same sectors).
+template <typename T, bool HALF, int V>
 __global__ void __launch_bounds__(kRotaryThreads)
 rotary_kernel(RotarySide q, RotarySide k, const int32_t* __restrict__ positions,
               const double* __restrict__ freq, float amplitude, int64_t n_tokens, int d, int rot,
               int tile) {
-    constexpr int V = 16 / sizeof(T);
-    extern __shared__ __align__(16) float2 cs[];
-    const int half = rot / 2;
+    using Raw = typename RawOf<V * sizeof(T)>::type;
+    constexpr int A = HALF ? V : V / 2;                    // angles of a unit
+    constexpr int H = rotary_heads(HALF, V * sizeof(T));
+    extern __shared__ __align__(16) float2 cs[];           // [tokens][A][turned]
+    const int half = rot / 2, turned = half / A;
     const int64_t t0 = (int64_t)blockIdx.x * tile;
     const int nt = (int)(n_tokens - t0 < tile ? n_tokens - t0 : tile);
-    rotary_table(cs, positions, freq, amplitude, t0, nt, half);
+    for (int i = threadIdx.x; i < nt * half; i += kRotaryThreads) {
+        const int t = i / half, angle = i - t * half;
+        const float2 w = rotary_angle(freq[angle] * 0.15915494309189535, positions[t0 + t]);   // 1 / 2 pi
+        cs[t * half + angle % A * turned + angle / A] = make_float2(w.x * amplitude, w.y * amplitude);
+    }
+    __syncthreads();
 
-    const int turned = HALF ? half / V : rot / V;
-    const int units = turned + (d - rot) / V;
-    const int places = (q.heads + k.heads) * units;
-    for (int place = threadIdx.x; place < places; place += kRotaryThreads) {
-        const int row = place / units, u = place - row * units;
-        const bool is_q = row < q.heads;
-        const int h = is_q ? row : row - q.heads;
-        const int64_t xs = is_q ? q.xs : k.xs, ys = is_q ? q.ys : k.ys;
+    constexpr int W = 16 / sizeof(T);
+    constexpr bool APART = V * sizeof(T) == 2;
+    const int wide0 = APART ? (rot + W - 1) / W * W : d;   // where 16-byte copies begin
+    const int units = turned + (wide0 - rot) / V;
+    const int heads = q.heads + k.heads, lanes = (heads + H - 1) / H;
+    const int each = lanes * units;
+    for (int i = threadIdx.x; i < nt * each; i += kRotaryThreads) {
+        const int t = i / each, rest = i - t * each;
+        const int h0 = rest / units, u = rest - h0 * units;
         const bool copied = u >= turned;
-        const int64_t e0 = (int64_t)h * d + (copied ? rot + (u - turned) * V : u * V);
-        const T* x = static_cast<const T*>(is_q ? q.x : k.x) + t0 * xs + e0;
-        T* y = static_cast<T*>(is_q ? q.y : k.y) + t0 * ys + e0;
-        const bool pair = HALF && !copied;
-        for (int t = 0; t < nt; t += kRotaryBatch) {
-            uint4 a[kRotaryBatch], b[kRotaryBatch];
+        const int e0 = copied ? rot + (u - turned) * V : u * V;
+        const T* qx = static_cast<const T*>(q.x) + (t0 + t) * q.xs + e0;
+        const T* kx = static_cast<const T*>(k.x) + (t0 + t) * k.xs + e0;
+        Raw a[H], b[H];
 #pragma unroll
-            for (int j = 0; j < kRotaryBatch; ++j)
-                if (t + j < nt) {
-                    a[j] = __ldcs(reinterpret_cast<const uint4*>(x + (t + j) * xs));
-                    if (pair) b[j] = __ldcs(reinterpret_cast<const uint4*>(x + (t + j) * xs + half));
-                }
-#pragma unroll
-            for (int j = 0; j < kRotaryBatch; ++j)
-                if (t + j < nt) {
-                    uint4 out = a[j];
-                    if (!copied) {
-                        const float2* c = cs + (t + j) * half;
-                        float f[V];
-                        unpack16<T>(a[j], f);
-                        if constexpr (HALF) {
-                            float g[V];
-                            unpack16<T>(b[j], g);
-#pragma unroll
-                            for (int i = 0; i < V; ++i) {
-                                const float2 w = c[u * V + i];
-                                const float fx = f[i], gx = g[i];
-                                f[i] = fx * w.x - gx * w.y;
-                                g[i] = gx * w.x + fx * w.y;
-                            }
-                            __stcs(reinterpret_cast<uint4*>(y + (t + j) * ys + half), pack16<T>(g));
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < V; i += 2) {
-                                const float2 w = c[(u * V + i) / 2];
-                                const float fx = f[i], gx = f[i + 1];
-                                f[i] = fx * w.x - gx * w.y;
-                                f[i + 1] = gx * w.x + fx * w.y;
-                            }
-                        }
-                        out = pack16<T>(f);
-                    }
-                    __stcs(reinterpret_cast<uint4*>(y + (t + j) * ys), out);
-                }
-        }
-    }
-}
-
-// Any even rot: rows pass through shared memory a group of heads at a time
-// (read whole, then written from the copy, so the output may be the input),
-// and a thread makes the 16-byte vectors of the output element by element.
-// Two buffers: a group is read into one while the other's readers finish.
-template <typename T>
-__global__ void __launch_bounds__(kRotaryThreads)
-rotary_ragged_kernel(RotarySide q, RotarySide k, const int32_t* __restrict__ positions,
-                     const double* __restrict__ freq, float amplitude, int64_t n_tokens, int d,
-                     int rot, bool half_layout, int tile, int group) {
-    constexpr int V = 16 / sizeof(T);
-    extern __shared__ __align__(16) float2 cs[];
-    const int half = rot / 2;
-    const int64_t t0 = (int64_t)blockIdx.x * tile;
-    const int nt = (int)(n_tokens - t0 < tile ? n_tokens - t0 : tile);
-    uint4* rows = reinterpret_cast<uint4*>(cs + ((tile * half + 1) & ~1));   // 2 x [group][units]
-    const T* elems = reinterpret_cast<const T*>(rows);
-    rotary_table(cs, positions, freq, amplitude, t0, nt, half);
-
-    const int units = d / V, heads = q.heads + k.heads;
-    int buf = 0;
-    for (int t = 0; t < nt; ++t) {
-        const float2* c = cs + t * half;
-        for (int h0 = 0; h0 < heads; h0 += group) {
-            const int places = (heads - h0 < group ? heads - h0 : group) * units;
-            for (int place = threadIdx.x; place < places; place += kRotaryThreads) {
-                const int at = h0 * units + place;
-                const bool is_q = at < q.heads * units;
-                const int off = is_q ? at : at - q.heads * units;
-                const T* x = static_cast<const T*>(is_q ? q.x : k.x) + (t0 + t) * (is_q ? q.xs : k.xs);
-                rows[buf + place] = __ldcs(reinterpret_cast<const uint4*>(x) + off);
+        for (int j = 0; j < H; ++j) {
+            const int h = h0 + j * lanes;
+            if (h < heads) {
+                const T* x = h < q.heads ? qx + h * d : kx + (h - q.heads) * d;
+                a[j] = __ldcs(reinterpret_cast<const Raw*>(x));
+                if (HALF && !copied) b[j] = __ldcs(reinterpret_cast<const Raw*>(x + half));
             }
-            __syncthreads();
-            for (int place = threadIdx.x; place < places; place += kRotaryThreads) {
-                const int at = h0 * units + place;
-                const bool is_q = at < q.heads * units;
-                const int off = is_q ? at : at - q.heads * units;
-                const int row = place / units, e0 = (place - row * units) * V;
+        }
+        float2 w[A];
+        if (!copied) {
+#pragma unroll
+            for (int c = 0; c < A; ++c) w[c] = cs[t * half + c * turned + u];
+        }
+        T* qy = static_cast<T*>(q.y) + (t0 + t) * q.ys + e0;
+        T* ky = static_cast<T*>(k.y) + (t0 + t) * k.ys + e0;
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            const int h = h0 + j * lanes;
+            if (h >= heads) break;
+            T* y = h < q.heads ? qy + h * d : ky + (h - q.heads) * d;
+            if (!copied) {
                 float f[V];
-                unpack16<T>(rows[buf + place], f);
+                unpack_raw<T, V>(a[j], f);
+                if constexpr (HALF) {
+                    float g[V];
+                    unpack_raw<T, V>(b[j], g);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int e = e0 + i;
-                    if (e < rot) {
-                        const bool first = half_layout ? e < half : (e & 1) == 0;
-                        const int mate = half_layout ? (first ? e + half : e - half) : e ^ 1;
-                        const float2 w = c[half_layout ? (first ? e : mate) : e >> 1];
-                        const float g = to_f32(elems[buf * V + row * d + mate]);
-                        f[i] = first ? f[i] * w.x - g * w.y : f[i] * w.x + g * w.y;
+                    for (int c = 0; c < V; ++c) {
+                        const float fx = f[c], gx = g[c];
+                        f[c] = fx * w[c].x - gx * w[c].y;
+                        g[c] = gx * w[c].x + fx * w[c].y;
+                    }
+                    __stcs(reinterpret_cast<Raw*>(y + half), pack_raw<T, V>(g));
+                } else {
+#pragma unroll
+                    for (int c = 0; c < A; ++c) {
+                        const float fx = f[2 * c], gx = f[2 * c + 1];
+                        f[2 * c] = fx * w[c].x - gx * w[c].y;
+                        f[2 * c + 1] = gx * w[c].x + fx * w[c].y;
                     }
                 }
-                T* y = static_cast<T*>(is_q ? q.y : k.y) + (t0 + t) * (is_q ? q.ys : k.ys);
-                __stcs(reinterpret_cast<uint4*>(y) + off, pack16<T>(f));
+                a[j] = pack_raw<T, V>(f);
             }
-            buf = buf ? 0 : group * units;
+            __stcs(reinterpret_cast<Raw*>(y), a[j]);
+        }
+    }
+
+    if constexpr (!APART) return;
+    const bool q_apart = q.x != q.y || q.xs != q.ys, k_apart = k.x != k.y || k.xs != k.ys;
+    const int wide = lanes * ((d - wide0) / W);
+    if (wide == 0 || !(q_apart || k_apart)) return;
+    for (int i = threadIdx.x; i < nt * wide; i += kRotaryThreads) {
+        const int t = i / wide, rest = i - t * wide;
+        const int h0 = rest / (wide / lanes), e0 = wide0 + (rest - h0 * (wide / lanes)) * W;
+        const T* qx = static_cast<const T*>(q.x) + (t0 + t) * q.xs + e0;
+        const T* kx = static_cast<const T*>(k.x) + (t0 + t) * k.xs + e0;
+        T* qy = static_cast<T*>(q.y) + (t0 + t) * q.ys + e0;
+        T* ky = static_cast<T*>(k.y) + (t0 + t) * k.ys + e0;
+        uint4 a[H];
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            const int h = h0 + j * lanes;
+            if (h < heads)
+                a[j] = __ldcs(reinterpret_cast<const uint4*>(h < q.heads ? qx + h * d : kx + (h - q.heads) * d));
+        }
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            const int h = h0 + j * lanes;
+            if (h < heads)
+                __stcs(reinterpret_cast<uint4*>(h < q.heads ? qy + h * d : ky + (h - q.heads) * d), a[j]);
         }
     }
 }
 
-template <typename T>
+template <typename T, bool HALF, int V>
 static cudaError_t launch_rotary(const RotarySide& q, const RotarySide& k, const int32_t* positions,
                                  const double* freq, float amplitude, int64_t n_tokens, int d,
-                                 int rot, bool half_layout, cudaStream_t stream, int num_sms) {
-    constexpr int V = 16 / sizeof(T);
-    // Tokens a CTA takes: enough that the angles are shared out and four tokens'
-    // loads are in flight, but no more while there are SMs without a CTA.
-    int tile = 8;
-    while (tile > 1 && (n_tokens + tile - 1) / tile < 2 * num_sms) tile /= 2;
+                                 int rot, cudaStream_t stream, int num_sms) {
+    // Tokens a CTA takes: enough to keep its threads busy for some rounds, but no
+    // more while there are SMs without a CTA.
+    int tile = 16;
+    while (tile > 1 && (n_tokens + tile - 1) / tile < 4 * num_sms) tile /= 2;
     const unsigned grid = (unsigned)((n_tokens + tile - 1) / tile);
-    const size_t table = (size_t)((tile * (rot / 2) + 1) & ~1) * sizeof(float2);
-    if (half_layout && rot / 2 % V == 0) {
-        rotary_kernel<T, true><<<grid, kRotaryThreads, table, stream>>>(
-            q, k, positions, freq, amplitude, n_tokens, d, rot, tile);
-    } else if (!half_layout && rot % V == 0) {
-        rotary_kernel<T, false><<<grid, kRotaryThreads, table, stream>>>(
-            q, k, positions, freq, amplitude, n_tokens, d, rot, tile);
-    } else {
-        int group = kRotaryRowBytes / (d * (int)sizeof(T));   // d <= 256: at least 16 heads
-        if (group > q.heads + k.heads) group = q.heads + k.heads;
-        const size_t smem = table + 2 * (size_t)group * d * sizeof(T);
-        rotary_ragged_kernel<T><<<grid, kRotaryThreads, smem, stream>>>(
-            q, k, positions, freq, amplitude, n_tokens, d, rot, half_layout, tile, group);
-    }
+    rotary_kernel<T, HALF, V><<<grid, kRotaryThreads, (size_t)tile * (rot / 2) * sizeof(float2), stream>>>(
+        q, k, positions, freq, amplitude, n_tokens, d, rot, tile);
     return cudaGetLastError();
+}
+
+// The widest vector that rot allows; d is whole 16-byte vectors.
+template <typename T>
+static cudaError_t by_vector(const RotarySide& q, const RotarySide& k, const int32_t* positions,
+                             const double* freq, float amplitude, int64_t n_tokens, int d, int rot,
+                             bool half_layout, cudaStream_t stream, int num_sms) {
+    constexpr int W = 16 / sizeof(T);
+#define KDA_ROTARY(HALF, V) \
+    launch_rotary<T, HALF, V>(q, k, positions, freq, amplitude, n_tokens, d, rot, stream, num_sms)
+    if (half_layout) {
+        const int n = rot / 2;
+        if (n % W == 0) return KDA_ROTARY(true, W);
+        if (n % (W / 2) == 0) return KDA_ROTARY(true, W / 2);
+        if constexpr (W == 8)
+            if (n % 2 == 0) return KDA_ROTARY(true, 2);
+        return KDA_ROTARY(true, 1);
+    }
+    if (rot % W == 0) return KDA_ROTARY(false, W);
+    if constexpr (W == 8)
+        if (rot % 4 == 0) return KDA_ROTARY(false, 4);
+    return KDA_ROTARY(false, 2);
+#undef KDA_ROTARY
 }
 
 cudaError_t run_rotary(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int H_q,
@@ -235,11 +231,10 @@ cudaError_t run_rotary(const void* q, int64_t q_stride, void* q_out, int64_t q_o
                        cudaStream_t stream, int num_sms) {
     const RotarySide qs{q, q_out, q_stride, q_out_stride, H_q};
     const RotarySide ks{k, k_out, k_stride, k_out_stride, H_k};
-    if (bf16)
-        return launch_rotary<__nv_bfloat16>(qs, ks, positions, freq, amplitude, n_tokens, d, rot,
-                                            half_layout, stream, num_sms);
-    return launch_rotary<float>(qs, ks, positions, freq, amplitude, n_tokens, d, rot, half_layout,
-                                stream, num_sms);
+    return bf16 ? by_vector<__nv_bfloat16>(qs, ks, positions, freq, amplitude, n_tokens, d, rot,
+                                           half_layout, stream, num_sms)
+                : by_vector<float>(qs, ks, positions, freq, amplitude, n_tokens, d, rot, half_layout,
+                                   stream, num_sms);
 }
 
 }  // namespace kda
