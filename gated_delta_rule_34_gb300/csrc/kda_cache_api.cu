@@ -254,10 +254,11 @@ kda_status kda_cache_attention(const void* q, int64_t q_stride, const void* k_co
     if (table_pages > 0) KDA_POINTER(block_table, 4);
     a.q = q;
     a.q_stride = q_stride;
-    a.k_codes = static_cast<const uint8_t*>(k_codes);
-    a.v_codes = static_cast<const uint8_t*>(v_codes);
-    a.k_scale = k_scale;
-    a.v_scale = v_scale;
+    // (a pool without pages is not read, but its address goes into empty copies)
+    a.k_codes = static_cast<const uint8_t*>(n_pages > 0 ? k_codes : q);
+    a.v_codes = static_cast<const uint8_t*>(n_pages > 0 ? v_codes : q);
+    a.k_scale = n_pages > 0 ? k_scale : static_cast<const float*>(q);
+    a.v_scale = n_pages > 0 ? v_scale : static_cast<const float*>(q);
     a.table = block_table;
     a.lengths = lengths;
     a.o = o;

@@ -56,80 +56,16 @@
 // some rows see and others do not is looked through for NaN codes of v: if there are
 // any they count as zeros, and a product of the rows' sight with the places of
 // the NaN marks the outputs that they do reach.
-#include <climits>
-
-#include "kda_cache.cuh"
-#include "kda_internal.h"
-#include "tc_util.cuh"
+#include "kda_attention_common.cuh"
 
 namespace kda {
 namespace {
 
+using namespace attn;
+
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStep = 16;             // tokens of a step
-constexpr int kMinShare = 8;          // steps below which no item is cut further
-constexpr int kJoinThreads = 256;
-constexpr int kMaxScan = 8192;        // (sequence, row tile) pairs that every CTA sums up
-constexpr float kWeightBits = 12.0f;
-constexpr float kSlack = 2.0f;        // log2 of how far scores may pass the reference
-constexpr float kLowest = -3.402823466e38f;   // the reference before any score
 
-struct Plan {
-    int group;          // query heads of a head of keys
-    int rows;           // T_q * group
-    int row_tiles;
-    int stored;         // rows of a tile that exist
-    float* sums;        // [grid][2][stored][D]
-    float4* stats;      // [grid][2][stored]: m, dm, l
-    int4* joins;        // [grid]: pair (sequence, row tile), head, last CTA, slot; pair < 0: none
-};
-
-// What a row tile of a sequence sees, in steps.
-struct Tile {
-    int p0, p1;         // positions of its first and last row
-    int end;            // tokens [0, end) at most
-    int first_step;     // of the window (or 0), after sink_steps steps from 0
-    int sink_steps;
-    int steps;          // at least 1, so that a row that sees nothing is written too
-    __device__ __forceinline__ int token(int s) const {
-        return (s < sink_steps ? s : first_step + s - sink_steps) * kStep;
-    }
-};
-
-template <int ROWS>
-__device__ __forceinline__ Tile make_tile(const CacheAttention& a, const Plan& plan, int len, int rt) {
-    Tile t;
-    const int r0 = rt * ROWS;
-    const int r1 = (plan.rows < r0 + ROWS ? plan.rows : r0 + ROWS) - 1;
-    t.p0 = len - a.T_q + r0 / plan.group;
-    t.p1 = len - a.T_q + r1 / plan.group;
-    t.end = t.p1 + 1 > 0 ? t.p1 + 1 : 0;
-    int lo = 0, sink_end = 0;
-    if (a.window > 0) {
-        const int64_t l = (int64_t)t.p0 - a.window + 1;
-        lo = l > 0 ? (int)l : 0;
-        sink_end = a.sinks < lo ? a.sinks : lo;
-    }
-    t.first_step = lo / kStep;
-    t.sink_steps = (sink_end + kStep - 1) / kStep;
-    if (t.sink_steps > t.first_step) t.sink_steps = t.first_step;
-    const int n = t.sink_steps + (t.end + kStep - 1) / kStep - t.first_step;
-    t.steps = n > 1 ? n : 1;
-    return t;
-}
-
-__device__ __forceinline__ int length_of(const CacheAttention& a, int b) {
-    const int cap = a.table_pages << a.page_shift;
-    const int len = a.lengths[b];
-    return len < 0 ? 0 : (len > cap ? cap : len);
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ float quad_max(float x) {
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
     return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
@@ -146,10 +82,6 @@ __device__ __forceinline__ float column_sum(float x) {
     return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
 // What half2_bits lost of (lo, hi).
 __device__ __forceinline__ uint32_t half2_rest(float lo, float hi, uint32_t bits) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&bits));
@@ -178,25 +110,6 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
-}
-
-// 16 bytes, zeros unless real.
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool real) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16u : 0u)
-                 : "memory");
-}
-__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-// 0x7f in each byte that holds a NaN code, else 0.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-    return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
 
 // The sizes that go together: a warp takes NT tiles of 8 rows; MT warps share
@@ -362,7 +275,7 @@ struct Piece {
                     }
                 }
                 if (wt == 0 && lane < 2)
-                    copy_async4(scales + 4 * lane, (lane ? a.v_scale : a.k_scale) + block);
+                    copy_async4(scales + 4 * lane, (lane ? a.v_scale : a.k_scale) + block, true);
             } else if (wt == 0 && lane < 2) {
                 asm volatile("st.shared.b32 [%0], %1;" ::"r"(scales + 4 * lane), "r"(0) : "memory");
             }
@@ -554,18 +467,16 @@ struct Piece {
             const uint8_t* vs = stage + S::K_BYTES;
             uint32_t v[4][S::VB / 4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                {
-                    if constexpr (D == 128) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(vs + i * 512 + c * 128 + (g ^ 2 * c) * 16);
-                        v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-                    } else {
-                        const uint2 x = *reinterpret_cast<const uint2*>(
-                            vs + i * 256 + (c ^ (i & 1)) * 64 + ((g >> 1) ^ (c & 2)) * 16 + (g & 1) * 8);
-                        v[i][0] = x.x, v[i][1] = x.y;
-                    }
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (D == 128) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(vs + i * 512 + c * 128 + (g ^ 2 * c) * 16);
+                    v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2*>(
+                        vs + i * 256 + (c ^ (i & 1)) * 64 + ((g >> 1) ^ (c & 2)) * 16 + (g & 1) * 8);
+                    v[i][0] = x.x, v[i][1] = x.y;
                 }
+            }
             if (partly) {
                 uint32_t any = 0;
 #pragma unroll
@@ -625,7 +536,7 @@ struct Piece {
                 if (g == 0) stat_s[grp * S::ROWS + row] = make_float4(m[n][r], dm[n][r], l[n][r], 0.0f);
             }
         __syncthreads();
-        const int rows_here = plan.rows - rt * S::ROWS < S::ROWS ? plan.rows - rt * S::ROWS : S::ROWS;
+        const int rows_here = rows_of_tile(plan, rt);
         for (int u = threadIdx.x; u < rows_here * (D / 4); u += kThreads) {
             const int r = u / (D / 4), ch = u % (D / 4) * 4;
             float M = kLowest, MO = kLowest, L = 0.0f;
@@ -649,9 +560,7 @@ struct Piece {
                 o.w += f * x.w;
             }
             if (whole) {
-                const int row = rt * S::ROWS + r, i = row / plan.group;
-                write_row<T>(a, ((int64_t)b * a.T_q + i) * a.H_q + hk * plan.group + row - i * plan.group, ch, o,
-                             M, DM, L);
+                write_row<T>(a, output_row(a, plan, b, hk, rt, r), ch, o, M, DM, L);
             } else {
                 const int64_t at = ((int64_t)cta * 2 + slot) * plan.stored + r;
                 *reinterpret_cast<float4*>(plan.sums + at * D + ch) = o;
@@ -678,22 +587,6 @@ struct Piece {
                 for (int pc = 0; pc < PCS; ++pc) mma16816(acc[y0 + y][n], f[y], pf[pc][n][0], pf[pc][n][1]);
     }
 
-    template <typename U>
-    static __device__ __forceinline__ void write_row(const CacheAttention& a, int64_t row, int ch, float4 o,
-                                                     float M, float DM, float L) {
-        const float f = L == 0.0f ? 0.0f : ex2(-DM - kWeightBits) / L;
-        if (L == 0.0f) o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (ch < a.d) {
-            U* to = static_cast<U*>(a.o) + row * a.d + ch;
-            if constexpr (sizeof(U) == 2) {
-                const uint2 w = make_uint2(tc::pack_bf16x2(o.x * f, o.y * f), tc::pack_bf16x2(o.z * f, o.w * f));
-                *reinterpret_cast<uint2*>(to) = w;
-            } else {
-                *reinterpret_cast<float4*>(to) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-            }
-        }
-        if (ch == 0 && a.lse) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-    }
 };
 
 // Every CTA one item: (sequence, row tile, head), heads innermost.
@@ -702,9 +595,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT, MT>::CTAS)
 attention_whole_kernel(const CacheAttention a, const Plan plan) {
     extern __shared__ __align__(16) uint8_t smem[];
     const int pair = blockIdx.x / a.H_kv, hk = blockIdx.x % a.H_kv;
-    const int b = pair / plan.row_tiles, rt = pair % plan.row_tiles;
-    const Tile tile = make_tile<8 * NT * MT>(a, plan, length_of(a, b), rt);
-    Piece<T, D, NT, MT> piece{a, plan, smem, b, hk, rt, 0, tile.steps, tile};
+    const Tile tile = tile_of(a, plan, pair);
+    Piece<T, D, NT, MT> piece{a, plan, smem, pair / plan.row_tiles, hk, pair % plan.row_tiles, 0, tile.steps, tile};
     piece.run(0, 0, true);
 }
 
@@ -713,83 +605,13 @@ template <typename T, int D, int NT, int MT>
 __global__ void __launch_bounds__(kThreads, Shape<T, D, NT, MT>::CTAS)
 attention_share_kernel(const CacheAttention a, const Plan plan) {
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ int64_t warp_sum_s[kWarps];
-    __shared__ int64_t found_base;
-    __shared__ int found_pair;
     asm volatile("griddepcontrol.launch_dependents;");
-    constexpr int ROWS = 8 * NT * MT, COST = Shape<T, D, NT, MT>::ITEM_COST;
-    const int pairs = a.B * plan.row_tiles;
-    const int each = (pairs + kThreads - 1) / kThreads;
-    const int q0 = threadIdx.x * each;
-    int64_t mine = 0;
-    for (int q = q0; q < q0 + each && q < pairs; ++q)
-        mine += make_tile<ROWS>(a, plan, length_of(a, q / plan.row_tiles), q % plan.row_tiles).steps + COST;
-    int64_t before = mine;                                 // steps of one head, up to this thread's end
-#pragma unroll
-    for (int w = 1; w < 32; w <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, before, w);
-        if ((threadIdx.x & 31) >= w) before += x;
-    }
-    if ((threadIdx.x & 31) == 31) warp_sum_s[threadIdx.x >> 5] = before;
-    if (threadIdx.x == 0) found_pair = -1;
-    __syncthreads();
-    int64_t total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < (int)(threadIdx.x >> 5)) before += warp_sum_s[w];
-        total += warp_sum_s[w];
-    }
-    before = (before - mine) * a.H_kv;
-    total *= a.H_kv;
-    int64_t share = (total + gridDim.x - 1) / gridDim.x;
-    if (share < kMinShare) share = kMinShare;
-    const int64_t begin = share * blockIdx.x;
-    const int64_t end = begin + share < total ? begin + share : total;
-    if (begin >= before && begin < before + mine * a.H_kv) {
-        int64_t base = before;
-        for (int q = q0; q < pairs; ++q) {
-            const int64_t w = (int64_t)a.H_kv * (
-                make_tile<ROWS>(a, plan, length_of(a, q / plan.row_tiles), q % plan.row_tiles).steps + COST);
-            if (begin < base + w) {
-                found_pair = q;
-                found_base = base;
-                break;
-            }
-            base += w;
-        }
-    }
-    __syncthreads();
-    int pair = found_pair;
-    int4 join = make_int4(-1, 0, 0, 0);
-    if (pair >= 0) {
-        int64_t base = found_base, at = begin;
-        Tile tile = make_tile<ROWS>(a, plan, length_of(a, pair / plan.row_tiles), pair % plan.row_tiles);
-        int span = tile.steps + COST;                 // of an item in the list, its cost first
-        int hk = (int)((begin - base) / span);
-        base += (int64_t)hk * span;                        // where the item begins
-        while (at < end) {
-            const int64_t item_end = base + span;
-            const int64_t stop = item_end < end ? item_end : end;
-            const int from = at - base > COST ? (int)(at - base) - COST : 0;
-            const int to = stop - base > COST ? (int)(stop - base) - COST : 0;
-            if (from < to) {
-                const bool whole = from == 0 && to == tile.steps;
-                const int slot = at == begin ? 0 : 1;
-                Piece<T, D, NT, MT> piece{a, plan, smem, pair / plan.row_tiles, hk, pair % plan.row_tiles, from, to,
-                                          tile};
-                piece.run(blockIdx.x, slot, whole);
-                if (!whole && from == 0) join = make_int4(pair, hk, (int)((item_end - 1) / share), slot);
-            }
-            at = stop;
-            base = item_end;
-            if (++hk == a.H_kv && at < end) {
-                hk = 0;
-                ++pair;
-                tile = make_tile<ROWS>(a, plan, length_of(a, pair / plan.row_tiles), pair % plan.row_tiles);
-                span = tile.steps + COST;
-            }
-        }
-    }
+    const Share share = find_share<kThreads>(a, plan);
+    const int4 join = for_each_piece(a, plan, share, [&](int pair, int hk, const Tile& tile, int from, int to, int slot,
+                                                         bool whole) {
+        Piece<T, D, NT, MT> piece{a, plan, smem, pair / plan.row_tiles, hk, pair % plan.row_tiles, from, to, tile};
+        piece.run(blockIdx.x, slot, whole);
+    });
     if (threadIdx.x == 0) plan.joins[blockIdx.x] = join;
 }
 
@@ -797,11 +619,10 @@ attention_share_kernel(const CacheAttention a, const Plan plan) {
 // one, joined in order: the first from its slot, the later ones from slot 0.  Few
 // pieces: a warp a row, without a barrier; many: eight warps a row, each every
 // eighth piece, their sums joined in shared memory.
-constexpr int kJoinFew = 8;
-template <typename T, int D, int NT, int MT>
+template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads)
 attention_join_kernel(const CacheAttention a, const Plan plan) {
-    constexpr int WARPS = kJoinThreads / 32, PER = D / 32, ROWS = 8 * NT * MT;
+    constexpr int WARPS = kJoinThreads / 32, PER = D / 32;
     __shared__ float4 o_s[WARPS][D / PER];
     __shared__ float l_s[WARPS];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -810,7 +631,7 @@ attention_join_kernel(const CacheAttention a, const Plan plan) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n = join.z - (int)blockIdx.x + 1;
     const int b = join.x / plan.row_tiles, rt = join.x % plan.row_tiles;
-    const int rows_here = plan.rows - rt * ROWS < ROWS ? plan.rows - rt * ROWS : ROWS;
+    const int rows_here = rows_of_tile(plan, rt);
     const bool few = n <= kJoinFew;
     const int at_once = few ? WARPS : 1, part = few ? 0 : warp, parts = few ? 1 : WARPS;
     for (int r0 = blockIdx.y * at_once; r0 < rows_here; r0 += gridDim.y * at_once) {
@@ -869,10 +690,8 @@ attention_join_kernel(const CacheAttention a, const Plan plan) {
             o[3] = __shfl_down_sync(0xffffffffu, o[1], 1);
             if (lane & 1) continue;
         }
-        const int row = rt * ROWS + r, i = row / plan.group;
-        Piece<T, D, NT, MT>::template write_row<T>(
-            a, ((int64_t)b * a.T_q + i) * a.H_q + join.y * plan.group + row - i * plan.group, PER * lane,
-            make_float4(o[0], o[1], o[2], o[3]), M, DM, L);
+        write_row<T>(a, output_row(a, plan, b, join.y, rt, r), PER * lane, make_float4(o[0], o[1], o[2], o[3]), M, DM,
+                     L);
     }
 }
 
@@ -896,26 +715,33 @@ auto by_shape(const CacheAttention& a, bool bf16, F f) {
     return padded_d(a) == 64 ? by_rows<float, 64>(a, f) : by_rows<float, 128>(a, f);
 }
 
-// CTAs of the shared-out form; 0 where each item is one CTA's.
 template <typename S>
-int64_t share_grid(const CacheAttention& a, int num_sms) {
-    const int64_t row_tiles = (rows_of(a) + S::ROWS - 1) / S::ROWS;
+Plan make_plan(const CacheAttention& a) {
+    Plan plan = {};
+    plan.group = a.H_q / a.H_kv;
+    plan.rows = rows_of(a);
+    plan.tile_rows = S::ROWS;
+    plan.row_tiles = (plan.rows + S::ROWS - 1) / S::ROWS;
+    plan.stored = plan.rows < S::ROWS ? plan.rows : S::ROWS;
+    plan.item_cost = S::ITEM_COST;
+    plan.cut = 1;
+    return plan;
+}
+
+// CTAs of the shared-out form; 0 where each item is one CTA's.
+int64_t share_grid(const CacheAttention& a, const Plan& plan, int64_t most) {
     const int64_t cap = ((int64_t)a.table_pages << a.page_shift) / kStep;
-    if (cap <= kMinShare || a.B * row_tiles > kMaxScan) return 0;
-    const int64_t all = a.B * row_tiles * a.H_kv * (cap + S::ITEM_COST);
-    const int64_t most = (int64_t)num_sms * S::CTAS, useful = (all + kMinShare - 1) / kMinShare;
+    if (cap <= kMinShare || (int64_t)a.B * plan.row_tiles > kMaxScan) return 0;
+    const int64_t all = (int64_t)a.B * plan.row_tiles * a.H_kv * (cap + plan.item_cost);
+    const int64_t useful = (all + kMinShare - 1) / kMinShare;
     return useful < most ? useful : most;
 }
 
 template <typename T, int D, int NT, int MT>
-cudaError_t launch(const CacheAttention& a, void* workspace, cudaStream_t stream, int num_sms) {
+cudaError_t launch(Shape<T, D, NT, MT>, const CacheAttention& a, void* workspace, cudaStream_t stream, int num_sms) {
     using S = Shape<T, D, NT, MT>;
-    Plan plan = {};
-    plan.group = a.H_q / a.H_kv;
-    plan.rows = rows_of(a);
-    plan.row_tiles = (plan.rows + S::ROWS - 1) / S::ROWS;
-    plan.stored = plan.rows < S::ROWS ? plan.rows : S::ROWS;
-    const int64_t grid = share_grid<S>(a, num_sms);
+    Plan plan = make_plan<S>(a);
+    const int64_t grid = share_grid(a, plan, (int64_t)num_sms * S::CTAS);
     if (grid == 0) {
         const int64_t items = (int64_t)a.B * plan.row_tiles * a.H_kv;
         cudaError_t e = cudaFuncSetAttribute(attention_whole_kernel<T, D, NT, MT>,
@@ -924,18 +750,19 @@ cudaError_t launch(const CacheAttention& a, void* workspace, cudaStream_t stream
         attention_whole_kernel<T, D, NT, MT><<<(unsigned)items, kThreads, S::SMEM, stream>>>(a, plan);
         return cudaGetLastError();
     }
-    const int64_t slots = grid * 2 * plan.stored;
-    plan.joins = static_cast<int4*>(workspace);
-    plan.stats = reinterpret_cast<float4*>(plan.joins + grid);
-    plan.sums = reinterpret_cast<float*>(plan.stats + slots);
+    set_attention_pieces(plan, workspace, grid);
     cudaError_t e = cudaFuncSetAttribute(attention_share_kernel<T, D, NT, MT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
     attention_share_kernel<T, D, NT, MT><<<(unsigned)grid, kThreads, S::SMEM, stream>>>(a, plan);
     e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    // The second kernel's CTAs come up while the first ends, and wait for it.  A
-    // row a CTA where the items are so few that each ends in many pieces.
+    return e != cudaSuccess ? e : run_attention_join(a, plan, sizeof(T) == 2, D, grid, stream);
+}
+
+template <typename T, int D>
+cudaError_t launch_join(const CacheAttention& a, const Plan& plan, int64_t grid, cudaStream_t stream) {
+    // Its CTAs come up while the kernel before ends, and wait for it.  A row a CTA
+    // where the items are so few that each ends in many pieces.
     const bool many = grid > kJoinFew * (int64_t)a.B * plan.row_tiles * a.H_kv;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, (unsigned)(many ? plan.stored : (plan.stored + 7) / 8));
@@ -946,15 +773,28 @@ cudaError_t launch(const CacheAttention& a, void* workspace, cudaStream_t stream
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, D, NT, MT>, a, plan);
-}
-
-template <typename T, int D, int NT, int MT>
-cudaError_t launch(Shape<T, D, NT, MT>, const CacheAttention& a, void* ws, cudaStream_t stream, int num_sms) {
-    return launch<T, D, NT, MT>(a, ws, stream, num_sms);
+    return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, D>, a, plan);
 }
 
 }  // namespace
+
+size_t attention_piece_bytes(int64_t grid, int stored, int D) {
+    return (size_t)grid * (sizeof(int4) + 2 * (size_t)stored * (sizeof(float4) + D * sizeof(float)));
+}
+
+void set_attention_pieces(attn::Plan& plan, void* workspace, int64_t grid) {
+    plan.joins = static_cast<int4*>(workspace);
+    plan.stats = reinterpret_cast<float4*>(plan.joins + grid);
+    plan.sums = reinterpret_cast<float*>(plan.stats + grid * 2 * plan.stored);
+}
+
+cudaError_t run_attention_join(const CacheAttention& a, const attn::Plan& plan, bool bf16, int D, int64_t grid,
+                               cudaStream_t stream) {
+    if (bf16)
+        return D == 64 ? launch_join<__nv_bfloat16, 64>(a, plan, grid, stream)
+                       : launch_join<__nv_bfloat16, 128>(a, plan, grid, stream);
+    return D == 64 ? launch_join<float, 64>(a, plan, grid, stream) : launch_join<float, 128>(a, plan, grid, stream);
+}
 
 size_t cache_attention_workspace_bytes(const CacheAttention& a, int num_sms) {
     // the larger of what the two types of query need
@@ -962,9 +802,14 @@ size_t cache_attention_workspace_bytes(const CacheAttention& a, int num_sms) {
     for (int bf16 = 0; bf16 < 2; ++bf16) {
         const size_t need = by_shape(a, bf16 != 0, [&](auto shape) -> size_t {
             using S = decltype(shape);
-            const int64_t stored = rows_of(a) < S::ROWS ? rows_of(a) : S::ROWS;
-            return (size_t)share_grid<S>(a, num_sms) * (16 + 2 * stored * (16 + padded_d(a) * 4));
+            const Plan plan = make_plan<S>(a);
+            return attention_piece_bytes(share_grid(a, plan, (int64_t)num_sms * S::CTAS), plan.stored, padded_d(a));
         });
+        most = need > most ? need : most;
+    }
+    if (attention_tc_takes(a, true)) {
+        const Plan plan = attention_tc_plan(a);
+        const size_t need = attention_piece_bytes(attention_tc_grid(a, plan, num_sms), plan.stored, 128);
         most = need > most ? need : most;
     }
     return most;
@@ -972,6 +817,7 @@ size_t cache_attention_workspace_bytes(const CacheAttention& a, int num_sms) {
 
 cudaError_t run_cache_attention(const CacheAttention& a, bool bf16, void* workspace, cudaStream_t stream,
                                 int num_sms) {
+    if (attention_tc_takes(a, bf16)) return run_attention_tc(a, workspace, stream, num_sms);
     return by_shape(a, bf16, [&](auto shape) { return launch(shape, a, workspace, stream, num_sms); });
 }
 

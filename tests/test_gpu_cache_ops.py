@@ -378,6 +378,93 @@ def test_attention_extreme_queries():
     assert bool(torch.isnan(o[0, 3, 0]).all()) and bool(torch.isfinite(o[0, 3, 1]).all())
 
 
+@pytest.mark.parametrize("B, T_q, hq, hk, d, page, lengths", [
+    (1, 8, 4, 1, 128, 64, [100]), (1, 17, 1, 1, 128, 16, [17]), (2, 5, 8, 2, 80, 32, [128, 129]),
+    (3, 9, 6, 2, 96, 16, [0, 3, 300]), (1, 16, 8, 2, 112, 128, [1000]), (2, 33, 2, 1, 128, 64, [33, 500]),
+    (1, 3, 130, 1, 128, 256, [257]), (1, 70, 3, 1, 128, 16, [70]), (2, 20, 4, 4, 128, 32, [127, 641]),
+])
+def test_attention_many_rows(B, T_q, hq, hk, d, page, lengths):
+    """More than 16 rows a head, bf16, wide heads: the kernel whose codes are operands as they lie."""
+    _run_and_check(*_setup(sum(lengths) + d + hq, B, T_q, hq, hk, d, page, lengths, BF16))
+
+
+@pytest.mark.parametrize("window, sinks", [(1, 1), (16, 4), (100, 17), (129, 0), (64, 300), (1000, 3)])
+def test_attention_many_rows_window(window, sinks):
+    _run_and_check(*_setup(window + sinks, 2, 12, 4, 2, 128, 16, [12, 777], BF16), window=window, sinks=sinks)
+
+
+def test_attention_many_rows_long():
+    q, cache, table, lengths = _setup(31, 2, 8, 4, 1, 128, 64, [9001, 4096], BF16)
+    _run_and_check(q, cache, table, lengths)
+    _run_and_check(q, cache, table, lengths, window=5000, sinks=5)
+
+
+def test_attention_many_rows_many_sequences():
+    lengths = [(i * 37) % 300 for i in range(50)]
+    q, cache, table, _ = _setup(32, 50, 6, 6, 2, 128, 16, lengths, BF16, wide=60)
+    _run_and_check(q, cache, table, _int32(lengths))
+
+
+def test_attention_many_rows_pages_not_held():
+    q, cache, table, lengths = _setup(33, 3, 9, 4, 2, 128, 16, [700, 64, 40], BF16)
+    table[0, 3:9] = -1
+    table[0, 20:36] = cache.k.shape[0]
+    table[1] = -1
+    table[2, 2] = -1
+    o, lse = _run_and_check(q, cache, table, lengths)
+    assert not bool(o[1].any()) and bool((lse[1] == -math.inf).all())
+    _run_and_check(q, cache, table, lengths, window=60, sinks=20)
+
+
+def test_attention_many_rows_unseen_nan():
+    q, cache, table, lengths = _setup(34, 1, 12, 4, 2, 128, 16, [300], BF16)
+    nan = torch.full((1, 1, 2, 128), math.nan, device="cuda")
+    one = torch.randn(1, 1, 2, 128, generator=_gen(1)).cuda()
+    value_nan = one.clone()
+    value_nan[..., 5] = math.nan
+    value_nan[..., 100] = math.nan
+    kda.cache_write(cache, one, value_nan, table, _int32([294]))         # seen from row 6 on: two channels
+    kda.cache_write(cache, nan, one, table, _int32([297]))               # seen from row 9 on: the whole row
+    o, lse = _run_and_check(q, cache, table, lengths)
+    assert not bool(torch.isnan(o[:, :6]).any()) and bool(torch.isnan(o[:, 9:]).all())
+    assert bool(torch.isnan(o[:, 6:9, :, [5, 100]]).all()) and not bool(torch.isnan(o[:, 6:9, :, 6:100]).any())
+    q, cache, table, lengths = _setup(35, 1, 12, 4, 2, 128, 16, [300], BF16)
+    kda.cache_write(cache, one, value_nan, table, _int32([275]))         # leaves the window from row 7 on
+    o, _ = _run_and_check(q, cache, table, lengths, window=20, sinks=2)
+    assert bool(torch.isnan(o[:, :7, :, 5]).all()) and not bool(torch.isnan(o[:, 7:]).any())
+    q[0, 3, 1, 7] = math.nan
+    o = kda.cache_attention(q, cache, table, lengths)
+    assert bool(torch.isnan(o[0, 3, 1]).all()) and not bool(torch.isnan(o[0, :, 0, 6:100]).any())
+
+
+@pytest.mark.parametrize("factor", [1.0, 40.0, 1e-3])
+def test_attention_many_rows_uneven_scales(factor):
+    g = _gen(36)
+    heads, d, page, T = 2, 128, 16, 320
+    cache, table = kda.cache_new(20, heads, page, d), _table(g, 1, 20, 20).cuda()
+    size = torch.exp2(3.0 * torch.randperm(20, generator=g) - 30.0).repeat_interleave(page)[None, :, None, None]
+    k, v = (torch.randn(1, T, heads, d, generator=g) for _ in range(2))
+    kda.cache_write(cache, k.cuda(), (v * size).cuda(), table, _int32([0]))
+    q = (torch.randn(1, 10, 4, d, generator=g) * factor).to(BF16).cuda()
+    _run_and_check(q, cache, table, _int32([T]))
+    kda.cache_write(cache, (k * size.sqrt()).cuda(), v.cuda(), table, _int32([0]))
+    _run_and_check(q, cache, table, _int32([T]), scale=1e-4)
+
+
+def test_attention_many_rows_in_a_row():
+    """The same call three times over other work, with strided queries and a workspace of garbage: the same bits."""
+    q, cache, table, lengths = _setup(37, 3, 11, 8, 2, 128, 32, [700, 90, 2000], BF16)
+    want, want_lse = _run_and_check(q, cache, table, lengths)
+    qkv = torch.randn(3, 11, 12 * 128, device="cuda").to(BF16)
+    view = qkv[..., : 8 * 128].unflatten(-1, (8, 128))
+    view.copy_(q)
+    need = kda.cache_attention_workspace_size(3, 11, 8, 2, 128, 32, table.shape[1])
+    ws = torch.full((max(need, 1),), 0xFF, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        o, lse = kda.cache_attention(view, cache, table, lengths, workspace=ws, return_lse=True)
+        assert torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
 def test_attention_strides_streams_and_buffers():
     q, cache, table, lengths = _setup(16, 2, 3, 8, 2, 64, 32, [700, 90], BF16)
     want, want_lse = kda.cache_attention(q, cache, table, lengths, return_lse=True)
