@@ -42,7 +42,7 @@ constexpr int kTileSteps = kTokens / kStep;
 constexpr int kHalf = kTokens * 128;       // bytes of a tile's keys, or values
 constexpr int kSlots = 5;
 constexpr int kSoftmax = 256;              // threads of warps 0-7; then the loaders', and the issuer's warp
-constexpr int kLoaders = 64;
+constexpr int kLoaders = 64;               // eight rows at a time
 constexpr int kThreads = kSoftmax + 128;   // (whole warpgroups, for setmaxnreg: the last warp has no role)
 constexpr int kIssuerWarp = (kSoftmax + kLoaders) / 32;
 // Registers: 80 a thread at launch, then 96 for softmax and 40 for the others: 256 x 96 + 128 x 40 <= 384 x 80.
@@ -171,7 +171,8 @@ struct Loader {
         const int r = tid >> 3, chunk = tid & 7;           // row 0 .. 7 of a step (and 8 on), 16-byte piece of it
         const int32_t* table = a.table + (int64_t)(pair / c.plan.row_tiles) * a.table_pages;
         const int page_mask = (1 << a.page_shift) - 1;
-        const int lane_off = r * a.d + chunk * 16;
+        const bool in_row = chunk * 16 < a.d;
+        const int lane_off = r * a.d + chunk * 16, eight_rows = in_row ? 8 * a.d : 0;
         const uint32_t lane_to = r * 128 + ((chunk ^ r) << 4);
         // Lane k < 8: where step k of the tile at step s0 is in the pool, and how many of its tokens exist.
         auto page_of = [&](int s0) -> int {
@@ -186,7 +187,7 @@ struct Loader {
             const int64_t block = (int64_t)id * a.H_kv + hk;
             const int64_t off = held ? ((block << a.page_shift) + (t0 & page_mask)) * a.d : 0;
             const int n = held ? (tile.end - t0 < kStep ? tile.end - t0 : kStep) : 0;
-            const bool whole = a.d == 128 && __all_sync(0xffffffffu, n == kStep || lane >= kTileSteps);
+            const bool whole = __all_sync(0xffffffffu, n == kStep || lane >= kTileSteps);
             int64_t offs[kTileSteps];
 #pragma unroll
             for (int k = 0; k < kTileSteps; ++k) offs[k] = __shfl_sync(0xffffffffu, off, k) + lane_off;
@@ -202,20 +203,17 @@ struct Loader {
                 if (whole) {
 #pragma unroll
                     for (int k = 0; k < kTileSteps; ++k) {
-                        const uint8_t* src = codes + offs[k];
-#pragma unroll
-                        for (int up = 0; up < kStep; up += kLoaders / 8)
-                            copy_async(to_s + (k * kStep + up) * 128, src + up * 128, true);
+                        const uint8_t* src = in_row ? codes + offs[k] : codes;
+                        copy_async(to_s + k * kStep * 128, src, in_row);
+                        copy_async(to_s + (k * kStep + 8) * 128, src + eight_rows, in_row);
                     }
                 } else {
 #pragma unroll
                     for (int k = 0; k < kTileSteps; ++k) {
-                        const int n_all = __shfl_sync(0xffffffffu, n, k), n_k = chunk * 16 < a.d ? n_all : 0;
-#pragma unroll
-                        for (int up = 0; up < kStep; up += kLoaders / 8) {
-                            const bool real = r + up < n_k;
-                            copy_async(to_s + (k * kStep + up) * 128, real ? codes + offs[k] + up * a.d : codes, real);
-                        }
+                        const int n_all = __shfl_sync(0xffffffffu, n, k), n_k = in_row ? n_all : 0;
+                        copy_async(to_s + k * kStep * 128, r < n_k ? codes + offs[k] : codes, r < n_k);
+                        copy_async(to_s + (k * kStep + 8) * 128, r + 8 < n_k ? codes + offs[k] + eight_rows : codes,
+                                   r + 8 < n_k);
                     }
                 }
                 if (tid < kTileSteps) {
@@ -300,8 +298,8 @@ struct Issuer {
 struct Softmax {
     Cta c;
     int tile_n = 0;
-    bool bad = false;                      // a wait of this thread gave up
-    bool dead = false;                     // some thread's did: the same in all
+    bool bad = false;                      // a wait of this thread gave up: it waits no more, its numbers are none
+    bool dead = false;                     // some thread's did, as found at the piece's end: the same in all
 
     __device__ __forceinline__ void wait(uint64_t* b, uint32_t parity) {
         if (!bad && !dead && !tc::mbar_wait(b, parity)) bad = true;
@@ -400,35 +398,35 @@ struct Softmax {
 #pragma unroll
         for (int r = 0; r < kMine; ++r) se[r] = s[r] + e;
         rows->part_e[quarter][r0 + (lane >> 1)] = reduce_rows(se, most);
+        const float m = rows->m[lane], dm = first ? 0.0f : rows->dm[lane];   // read by all before any writes
+        const uint32_t unset_rows = first ? 0xffffffffu : rows->unset;
         tc::named_bar_sync(kBarVote, kSoftmax);
-        if (threadIdx.x < kRows) {
-            float top = rows->part[0][lane], top_e = rows->part_e[0][lane];
+        // Every warp works out all rows, a lane a row, and writes the same: no warp waits for another's.
+        float top = rows->part[0][lane], top_e = rows->part_e[0][lane];
 #pragma unroll
-            for (int w = 1; w < 4; ++w) {
-                top = fmaxf(top, rows->part[w][lane]);
-                top_e = fmaxf(top_e, rows->part_e[w][lane]);
-            }
-            // relative to the old m: the new one is m + up, above it unless no score has set it yet
-            const float m = rows->m[lane], dm = first ? 0.0f : rows->dm[lane];
-            const bool unset = first || (rows->unset >> lane & 1), seen = top != -INFINITY;
-            const float up = unset ? (seen ? top : 0.0f) : fmaxf(top, 0.0f);
-            const float dm_new = unset ? (seen ? up - top_e : 0.0f) : up - fmaxf(-dm, top_e);
-            rows->m[lane] = m + up;
-            rows->dm[lane] = dm_new;
-            rows->up[lane] = up;
-            rows->lift[lane] = ex2(dm_new + kBits);
-            rows->keep_l[lane] = unset ? 1.0f : ex2(-up);
-            rows->keep_o[lane] = unset ? 1.0f : ex2(dm_new - dm - up);
-            const uint32_t still = __ballot_sync(0xffffffffu, unset && !seen);
-            float most_dm = dm_new;
-#pragma unroll
-            for (int w = 16; w > 0; w >>= 1) most_dm = fmaxf(most_dm, __shfl_xor_sync(0xffffffffu, most_dm, w));
-            if (lane == 0) {
-                rows->dm_most = most_dm;
-                rows->unset = still;
-            }
+        for (int w = 1; w < 4; ++w) {
+            top = fmaxf(top, rows->part[w][lane]);
+            top_e = fmaxf(top_e, rows->part_e[w][lane]);
         }
-        tc::named_bar_sync(kBarVote, kSoftmax);
+        // relative to the old m: the new one is m + up, above it unless no score has set it yet
+        const bool unset = unset_rows >> lane & 1, seen = top != -INFINITY;
+        const float up = unset ? (seen ? top : 0.0f) : fmaxf(top, 0.0f);
+        const float dm_new = unset ? (seen ? up - top_e : 0.0f) : up - fmaxf(-dm, top_e);
+        rows->m[lane] = m + up;
+        rows->dm[lane] = dm_new;
+        rows->up[lane] = up;
+        rows->lift[lane] = ex2(dm_new + kBits);
+        rows->keep_l[lane] = unset ? 1.0f : ex2(-up);
+        rows->keep_o[lane] = unset ? 1.0f : ex2(dm_new - dm - up);
+        const uint32_t still = __ballot_sync(0xffffffffu, unset && !seen);
+        float most_dm = dm_new;
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) most_dm = fmaxf(most_dm, __shfl_xor_sync(0xffffffffu, most_dm, w));
+        if (lane == 0) {
+            rows->dm_most = most_dm;
+            rows->unset = still;
+        }
+        __syncwarp();
 #pragma unroll
         for (int r = 0; r < kMine; ++r) s[r] -= rows->up[r0 + r];
         if (first) return;                                 // nothing summed yet
@@ -516,13 +514,7 @@ struct Softmax {
                         if ((unset >> r & 1) && s[r] != -INFINITY) beyond = INFINITY;
                 }
             }
-            if (vote(bad || beyond > kFar || i == 0)) {
-                if (vote(bad)) {
-                    dead = true;
-                    continue;
-                }
-                move_references(s, e, l, r0, i == 0);
-            }
+            if (vote(beyond > kFar || i == 0)) move_references(s, e, l, r0, i == 0);
             if (i > 0) wait(&c.bar->pv_done, (n - 1) & 1);   // the weights before have been read
 
             // Weights: the pieces of 16 rows are 16 bytes each.
@@ -699,7 +691,7 @@ attn::Plan attention_tc_plan(const CacheAttention& a) {
     plan.tile_rows = kRows;
     plan.row_tiles = (plan.rows + kRows - 1) / kRows;
     plan.stored = plan.rows < kRows ? plan.rows : kRows;
-    plan.item_cost = 3 * kTileSteps;
+    plan.item_cost = 8 * kTileSteps;
     plan.cut = kTileSteps;
     return plan;
 }
