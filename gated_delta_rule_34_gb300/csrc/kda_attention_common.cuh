@@ -47,10 +47,15 @@ struct Tile {
 
 __device__ __forceinline__ Tile make_tile(const CacheAttention& a, const Plan& plan, int len, int rt) {
     Tile t;
-    const int r0 = rt * plan.tile_rows;
-    const int r1 = (plan.rows < r0 + plan.tile_rows ? plan.rows : r0 + plan.tile_rows) - 1;
-    t.p0 = len - a.T_q + r0 / plan.group;
-    t.p1 = len - a.T_q + r1 / plan.group;
+    if (plan.row_tiles == 1) {                             // no division on the way to a decode step's first loads
+        t.p0 = len - a.T_q;
+        t.p1 = len - 1;
+    } else {
+        const int r0 = rt * plan.tile_rows;
+        const int r1 = (plan.rows < r0 + plan.tile_rows ? plan.rows : r0 + plan.tile_rows) - 1;
+        t.p0 = len - a.T_q + r0 / plan.group;
+        t.p1 = len - a.T_q + r1 / plan.group;
+    }
     t.end = t.p1 + 1 > 0 ? t.p1 + 1 : 0;
     int lo = 0, sink_end = 0;
     if (a.window > 0) {
@@ -79,6 +84,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 // The tile of pair (sequence, row tile).
 __device__ __forceinline__ Tile tile_of(const CacheAttention& a, const Plan& plan, int pair) {
+    if (plan.row_tiles == 1) return make_tile(a, plan, length_of(a, pair), 0);
     return make_tile(a, plan, length_of(a, pair / plan.row_tiles), pair % plan.row_tiles);
 }
 
@@ -148,7 +154,8 @@ __device__ __forceinline__ Share find_share(const CacheAttention& a, const Plan&
     if (s.begin >= before && s.begin < before + mine * a.H_kv) {
         int64_t base = before;
         for (int q = q0; q < pairs; ++q) {
-            const int64_t w = (int64_t)a.H_kv * (tile_of(a, plan, q).steps + plan.item_cost);
+            // (its only pair: the one that its sum says)
+            const int64_t w = each == 1 ? mine * a.H_kv : (int64_t)a.H_kv * (tile_of(a, plan, q).steps + plan.item_cost);
             if (s.begin < base + w) {
                 found_pair = q;
                 found_base = base;

@@ -210,7 +210,7 @@ cache_write_kernel(CacheSpan w, const T* __restrict__ k, int64_t k_stride, const
         if constexpr (GROUP > 1) __syncthreads();
         amax = over_all([](const uint4 (&raw)[sizeof(T)], float m) { return unit_finite_amax<T>(raw, m); });
     }
-    const float s = fmaxf(page_scale(amax), old);
+    const float s = fmaxf(page_scale(amax), pow2_ceil(old));   // (old may be a caller's own, no power of two)
     const float inv = pow2_inverse(s);
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {

@@ -25,13 +25,14 @@ __device__ __forceinline__ float page_scale(float amax) {
     e = e < kScaleMinExp ? kScaleMinExp : e;
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
-// A page's scale as read back: 0 if it is none that page_scale gives (a page
-// that was never written), whose codes then count for nothing.
+// A page's scale as read back, if it is positive and in the range that page_scale gives;
+// else 0 (a page that was never written), whose codes then count for nothing.
 __device__ __forceinline__ float valid_scale(float s) {
-    const uint32_t bits = __float_as_uint(s);
-    const bool valid = (bits & 0x807fffffu) == 0 && bits >= (uint32_t)(127 + kScaleMinExp) << 23 &&
-                       bits <= (127u + 120u) << 23;
-    return valid ? s : 0.0f;
+    return s >= 7.888609052210118e-31f && s <= 1.329227995784916e36f ? s : 0.0f;   // 2^-100, 2^120
+}
+// The least power of two that is no less.
+__device__ __forceinline__ float pow2_ceil(float s) {
+    return __uint_as_float((__float_as_uint(s) + 0x7fffffu) & 0xff800000u);
 }
 // 1 / s of a power of two in [2^-126, 2^126].
 __device__ __forceinline__ float pow2_inverse(float s) {

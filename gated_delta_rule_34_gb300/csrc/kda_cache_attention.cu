@@ -114,15 +114,16 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 
 // The sizes that go together: a warp takes NT tiles of 8 rows; MT warps share
 // the tokens of their 8 NT MT rows; NG groups of them take steps in turn, each with a
-// ring of STAGES steps.  The more rows a warp has, the fewer warps' registers an SM holds.
+// ring of STAGES steps.  The more rows a warp has, the fewer warps' registers an SM holds.  (Four CTAs
+// and three stages with one tile of rows: a million tokens 369 us, against 359 us with three and four.)
 template <typename T, int D, int NT_, int MT_>
 struct Shape {
     static constexpr int NT = NT_, MT = MT_;
     static constexpr int PIECES = sizeof(T) == 4 ? 2 : 1;   // fp16 pieces of a query and a weight
     static constexpr int NG = kWarps / MT;
     static constexpr int ROWS = 8 * NT * MT;
-    static constexpr int CTAS = PIECES == 1 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2) : (NT == 1 ? 3 : 2);   // resident a SM
-    static constexpr int STAGES = MT == 1 ? (CTAS == 4 ? 3 : NT == 4 ? 6 : 4) : MT == 2 ? 6 : 8;
+    static constexpr int CTAS = PIECES == 1 ? (NT == 4 ? 2 : 3) : (NT == 1 ? 3 : 2);   // resident a SM
+    static constexpr int STAGES = MT == 1 ? (NT == 4 ? 6 : 4) : MT == 2 ? 6 : 8;
     static constexpr int ITEM_COST = NT == 4 ? 32 : 12;     // what an item's start and end cost, in steps
     static constexpr bool Q_HELD = NT <= 2;           // queries in registers, or read again at every step
     static constexpr int KC = D / 64;                 // 16-byte pieces of a key that a lane reads
@@ -395,7 +396,9 @@ struct Piece {
                         }
                     }
             }
-            const float e = (float)((int)(__float_as_uint(scales.y) >> 23) - 127);   // log2 of v's scale
+            // log2 of v's scale: its exponent, and what remains (1 for the powers of two that cache writes give)
+            const float e = (float)((int)(__float_as_uint(scales.y) >> 23) - 127);
+            const float mantissa = __uint_as_float((__float_as_uint(scales.y) & 0x7fffffu) | 0x3f800000u);
             // x = score - m, in powers of two
             float x[NT][4];
 #pragma unroll
@@ -451,7 +454,7 @@ struct Piece {
             for (int n = 0; n < NT; ++n) {
                 float lift[2];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) lift[r] = ex2(fminf(dm[n][r] + (e + kWeightBits), 126.0f));
+                for (int r = 0; r < 2; ++r) lift[r] = ex2(fminf(dm[n][r] + (e + kWeightBits), 126.0f)) * mantissa;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float p0 = ex2(x[n][2 * h]), p1 = ex2(x[n][2 * h + 1]);
@@ -699,15 +702,20 @@ int rows_of(const CacheAttention& a) { return a.T_q * (a.H_q / a.H_kv); }
 int padded_d(const CacheAttention& a) { return a.d <= 64 ? 64 : 128; }
 
 // Calls f with the shape for these queries: as many rows a warp as registers allow
-// before warps have to share tokens.
+// before warps have to share tokens.  (More than 16 bf16 rows of more than 64 channels
+// are the other kernel's: attention_tc_takes.)
 template <typename T, int D, typename F>
 auto by_rows(const CacheAttention& a, F f) {
-    constexpr int MOST = sizeof(T) == 4 ? 2 : 4;
     const int rows = rows_of(a);
     if (rows <= 8) return f(Shape<T, D, 1, 1>{});
-    if (rows <= 16) return f(Shape<T, D, 2, 1>{});
-    if (rows <= 32) return f(Shape<T, D, MOST, 4 / MOST>{});
-    return f(Shape<T, D, MOST, 8 / MOST>{});
+    if constexpr (sizeof(T) == 2 && D == 128) {
+        return f(Shape<T, D, 2, 1>{});
+    } else {
+        constexpr int MOST = sizeof(T) == 4 ? 2 : 4;
+        if (rows <= 16) return f(Shape<T, D, 2, 1>{});
+        if (rows <= 32) return f(Shape<T, D, MOST, 4 / MOST>{});
+        return f(Shape<T, D, MOST, 8 / MOST>{});
+    }
 }
 template <typename F>
 auto by_shape(const CacheAttention& a, bool bf16, F f) {

@@ -403,7 +403,8 @@ kda_status kda_spec_commit(const void *k, const void *v, const void *z, const vo
  *                     see its tokens.  So are positions past the table.
  * A scale is the least power of two, at least 2^-100, that brings every finite
  * value of the page's tokens to 448 or less.  Pages start out with any
- * contents; writing a page's first token starts its scale anew.
+ * contents; writing a page's first token starts its scale anew.  Pages that
+ * a caller filled itself may have any scales in [2^-100, 2^120].
  */
 
 /* Which channels of a head make a pair: (i, i + rot/2) or (2i, 2i + 1). */
@@ -483,7 +484,8 @@ kda_status kda_cache_read(const void *k_codes, const void *v_codes, const float 
  * Scores, sums and outputs are fp32 until the one rounding to dtype.  Weights
  * meet the values as fp16 numbers (two of them, 22 bits, where dtype is fp32) relative
  * to the row's largest w_t times its page's scale of v: what lies below 2^-36 of
- * that is lost.
+ * that is lost (below 2^-30 with more than 16 bf16 rows a head, T_q * H_q / H_kv, of
+ * more than 64 channels, whose products take the codes as they are).
  */
 kda_status kda_cache_attention(const void *q, int64_t q_stride, const void *k_codes,
                                const void *v_codes, const float *k_scale, const float *v_scale,
