@@ -23,7 +23,7 @@
 //               the rows into 128-byte-swizzled rows, zeros where there is no token
 //   1 issuer    the score product of the next tile, then the value product of this one
 // The maximum m and the reference of v's sums (kept as dm) are common to the CTA and move only when a
-// score passes them by more than a factor of 128, which a vote of the softmax warps tells; the sums in
+// score passes them by more than a factor of 128, which a vote of the four warps of its row tells; the sums in
 // TMEM are then multiplied in place.  (A move costs some 3000 cycles; with a factor of 4 every third tile had one.)
 //
 // NaN that a row does not see (0 times NaN is NaN): see Softmax::mend_values.  A wait that gives up
@@ -51,7 +51,8 @@ constexpr int kMine = kRows / 2;           // rows of a softmax thread
 constexpr float kBits = 8.0f, kFar = 7.0f;    // log2 of the largest weight at its reference, and of how far above it
 constexpr float kToPlan = 16.0f;           // 2^(kWeightBits - kBits)
 constexpr int kCtas = 2;                   // a SM
-constexpr int kBarVote = 1;                // named barrier of the softmax warps
+constexpr int kBarSoftmax = 1;             // named barriers: of all softmax warps,
+constexpr int kBarHalf = 2;                // and (2 and 3) of the four that have the same 16 rows
 
 // Shared memory, from a 1024-byte boundary.
 constexpr int kRingAt = 0;
@@ -68,8 +69,8 @@ struct alignas(16) Rows {
     float lift[kRows];                     // 2^(dm + kWeightBits)
     float up[kRows];                       // by how much a reference moved,
     float keep_o[kRows], keep_l[kRows];    // and what that multiplies the sums by
-    float dm_most;                         // the largest dm
-    uint32_t unset;                        // rows that have seen no score yet, a bit each: m = 0 is none of theirs
+    float dm_most[4];                      // of each 16 rows: the largest dm,
+    uint32_t unset[4];                     // and those that have seen no score yet, a bit each: m = 0 is none of theirs
     float part[4][kRows], part_e[4][kRows];
     uint32_t nan[kRows][4];                // channels whose output is NaN, a bit each
 };
@@ -98,8 +99,8 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, 
         : "memory");
 }
 
-// Whether any of the softmax warps' threads says yes.
-__device__ __forceinline__ bool vote(bool yes) {
+// Whether any of the `count` threads at barrier `id` says yes.
+__device__ __forceinline__ bool vote(bool yes, uint32_t id, uint32_t count) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
@@ -107,7 +108,7 @@ __device__ __forceinline__ bool vote(bool yes) {
         "bar.red.or.pred q, %2, %3, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)yes), "n"(kBarVote), "n"(kSoftmax)
+        : "r"((uint32_t)yes), "r"(id), "r"(count)
         : "memory");
     return r != 0;
 }
@@ -398,33 +399,34 @@ struct Softmax {
 #pragma unroll
         for (int r = 0; r < kMine; ++r) se[r] = s[r] + e;
         rows->part_e[quarter][r0 + (lane >> 1)] = reduce_rows(se, most);
-        const float m = rows->m[lane], dm = first ? 0.0f : rows->dm[lane];   // read by all before any writes
-        const uint32_t unset_rows = first ? 0xffffffffu : rows->unset;
-        tc::named_bar_sync(kBarVote, kSoftmax);
-        // Every warp works out all rows, a lane a row, and writes the same: no warp waits for another's.
-        float top = rows->part[0][lane], top_e = rows->part_e[0][lane];
+        const int half = r0 / kMine, row = r0 + (lane & 15);
+        const float m = rows->m[row], dm = first ? 0.0f : rows->dm[row];     // read by all before any writes
+        const uint32_t unset_rows = first ? 0xffffu : rows->unset[half];
+        tc::named_bar_sync(kBarHalf + half, kSoftmax / 2);
+        // Every warp works out its 16 rows, a lane a row, and writes the same: no warp waits for another's.
+        float top = rows->part[0][row], top_e = rows->part_e[0][row];
 #pragma unroll
         for (int w = 1; w < 4; ++w) {
-            top = fmaxf(top, rows->part[w][lane]);
-            top_e = fmaxf(top_e, rows->part_e[w][lane]);
+            top = fmaxf(top, rows->part[w][row]);
+            top_e = fmaxf(top_e, rows->part_e[w][row]);
         }
         // relative to the old m: the new one is m + up, above it unless no score has set it yet
-        const bool unset = unset_rows >> lane & 1, seen = top != -INFINITY;
+        const bool unset = unset_rows >> (lane & 15) & 1, seen = top != -INFINITY;
         const float up = unset ? (seen ? top : 0.0f) : fmaxf(top, 0.0f);
         const float dm_new = unset ? (seen ? up - top_e : 0.0f) : up - fmaxf(-dm, top_e);
-        rows->m[lane] = m + up;
-        rows->dm[lane] = dm_new;
-        rows->up[lane] = up;
-        rows->lift[lane] = ex2(dm_new + kBits);
-        rows->keep_l[lane] = unset ? 1.0f : ex2(-up);
-        rows->keep_o[lane] = unset ? 1.0f : ex2(dm_new - dm - up);
-        const uint32_t still = __ballot_sync(0xffffffffu, unset && !seen);
+        rows->m[row] = m + up;
+        rows->dm[row] = dm_new;
+        rows->up[row] = up;
+        rows->lift[row] = ex2(dm_new + kBits);
+        rows->keep_l[row] = unset ? 1.0f : ex2(-up);
+        rows->keep_o[row] = unset ? 1.0f : ex2(dm_new - dm - up);
+        const uint32_t still = __ballot_sync(0xffffffffu, unset && !seen) & 0xffffu;
         float most_dm = dm_new;
 #pragma unroll
-        for (int w = 16; w > 0; w >>= 1) most_dm = fmaxf(most_dm, __shfl_xor_sync(0xffffffffu, most_dm, w));
+        for (int w = 8; w > 0; w >>= 1) most_dm = fmaxf(most_dm, __shfl_xor_sync(0xffffffffu, most_dm, w));
         if (lane == 0) {
-            rows->dm_most = most_dm;
-            rows->unset = still;
+            rows->dm_most[half] = most_dm;
+            rows->unset[half] = still;
         }
         __syncwarp();
 #pragma unroll
@@ -460,11 +462,11 @@ struct Softmax {
         const int b = pair / plan.row_tiles, rt = pair % plan.row_tiles;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         // The products of the piece before have read its queries; all threads have left its rows.
-        tc::named_bar_sync(kBarVote, kSoftmax);
+        tc::named_bar_sync(kBarSoftmax, kSoftmax);
         load_queries(b, hk, rt);
         tc::fence_async_smem();
         tc::mbar_arrive(&c.bar->q_full);
-        tc::named_bar_sync(kBarVote, kSoftmax);
+        tc::named_bar_sync(kBarSoftmax, kSoftmax);
 
         float l[kMine];
 #pragma unroll
@@ -507,14 +509,14 @@ struct Softmax {
 #pragma unroll
             for (int r = 1; r < kMine; ++r) beyond = fmaxf(beyond, s[r]);
             if (i > 0) {
-                beyond += fmaxf(rows->dm_most + e, 0.0f);
-                if (const uint32_t unset = rows->unset >> r0) {
+                beyond += fmaxf(rows->dm_most[half] + e, 0.0f);
+                if (const uint32_t unset = rows->unset[half]) {
 #pragma unroll
                     for (int r = 0; r < kMine; ++r)
                         if ((unset >> r & 1) && s[r] != -INFINITY) beyond = INFINITY;
                 }
             }
-            if (vote(beyond > kFar || i == 0)) move_references(s, e, l, r0, i == 0);
+            if (vote(beyond > kFar || i == 0, kBarHalf + half, kSoftmax / 2)) move_references(s, e, l, r0, i == 0);
             if (i > 0) wait(&c.bar->pv_done, (n - 1) & 1);   // the weights before have been read
 
             // Weights: the pieces of 16 rows are 16 bytes each.
@@ -560,9 +562,9 @@ struct Softmax {
         // The end: the last sums, and the weights' sums over the tokens' threads.
         if (!dead) wait(&c.bar->pv_done, (tile_n - 1) & 1);
         tc::tc_fence_after();
-        if (!dead && vote(bad)) dead = true;
+        if (!dead && vote(bad, kBarSoftmax, kSoftmax)) dead = true;
         rows->part[quarter][r0 + (lane >> 1)] = reduce_rows(l, [](float x, float y) { return x + y; });
-        tc::named_bar_sync(kBarVote, kSoftmax);
+        tc::named_bar_sync(kBarSoftmax, kSoftmax);
         const int rows_here = rows_of_tile(plan, rt);
         const int64_t place = ((int64_t)blockIdx.x * 2 + slot) * plan.stored;
         auto sum_of = [&](int r) {
@@ -571,7 +573,7 @@ struct Softmax {
         if (threadIdx.x < rows_here) {
             const int r = threadIdx.x;
             const float L = sum_of(r);
-            if (!whole) plan.stats[place + r] = make_float4(rows->unset >> r & 1 ? kLowest : rows->m[r], rows->dm[r], L, 0.0f);
+            if (!whole) plan.stats[place + r] = make_float4(rows->unset[r / kMine] >> r % kMine & 1 ? kLowest : rows->m[r], rows->dm[r], L, 0.0f);
             else if (a.lse) a.lse[output_row(a, plan, b, hk, rt, r)] = row_lse(rows->m[r], L);
         }
         float o[16];
