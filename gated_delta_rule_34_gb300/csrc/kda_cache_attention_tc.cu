@@ -6,8 +6,8 @@
 // conversion of every code to fp16.  Here the codes go to the tensor cores as they lie in the
 // cache, as e4m3 operands; what is not 8 bits is split instead:
 //
-//   S^T [128 tokens x 32]  = K [128 x d] q1^T + K q2^T         q = q1 + q2, both e4m3: the 8 bits of a bf16 value, down
-//                                                             to 2^-18 of its row's largest
+//   S^T [128 tokens x 32]  = K [128 x d] (q1 + q2 + q3)^T      e5m2 pieces, which hold the 8 bits of a bf16 value exactly,
+//                                                             down to 2^-30 of its row's largest
 //   O^T [128 channels x 128] += V^T [128 x 128 tokens] (w1 | w2 | w3 | w4)
 //                                                             w = w1 + w2 / 4 + w3 / 16 + w4 / 64, e5m2: a weight in fp16,
 //                                                             cut into the top bytes of what remains of it
@@ -57,10 +57,11 @@ constexpr int kBarHalf = 2;                // and (2 and 3) of the four that hav
 // Shared memory, from a 1024-byte boundary.
 constexpr int kRingAt = 0;
 constexpr int kWeightsAt = kRingAt + kSlots * kHalf;            // [128 tokens][128 columns] e5m2
-constexpr int kQueriesAt = kWeightsAt + kTokens * 128;          // [64][128 channels] e4m3
-constexpr int kScalesAt = kQueriesAt + 2 * kRows * 128;         // [4 tiles][k, v][8 steps]
+constexpr int kQueriesAt = kWeightsAt + kTokens * 128;          // [3 pieces][32][128 channels] e5m2
+constexpr int kScalesAt = kQueriesAt + 3 * kRows * 128;         // [4 tiles][k, v][8 steps]
 constexpr int kRowsAt = kScalesAt + 4 * 2 * kTileSteps * 4;     // Rows
-constexpr int kBarriersAt = kRowsAt + 4096;
+constexpr int kRowsBytes = 2560;
+constexpr int kBarriersAt = kRowsAt + kRowsBytes;
 constexpr int kSmem = kBarriersAt + 256 + 1024;
 
 struct alignas(16) Rows {
@@ -74,7 +75,7 @@ struct alignas(16) Rows {
     float part[4][kRows], part_e[4][kRows];
     uint32_t nan[kRows][4];                // channels whose output is NaN, a bit each
 };
-static_assert(sizeof(Rows) <= 4096, "Rows");
+static_assert(sizeof(Rows) <= kRowsBytes, "Rows");
 
 struct Barriers {
     uint64_t full[kSlots], empty[kSlots], s_full[2], s_free[2], w_full, pv_done, q_full;
@@ -129,6 +130,19 @@ __device__ __forceinline__ float reduce_rows(const float (&v)[kMine], Op op) {
             u[i] = op(up ? u[i + w / 2] : u[i], __shfl_xor_sync(0xffffffffu, up ? u[i] : u[i + w / 2], w));
     }
     return op(u[0], __shfl_xor_sync(0xffffffffu, u[0], 1));
+}
+
+// Four values to e5m2 (nearest) and back: an e5m2 code is the upper byte of an fp16 number.
+__device__ __forceinline__ uint32_t to_e5m2x4(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E5M2);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E5M2);
+    return lo | hi << 16;
+}
+__device__ __forceinline__ void from_e5m2x4(uint32_t four, float* f) {
+    const uint32_t lo = __byte_perm(four, 0, 0x1404), hi = __byte_perm(four, 0, 0x3424);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
 }
 
 __device__ __forceinline__ uint32_t half2_sub(uint32_t a, uint32_t b) {
@@ -245,7 +259,7 @@ struct Issuer {
     __device__ __forceinline__ void wait(uint64_t* b, uint32_t parity) {
         if (!dead && !tc::mbar_wait(b, parity)) dead = true;
     }
-    // S[n & 1] = K q1^T + K q2^T of tile n.
+    // S[n & 1] = K (q1 + q2 + q3)^T of tile n.
     __device__ __forceinline__ void scores(int n) {
         const int j = 2 * n, slot = j % kSlots;
         wait(&c.bar->full[slot], (j / kSlots) & 1);
@@ -256,9 +270,9 @@ struct Issuer {
         const uint64_t k = tc::desc_sw128(smem_u32(c.sm + kRingAt + slot * kHalf));
         const uint64_t q = tc::desc_sw128(smem_u32(c.sm + kQueriesAt));
 #pragma unroll
-        for (int x = 0; x < 8; ++x)                        // 32 channels a product; q2 is 32 rows of 128 bytes on
+        for (int x = 0; x < 12; ++x)                       // 32 channels a product; a piece is 32 rows of 128 bytes
             mma_f8(c.tmem + kRows * (n & 1), k + 2 * (x & 3), q + 2 * (x & 3) + (x >> 2) * (kRows * 128 >> 4),
-                   idesc_f8(128, kRows, 0, false, false), x > 0);
+                   idesc_f8(128, kRows, 1, false, false), x > 0);
         tc::mma_commit(&c.bar->empty[slot]);
         tc::mma_commit(&c.bar->s_full[n & 1]);
     }
@@ -331,25 +345,29 @@ struct Softmax {
 #pragma unroll
         for (int w = 1; w < 8; w <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, w));
         finite = (__ballot_sync(0xffffffffu, !finite) >> (threadIdx.x & 24) & 255u) == 0;
-        // 2^ex <= amax < 2^(ex + 1): times 2^(7 - ex), under e4m3's largest value
+        // 2^ex <= amax < 2^(ex + 1): times 2^(14 - ex), under e5m2's largest value
         int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-        ex = ex < -119 ? -119 : ex;
-        const float up = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
-        uint32_t one[4], two[4];
+        ex = ex < -112 ? -112 : ex;
+        const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+        float rest[16];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            float f[4], g[4];
+        for (int x = 0; x < 16; ++x) rest[x] = finite ? to_f32(e[x]) * up : 0.0f;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) f[x] = finite ? to_f32(e[4 * w + x]) * up : 0.0f;
-            one[w] = to_e4m3x4(f[0], f[1], f[2], f[3]);
-            from_e4m3x4(one[w], g);
-            two[w] = to_e4m3x4(f[0] - g[0], f[1] - g[1], f[2] - g[2], f[3] - g[3]);
+        for (int k = 0; k < 3; ++k) {
+            uint32_t word[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                word[w] = to_e5m2x4(rest[4 * w], rest[4 * w + 1], rest[4 * w + 2], rest[4 * w + 3]);
+                float f[4];
+                from_e5m2x4(word[w], f);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) rest[4 * w + x] -= f[x];
+            }
+            *reinterpret_cast<uint4*>(c.sm + kQueriesAt + tc::sw128(k * kRows + row, part)) =
+                make_uint4(word[0], word[1], word[2], word[3]);
         }
-        uint8_t* q_s = c.sm + kQueriesAt;
-        *reinterpret_cast<uint4*>(q_s + tc::sw128(row, part)) = make_uint4(one[0], one[1], one[2], one[3]);
-        *reinterpret_cast<uint4*>(q_s + tc::sw128(kRows + row, part)) = make_uint4(two[0], two[1], two[2], two[3]);
         if (part == 0) {
-            c.rows->factor[row] = finite ? a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + ex - 7) << 23)
+            c.rows->factor[row] = finite ? a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + ex - 14) << 23)
                                          : NAN;
             c.rows->m[row] = 0.0f;                         // until the first tile's scores
         }
