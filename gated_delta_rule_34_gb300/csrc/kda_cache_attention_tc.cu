@@ -2,9 +2,9 @@
 // tokens and prompts, whose rows share each head's keys.
 //
 // The mathematics is that of kda_cache_attention.cu.  With more than some 16 rows a head the
-// products there bound it (32 rows: 170 us for 537 MB of codes, 47% of the copy rate), above all the
-// conversion of every code to fp16.  Here the codes go to the tensor cores as they lie in the
-// cache, as e4m3 operands; what is not 8 bits is split instead:
+// products there bound it (537 MB of codes under 32 rows: 170 us; here 141 us, 3.8 TB/s; 64 rows 330 and 250 us),
+// above all the conversion of every code to fp16.  Here the codes go to the tensor cores as they lie in
+// the cache, as e4m3 operands; what is not 8 bits is split instead:
 //
 //   S^T [128 tokens x 32]  = K [128 x d] (q1 + q2 + q3)^T      e5m2 pieces, which hold the 8 bits of a bf16 value exactly,
 //                                                             down to 2^-30 of its row's largest

@@ -481,6 +481,8 @@ kda_status kda_cache_read(const void *k_codes, const void *v_codes, const float 
  *   lse        nullable; fp32 [B, T_q, H_q] (written)
  *   workspace  kda_cache_attention_workspace_size() bytes, 256-byte aligned;
  *              contents on entry are ignored
+ * If one of the bounded waits (about 2 s) of the kernel for more than 16 rows gives
+ * up, the outputs of that item and of its CTA's later ones are NaN.
  * Scores, sums and outputs are fp32 until the one rounding to dtype.  Weights
  * meet the values as fp16 numbers (two of them, 22 bits, where dtype is fp32) relative
  * to the row's largest w_t times its page's scale of v: what lies below 2^-36 of
