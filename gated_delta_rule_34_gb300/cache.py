@@ -21,16 +21,16 @@ E4M3, F32, F64, I32 = torch.float8_e4m3fn, torch.float32, torch.float64, torch.i
 # they do: one plain condition decides that all is well, and what is wrong is looked for
 # only where it is not.
 
+_current = torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # (absent where torch has no CUDA)
 
-def _call(index: int, fn, *args) -> None:
-    """fn(*args, stream) with device ``index`` current, on its current stream."""
-    if index == torch.cuda.current_device():
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with torch.cuda.device(index):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    if status:
-        _check(status)
+
+def _elsewhere(index: int, fn, *args, **kwargs):
+    """fn with device ``index`` current, which is not the current one (or no CUDA device)."""
+    if index < 0:
+        raise ValueError("the global-attention operators take CUDA tensors")
+    with torch.cuda.device(index):
+        return fn(*args, **kwargs)
 
 
 def _tensor(name, t, dtype, shape, index):
@@ -63,17 +63,21 @@ def _rows(name, t, dtype, index):
     strides = t.stride()
     if (d > 1 and strides[-1] != 1) or (h > 1 and strides[-2] != d):
         raise ValueError(f"{name}: the heads of a token must be dense")
-    stride, span = 0, 0                  # tokens of the inner dimensions, once there are two or more
+    stride, span = None, 0               # of the inner dimensions' tokens, once there are two or more
     for n, s in zip(reversed(shape[:-2]), reversed(strides[:-2])):
         if n == 1:
             continue
-        if not stride:
+        if stride is None:
             stride, span = s, s * n
         elif s != span:
             raise ValueError(f"{name}: all tokens must be evenly spaced")
         else:
             span *= n
-    return stride or h * d
+    if stride is None:
+        return h * d
+    if stride < h * d:
+        raise ValueError(f"{name}: tokens must not overlap")
+    return stride
 
 
 def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -111,7 +115,10 @@ def rotary(q, k, positions, freq, layout: str = "half", amplitude: float = 1.0, 
     positions: int32, one a token; freq: fp64 [rot / 2] (rotary_frequencies); layout "half" or
     "interleaved".  Returns (q_out, k_out), allocated dense unless given; they may be q and k.
     """
-    shape, dtype, index = q.shape, q.dtype, q.get_device()
+    index = q.get_device()
+    if index < 0 or index != _current():
+        return _elsewhere(index, rotary, q, k, positions, freq, layout, amplitude, q_out, k_out)
+    shape, dtype = q.shape, q.dtype
     qs = _rows("q", q, dtype, index)
     h_q, d = shape[-2:]
     n = q.numel() // (h_q * d) if h_q * d else 0
@@ -142,8 +149,11 @@ def rotary(q, k, positions, freq, layout: str = "half", amplitude: float = 1.0, 
     code = LAYOUTS.get(layout)
     if code is None:
         raise ValueError(f"layout must be half or interleaved, got {layout!r}")
-    _call(index, lib().kda_rotary, q.data_ptr(), qs, q_out.data_ptr(), qos, h_q, k_ptr, ks, ko_ptr, kos, h_k,
-          positions.data_ptr(), freq.data_ptr(), amplitude, n, d, 2 * freq.numel(), code, _dtype_code(dtype))
+    status = lib().kda_rotary(q.data_ptr(), qs, q_out.data_ptr(), qos, h_q, k_ptr, ks, ko_ptr, kos, h_k,
+                              positions.data_ptr(), freq.data_ptr(), amplitude, n, d, 2 * freq.numel(), code,
+                              _dtype_code(dtype), _raw_stream(index))
+    if status:
+        _check(status)
     return q_out, k_out
 
 
@@ -201,16 +211,22 @@ def cache_write(cache: PagedCache, k, v, block_table, start, cu_seqlens=None) ->
     bf16, tokens evenly spaced, heads dense); block_table: int32 [N, table_pages];
     start: int32 [N], the position of each sequence's first new token.
     """
-    shape, dtype, index = k.shape, k.dtype, k.get_device()
+    index = k.get_device()
+    if index < 0 or index != _current():
+        return _elsewhere(index, cache_write, cache, k, v, block_table, start, cu_seqlens)
+    shape, dtype = k.shape, k.dtype
     ks, vs = _rows("k", k, dtype, index), _rows("v", v, dtype, index)
     n_pages, h, page, d = _pool(cache, index)
     if len(shape) != 4 or v.shape != shape or shape[2] != h or shape[3] != d:
         raise ValueError(f"k and v must be [B, T, {h}, {d}], got {tuple(shape)} and {tuple(v.shape)}")
     n = _sequences(shape[0], cu_seqlens, block_table, start, index)
-    _call(index, lib().kda_cache_write, k.data_ptr(), ks, v.data_ptr(), vs, cache.k.data_ptr(), cache.v.data_ptr(),
-          cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), block_table.data_ptr(), block_table.shape[1],
-          start.data_ptr(), 0 if cu_seqlens is None else cu_seqlens.data_ptr(), n, shape[1], h, d, n_pages, page,
-          _dtype_code(dtype))
+    codes, values, k_scale, v_scale = cache
+    status = lib().kda_cache_write(
+        k.data_ptr(), ks, v.data_ptr(), vs, codes.data_ptr(), values.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        block_table.data_ptr(), block_table.shape[1], start.data_ptr(), 0 if cu_seqlens is None else cu_seqlens.data_ptr(),
+        n, shape[1], h, d, n_pages, page, _dtype_code(dtype), _raw_stream(index))
+    if status:
+        _check(status)
     return cache
 
 
@@ -221,6 +237,8 @@ def cache_read(cache: PagedCache, block_table, start, T: int, cu_seqlens=None, d
     all ([1, T, H_kv, d]).  Returns (k, v), allocated unless given."""
     device = cache.k.device
     index = cache.k.get_device()
+    if index < 0 or index != _current():
+        return _elsewhere(index, cache_read, cache, block_table, start, T, cu_seqlens, dtype, k_out, v_out)
     n_pages, h, page, d = _pool(cache, index)
     n = _sequences(block_table.shape[0] if cu_seqlens is None else 1, cu_seqlens, block_table, start, index)
     shape = (n if cu_seqlens is None else 1, T, h, d)
@@ -230,10 +248,12 @@ def cache_read(cache: PagedCache, block_table, start, T: int, cu_seqlens=None, d
         _tensor("k_out", k, dtype, shape, index)
     if v_out is not None:
         _tensor("v_out", v, dtype, shape, index)
-    _call(index, lib().kda_cache_read, cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
-          cache.v_scale.data_ptr(), block_table.data_ptr(), block_table.shape[1], start.data_ptr(),
-          0 if cu_seqlens is None else cu_seqlens.data_ptr(), n, T, h, d, n_pages, page, k.data_ptr(), v.data_ptr(),
-          _dtype_code(dtype))
+    status = lib().kda_cache_read(
+        cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(),
+        block_table.data_ptr(), block_table.shape[1], start.data_ptr(), 0 if cu_seqlens is None else cu_seqlens.data_ptr(),
+        n, T, h, d, n_pages, page, k.data_ptr(), v.data_ptr(), _dtype_code(dtype), _raw_stream(index))
+    if status:
+        _check(status)
     return k, v
 
 
@@ -259,7 +279,11 @@ def cache_attention(q, cache: PagedCache, block_table, lengths, scale: float | N
     ``sinks`` tokens besides.  Returns o [B, T_q, H_q, d], or with return_lse (o, lse) where
     lse is fp32 [B, T_q, H_q].  A workspace of the required size is allocated with torch if none is given.
     """
-    shape, dtype, index = q.shape, q.dtype, q.get_device()
+    index = q.get_device()
+    if index < 0 or index != _current():
+        return _elsewhere(index, cache_attention, q, cache, block_table, lengths, scale, window, sinks, out, lse, return_lse,
+                          workspace)
+    shape, dtype = q.shape, q.dtype
     qs = _rows("q", q, dtype, index)
     n_pages, h, page, d = _pool(cache, index)
     if len(shape) != 4 or shape[3] != d:
@@ -279,20 +303,20 @@ def cache_attention(q, cache: PagedCache, block_table, lengths, scale: float | N
         lse = torch.empty((B, t_q, h_q), dtype=F32, device=device)
     ws, ws_bytes = 0, 0
     if workspace is None:
-        if index == torch.cuda.current_device():
-            need = _workspace_need(index, B, t_q, h_q, h, d, page, wide)
-        else:
-            with torch.cuda.device(index):
-                need = _workspace_need(index, B, t_q, h_q, h, d, page, wide)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-            ws, ws_bytes = workspace.data_ptr(), need
+        ws_bytes = _workspace_need(index, B, t_q, h_q, h, d, page, wide)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+            ws = workspace.data_ptr()
     else:
         if workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _call(index, lib().kda_cache_attention, q.data_ptr(), qs, cache.k.data_ptr(), cache.v.data_ptr(),
-          cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), block_table.data_ptr(), wide, lengths.data_ptr(),
-          out.data_ptr(), 0 if lse is None else lse.data_ptr(), B, t_q, h_q, h, d, n_pages, page,
-          1.0 / math.sqrt(d) if scale is None else scale, window, sinks, _dtype_code(dtype), ws, ws_bytes)
+    codes, values, k_scale, v_scale = cache
+    status = lib().kda_cache_attention(
+        q.data_ptr(), qs, codes.data_ptr(), values.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        block_table.data_ptr(), wide, lengths.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), B, t_q,
+        h_q, h, d, n_pages, page, 1.0 / math.sqrt(d) if scale is None else scale, window, sinks, _dtype_code(dtype), ws,
+        ws_bytes, _raw_stream(index))
+    if status:
+        _check(status)
     return (out, lse) if return_lse else out

@@ -597,6 +597,13 @@ def test_binding_refusals():
         kda.cache_attention(q.transpose(1, 2), cache, table, lengths)
     with pytest.raises(TypeError):
         kda.cache_attention(q.half(), cache, table, lengths)
+    with pytest.raises(ValueError, match="overlap"):
+        kda.cache_attention(q[:1].expand(2, 1, 4, 64), cache, table, lengths)
+    with pytest.raises(ValueError, match="overlap"):
+        kda.rotary(q[:1].expand(2, 1, 4, 64), None, lengths, kda.rotary_frequencies(64))
+    with pytest.raises(ValueError, match="evenly"):
+        kda.rotary(torch.zeros(2, 5, 2, 64, device="cuda")[:, :3], None, torch.zeros(6, dtype=torch.int32, device="cuda"),
+                   kda.rotary_frequencies(64))
     with pytest.raises(kda.KDAError):
         kda.cache_attention(q, cache, table, lengths, window=-1)
     with pytest.raises(ValueError):
