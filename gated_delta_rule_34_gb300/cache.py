@@ -3,34 +3,53 @@
 
 Argument marshalling only, as in ``api``: tensors are checked for device, dtype, shape and
 layout, and their data pointers plus the current CUDA stream are handed to ``libkda.so``.
+A decode step's kernels take a few microseconds, so the marshalling itself is compiled
+(csrc/cache_binding.cpp): a call that it finds well formed is launched, for any other it returns
+None and launches nothing, and what is wrong is then looked for here.
 """
 from __future__ import annotations
 
+import ctypes
 import functools
+import importlib.util
 import math
+import os
+from importlib.machinery import ExtensionFileLoader
 from typing import NamedTuple
 
 import torch
 
+from . import build as _build
 from .api import _check, _dtype_code, lib
 
-LAYOUTS = {"half": 0, "interleaved": 1}
 E4M3, F32, F64, I32 = torch.float8_e4m3fn, torch.float32, torch.float64, torch.int32
 
-# A decode step's kernels take a few microseconds, so the checks below cost as much as
-# they do: one plain condition decides that all is well, and what is wrong is looked for
-# only where it is not.
 
-_current = torch.cuda.current_device
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # (absent where torch has no CUDA)
+@functools.lru_cache(maxsize=None)
+def _binding():
+    """The compiled marshalling, calling the library that ``lib`` has loaded; raises if it has not been built."""
+    entries = [getattr(lib(), name) for name in ("kda_rotary", "kda_cache_write", "kda_cache_read",
+                                                 "kda_cache_attention", "kda_cache_attention_workspace_size")]
+    if not os.path.exists(_build.BINDING):
+        raise RuntimeError(
+            f"KDA binding not found at {_build.BINDING}; build it with "
+            "`python -m gated_delta_rule_34_gb300.build` (there is no fallback path)")
+    loader = ExtensionFileLoader("kda_cache_binding", _build.BINDING)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader(loader.name, loader))
+    loader.exec_module(module)
+    module.bind(*(ctypes.cast(e, ctypes.c_void_p).value for e in entries), _check)
+    return module
 
 
-def _elsewhere(index: int, fn, *args, **kwargs):
-    """fn with device ``index`` current, which is not the current one (or no CUDA device)."""
+def _is_elsewhere(index: int) -> bool:
+    """Whether device ``index`` is another than the current one."""
     if index < 0:
         raise ValueError("the global-attention operators take CUDA tensors")
-    with torch.cuda.device(index):
-        return fn(*args, **kwargs)
+    return index != torch.cuda.current_device()
+
+
+def _not_understood(name: str):
+    raise TypeError(f"{name}: arguments of a type or size that it does not take")
 
 
 def _tensor(name, t, dtype, shape, index):
@@ -48,8 +67,8 @@ def _tensor(name, t, dtype, shape, index):
 
 
 def _rows(name, t, dtype, index):
-    """The token stride, in elements, of [..., tokens, H, d] whose [H, d] are dense and whose
-    leading dimensions, if any, are token runs one after another."""
+    """[..., tokens, H, d] whose [H, d] are dense and whose tokens are evenly spaced, leading
+    dimensions being token runs one after another."""
     if index < 0 or t.get_device() != index:
         raise ValueError(f"{name} must be a CUDA tensor" + (f" on cuda:{index}" if index >= 0 else ""))
     if t.dtype is not dtype:
@@ -59,7 +78,7 @@ def _rows(name, t, dtype, index):
         raise ValueError(f"{name} must be [..., tokens, H, d], got {tuple(shape)}")
     h, d = shape[-2:]
     if t.is_contiguous():
-        return h * d
+        return
     strides = t.stride()
     if (d > 1 and strides[-1] != 1) or (h > 1 and strides[-2] != d):
         raise ValueError(f"{name}: the heads of a token must be dense")
@@ -73,11 +92,8 @@ def _rows(name, t, dtype, index):
             raise ValueError(f"{name}: all tokens must be evenly spaced")
         else:
             span *= n
-    if stride is None:
-        return h * d
-    if stride < h * d:
+    if stride is not None and stride < h * d:
         raise ValueError(f"{name}: tokens must not overlap")
-    return stride
 
 
 def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -115,46 +131,39 @@ def rotary(q, k, positions, freq, layout: str = "half", amplitude: float = 1.0, 
     positions: int32, one a token; freq: fp64 [rot / 2] (rotary_frequencies); layout "half" or
     "interleaved".  Returns (q_out, k_out), allocated dense unless given; they may be q and k.
     """
+    done = _binding().rotary(q, k, positions, freq, layout, amplitude, q_out, k_out)
+    if done is not None:
+        return done
     index = q.get_device()
-    if index < 0 or index != _current():
-        return _elsewhere(index, rotary, q, k, positions, freq, layout, amplitude, q_out, k_out)
+    if _is_elsewhere(index):
+        with torch.cuda.device(index):
+            return rotary(q, k, positions, freq, layout, amplitude, q_out, k_out)
     shape, dtype = q.shape, q.dtype
-    qs = _rows("q", q, dtype, index)
+    _dtype_code(dtype)
+    _rows("q", q, dtype, index)
     h_q, d = shape[-2:]
     n = q.numel() // (h_q * d) if h_q * d else 0
-    if q_out is None:
-        q_out, qos = torch.empty(shape, dtype=dtype, device=q.device), h_q * d
-    else:
-        qos = _rows("q_out", q_out, dtype, index)
+    if q_out is not None:
+        _rows("q_out", q_out, dtype, index)
         if q_out.shape != shape:
             raise ValueError("q_out must have q's shape")
-    ks, kos, h_k, k_ptr, ko_ptr = 0, 0, 0, 0, 0
     if k is not None:
-        ks, h_k = _rows("k", k, dtype, index), k.shape[-2]
+        _rows("k", k, dtype, index)
         if k.shape[:-2] != shape[:-2] or k.shape[-1] != d:
             raise ValueError(f"k must be [..., H_k, d] of q's tokens, got {tuple(k.shape)} beside {tuple(shape)}")
-        if k_out is None:
-            k_out, kos = torch.empty(k.shape, dtype=dtype, device=q.device), h_k * d
-        else:
-            kos = _rows("k_out", k_out, dtype, index)
+        if k_out is not None:
+            _rows("k_out", k_out, dtype, index)
             if k_out.shape != k.shape:
                 raise ValueError("k_out must have k's shape")
-        k_ptr, ko_ptr = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
     if positions.numel() != n:
         raise ValueError(f"{n} tokens but {positions.numel()} positions")
     _tensor("positions", positions, I32, positions.shape, index)
     _tensor("freq", freq, F64, (-1,) if freq.dim() != 1 else freq.shape, index)
-    code = LAYOUTS.get(layout)
-    if code is None:
+    if layout not in ("half", "interleaved"):
         raise ValueError(f"layout must be half or interleaved, got {layout!r}")
-    status = lib().kda_rotary(q.data_ptr(), qs, q_out.data_ptr(), qos, h_q, k_ptr, ks, ko_ptr, kos, h_k,
-                              positions.data_ptr(), freq.data_ptr(), amplitude, n, d, 2 * freq.numel(), code,
-                              _dtype_code(dtype), _raw_stream(index))
-    if status:
-        _check(status)
-    return q_out, k_out
+    _not_understood("rotary")
 
 
 class PagedCache(NamedTuple):
@@ -211,23 +220,22 @@ def cache_write(cache: PagedCache, k, v, block_table, start, cu_seqlens=None) ->
     bf16, tokens evenly spaced, heads dense); block_table: int32 [N, table_pages];
     start: int32 [N], the position of each sequence's first new token.
     """
+    done = _binding().cache_write(cache, k, v, block_table, start, cu_seqlens)
+    if done is not None:
+        return done
     index = k.get_device()
-    if index < 0 or index != _current():
-        return _elsewhere(index, cache_write, cache, k, v, block_table, start, cu_seqlens)
+    if _is_elsewhere(index):
+        with torch.cuda.device(index):
+            return cache_write(cache, k, v, block_table, start, cu_seqlens)
     shape, dtype = k.shape, k.dtype
-    ks, vs = _rows("k", k, dtype, index), _rows("v", v, dtype, index)
+    _dtype_code(dtype)
+    _rows("k", k, dtype, index)
+    _rows("v", v, dtype, index)
     n_pages, h, page, d = _pool(cache, index)
     if len(shape) != 4 or v.shape != shape or shape[2] != h or shape[3] != d:
         raise ValueError(f"k and v must be [B, T, {h}, {d}], got {tuple(shape)} and {tuple(v.shape)}")
-    n = _sequences(shape[0], cu_seqlens, block_table, start, index)
-    codes, values, k_scale, v_scale = cache
-    status = lib().kda_cache_write(
-        k.data_ptr(), ks, v.data_ptr(), vs, codes.data_ptr(), values.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-        block_table.data_ptr(), block_table.shape[1], start.data_ptr(), 0 if cu_seqlens is None else cu_seqlens.data_ptr(),
-        n, shape[1], h, d, n_pages, page, _dtype_code(dtype), _raw_stream(index))
-    if status:
-        _check(status)
-    return cache
+    _sequences(shape[0], cu_seqlens, block_table, start, index)
+    _not_understood("cache_write")
 
 
 def cache_read(cache: PagedCache, block_table, start, T: int, cu_seqlens=None, dtype=torch.bfloat16,
@@ -235,32 +243,22 @@ def cache_read(cache: PagedCache, block_table, start, T: int, cu_seqlens=None, d
     """Cached tokens as dense rows, through kda_cache_read: T tokens of each sequence from
     position start[n] on ([N, T, H_kv, d]), or with cu_seqlens those of its packed rows, T rows in
     all ([1, T, H_kv, d]).  Returns (k, v), allocated unless given."""
-    device = cache.k.device
-    index = cache.k.get_device()
-    if index < 0 or index != _current():
-        return _elsewhere(index, cache_read, cache, block_table, start, T, cu_seqlens, dtype, k_out, v_out)
+    done = _binding().cache_read(cache, block_table, start, T, cu_seqlens, dtype, k_out, v_out)
+    if done is not None:
+        return done
+    index = cache[0].get_device()
+    if _is_elsewhere(index):
+        with torch.cuda.device(index):
+            return cache_read(cache, block_table, start, T, cu_seqlens, dtype, k_out, v_out)
+    _dtype_code(dtype)
     n_pages, h, page, d = _pool(cache, index)
     n = _sequences(block_table.shape[0] if cu_seqlens is None else 1, cu_seqlens, block_table, start, index)
     shape = (n if cu_seqlens is None else 1, T, h, d)
-    k = torch.empty(shape, dtype=dtype, device=device) if k_out is None else k_out
-    v = torch.empty(shape, dtype=dtype, device=device) if v_out is None else v_out
     if k_out is not None:
-        _tensor("k_out", k, dtype, shape, index)
+        _tensor("k_out", k_out, dtype, shape, index)
     if v_out is not None:
-        _tensor("v_out", v, dtype, shape, index)
-    status = lib().kda_cache_read(
-        cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(),
-        block_table.data_ptr(), block_table.shape[1], start.data_ptr(), 0 if cu_seqlens is None else cu_seqlens.data_ptr(),
-        n, T, h, d, n_pages, page, k.data_ptr(), v.data_ptr(), _dtype_code(dtype), _raw_stream(index))
-    if status:
-        _check(status)
-    return k, v
-
-
-@functools.lru_cache(maxsize=1024)
-def _workspace_need(index, *sizes) -> int:
-    """The library's answer for the current device, which is ``index``: a function of sizes alone."""
-    return int(lib().kda_cache_attention_workspace_size(*sizes))
+        _tensor("v_out", v_out, dtype, shape, index)
+    _not_understood("cache_read")
 
 
 def cache_attention_workspace_size(B: int, T_q: int, H_q: int, H_kv: int, d: int, page: int,
@@ -279,44 +277,25 @@ def cache_attention(q, cache: PagedCache, block_table, lengths, scale: float | N
     ``sinks`` tokens besides.  Returns o [B, T_q, H_q, d], or with return_lse (o, lse) where
     lse is fp32 [B, T_q, H_q].  A workspace of the required size is allocated with torch if none is given.
     """
+    done = _binding().cache_attention(q, cache, block_table, lengths, scale, window, sinks, out, lse, return_lse, workspace)
+    if done is not None:
+        return done
     index = q.get_device()
-    if index < 0 or index != _current():
-        return _elsewhere(index, cache_attention, q, cache, block_table, lengths, scale, window, sinks, out, lse, return_lse,
-                          workspace)
+    if _is_elsewhere(index):
+        with torch.cuda.device(index):
+            return cache_attention(q, cache, block_table, lengths, scale, window, sinks, out, lse, return_lse, workspace)
     shape, dtype = q.shape, q.dtype
-    qs = _rows("q", q, dtype, index)
+    _dtype_code(dtype)
+    _rows("q", q, dtype, index)
     n_pages, h, page, d = _pool(cache, index)
     if len(shape) != 4 or shape[3] != d:
         raise ValueError(f"q must be [B, T_q, H_q, {d}], got {tuple(shape)}")
-    B, t_q, h_q, _ = shape
-    wide = block_table.shape[-1]
-    _tensor("block_table", block_table, I32, (B, wide), index)
-    _tensor("lengths", lengths, I32, (B,), index)
-    device = q.device
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
-    else:
+    _tensor("block_table", block_table, I32, (shape[0], block_table.shape[-1]), index)
+    _tensor("lengths", lengths, I32, (shape[0],), index)
+    if out is not None:
         _tensor("out", out, dtype, shape, index)
     if lse is not None:
-        _tensor("lse", lse, F32, (B, t_q, h_q), index)
-    elif return_lse:
-        lse = torch.empty((B, t_q, h_q), dtype=F32, device=device)
-    ws, ws_bytes = 0, 0
-    if workspace is None:
-        ws_bytes = _workspace_need(index, B, t_q, h_q, h, d, page, wide)
-        if ws_bytes:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
-            ws = workspace.data_ptr()
-    else:
-        if workspace.get_device() != index or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    codes, values, k_scale, v_scale = cache
-    status = lib().kda_cache_attention(
-        q.data_ptr(), qs, codes.data_ptr(), values.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-        block_table.data_ptr(), wide, lengths.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), B, t_q,
-        h_q, h, d, n_pages, page, 1.0 / math.sqrt(d) if scale is None else scale, window, sinks, _dtype_code(dtype), ws,
-        ws_bytes, _raw_stream(index))
-    if status:
-        _check(status)
-    return (out, lse) if return_lse else out
+        _tensor("lse", lse, F32, shape[:3], index)
+    if workspace is not None and (workspace.get_device() != index or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {q.device}")
+    _not_understood("cache_attention")
