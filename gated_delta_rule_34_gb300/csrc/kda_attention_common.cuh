@@ -5,6 +5,7 @@
 #include <climits>
 
 #include "kda_cache.cuh"
+#include "kda_chained.cuh"
 #include "kda_internal.h"
 #include "tc_util.cuh"
 

@@ -23,6 +23,7 @@
 // 255 us, 6.4 TB/s; 16 of up to 16384 tokens, 8 heads, read in 132 us, 6.5 TB/s; one token of each
 // of 256 sequences, 8 heads, written in 5.9 us, most of it loads that wait for one another.
 #include "kda_cache.cuh"
+#include "kda_chained.cuh"
 #include "kda_internal.h"
 
 namespace kda {
@@ -149,14 +150,15 @@ __device__ __forceinline__ void round_unit(const uint4 (&raw)[sizeof(T)], float 
 // 6.4 TB/s; 258 us with seven.)
 template <typename T, int GROUP>
 __global__ void __launch_bounds__(kCacheThreads, sizeof(T) == 2 ? 8 : 5)
-cache_write_kernel(CacheSpan w, const T* __restrict__ k, int64_t k_stride, const T* __restrict__ v,
-                   int64_t v_stride, uint8_t* __restrict__ k_codes, uint8_t* __restrict__ v_codes,
-                   float* __restrict__ k_scale, float* __restrict__ v_scale,
-                   const int32_t* __restrict__ table, const int32_t* __restrict__ start,
-                   const int32_t* __restrict__ cu) {
+cache_write_kernel(CacheSpan w, const T* k, int64_t k_stride, const T* v,
+                   int64_t v_stride, uint8_t* k_codes, uint8_t* v_codes,
+                   float* k_scale, float* v_scale,
+                   const int32_t* table, const int32_t* start,
+                   const int32_t* cu) {
     constexpr int ITEMS = kCacheThreads / 32 / GROUP;      // of one CTA, all of one slot
     constexpr int THREADS = 32 * GROUP;
     __shared__ float warp_max[kCacheThreads / 32];
+    after_the_kernel_before();
     const int chunks = (2 * w.H + ITEMS - 1) / ITEMS;
     const int64_t slot = blockIdx.x / chunks;
     const int item = (int)(blockIdx.x - slot * chunks) * ITEMS + threadIdx.x / THREADS;
@@ -247,11 +249,12 @@ cache_write_kernel(CacheSpan w, const T* __restrict__ k, int64_t k_stride, const
 
 template <typename T>
 __global__ void __launch_bounds__(kCacheThreads)
-cache_read_kernel(CacheSpan w, const uint8_t* __restrict__ k_codes,
-                  const uint8_t* __restrict__ v_codes, const float* __restrict__ k_scale,
-                  const float* __restrict__ v_scale, const int32_t* __restrict__ table,
-                  const int32_t* __restrict__ start, const int32_t* __restrict__ cu,
-                  T* __restrict__ k, T* __restrict__ v) {
+cache_read_kernel(CacheSpan w, const uint8_t* k_codes,
+                  const uint8_t* v_codes, const float* k_scale,
+                  const float* v_scale, const int32_t* table,
+                  const int32_t* start, const int32_t* cu,
+                  T* k, T* v) {
+    after_the_kernel_before();
     const int64_t slot = blockIdx.x / (2 * w.H);
     const int item = (int)(blockIdx.x - slot * (2 * w.H));
     const PageRun run = page_run(slot, w, cu, start, table);
@@ -310,16 +313,17 @@ static cudaError_t launch_write(const CacheSpan& w, const void* k, int64_t ks, c
     // One warp an item up to an average of 8 rows a sequence, four above.
     if (w.rows <= 8LL * w.n_seqs) {
         const int64_t grid = slots * ((2 * w.H + 3) / 4);
-        cache_write_kernel<T, 1><<<(unsigned)grid, kCacheThreads, 0, stream>>>(
+        return launch_chained(
+            cache_write_kernel<T, 1>, (unsigned)grid, kCacheThreads, 0, stream,
             w, static_cast<const T*>(k), ks, static_cast<const T*>(v), vs, static_cast<uint8_t*>(kc),
             static_cast<uint8_t*>(vc), k_scale, v_scale, table, start, cu);
     } else {
         const int64_t grid = slots * 2 * w.H;
-        cache_write_kernel<T, 4><<<(unsigned)grid, kCacheThreads, 0, stream>>>(
+        return launch_chained(
+            cache_write_kernel<T, 4>, (unsigned)grid, kCacheThreads, 0, stream,
             w, static_cast<const T*>(k), ks, static_cast<const T*>(v), vs, static_cast<uint8_t*>(kc),
             static_cast<uint8_t*>(vc), k_scale, v_scale, table, start, cu);
     }
-    return cudaGetLastError();
 }
 
 cudaError_t run_cache_write(const CacheSpan& w, const void* k, int64_t k_stride, const void* v,
@@ -341,14 +345,12 @@ cudaError_t run_cache_read(const CacheSpan& w, const void* k_codes, const void* 
     const uint8_t* kc = static_cast<const uint8_t*>(k_codes);
     const uint8_t* vc = static_cast<const uint8_t*>(v_codes);
     if (bf16)
-        cache_read_kernel<__nv_bfloat16><<<(unsigned)grid, kCacheThreads, 0, stream>>>(
-            w, kc, vc, k_scale, v_scale, table, start, cu, static_cast<__nv_bfloat16*>(k),
+        return launch_chained(
+            cache_read_kernel<__nv_bfloat16>, (unsigned)grid, kCacheThreads, 0, stream, w, kc, vc, k_scale, v_scale, table, start, cu, static_cast<__nv_bfloat16*>(k),
             static_cast<__nv_bfloat16*>(v));
-    else
-        cache_read_kernel<float><<<(unsigned)grid, kCacheThreads, 0, stream>>>(
-            w, kc, vc, k_scale, v_scale, table, start, cu, static_cast<float*>(k),
-            static_cast<float*>(v));
-    return cudaGetLastError();
+    return launch_chained(
+        cache_read_kernel<float>, (unsigned)grid, kCacheThreads, 0, stream, w, kc, vc, k_scale, v_scale, table, start, cu,
+        static_cast<float*>(k), static_cast<float*>(v));
 }
 
 }  // namespace kda

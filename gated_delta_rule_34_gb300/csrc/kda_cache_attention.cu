@@ -175,7 +175,7 @@ struct Piece {
                 const bool in = real && 64 * j + 16 * c < a.d;
 #pragma unroll
                 for (int w = 0; w < (int)sizeof(T); ++w)
-                    raw[j][w] = in ? __ldg(reinterpret_cast<const uint4*>(q + 64 * j + 16 * c) + w)
+                    raw[j][w] = in ? reinterpret_cast<const uint4*>(q + 64 * j + 16 * c)[w]
                                    : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
@@ -241,7 +241,7 @@ struct Piece {
         auto page_at = [&](int s) -> int {
             const int t = tile.token(s);
             if (s >= to || t >= tile.end) return -1;
-            return __ldg(table + (t >> a.page_shift));
+            return table[t >> a.page_shift];
         };
         // Copies step s (its page's id is pg) into stage st.
         auto issue = [&](int s, int pg, int st) {
@@ -610,6 +610,7 @@ template <typename T, int D, int NT, int MT>
 __global__ void __launch_bounds__(kThreads, Shape<T, D, NT, MT>::CTAS)
 attention_whole_kernel(const CacheAttention a, const Plan plan) {
     extern __shared__ __align__(16) uint8_t smem[];
+    after_the_kernel_before();
     const int pair = blockIdx.x / a.H_kv, hk = blockIdx.x % a.H_kv;
     const Tile tile = tile_of(a, plan, pair);
     Piece<T, D, NT, MT> piece{a, plan, smem, pair / plan.row_tiles, hk, pair % plan.row_tiles, 0, tile.steps, tile};
@@ -621,7 +622,7 @@ template <typename T, int D, int NT, int MT>
 __global__ void __launch_bounds__(kThreads, Shape<T, D, NT, MT>::CTAS)
 attention_share_kernel(const CacheAttention a, const Plan plan) {
     extern __shared__ __align__(16) uint8_t smem[];
-    asm volatile("griddepcontrol.launch_dependents;");
+    after_the_kernel_before();
     const Share share = find_share<kThreads>(a, plan);
     const int4 join = for_each_piece(a, plan, share, [&](int pair, int hk, const Tile& tile, int from, int to, int slot,
                                                          bool whole) {
@@ -641,7 +642,7 @@ attention_join_kernel(const CacheAttention a, const Plan plan) {
     constexpr int WARPS = kJoinThreads / 32, PER = D / 32;
     __shared__ float4 o_s[WARPS][D / PER];
     __shared__ float l_s[WARPS];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_the_kernel_before();
     const int4 join = plan.joins[blockIdx.x];
     if (join.x < 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -768,33 +769,22 @@ cudaError_t launch(Shape<T, D, NT, MT>, const CacheAttention& a, void* workspace
         cudaError_t e = cudaFuncSetAttribute(attention_whole_kernel<T, D, NT, MT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
         if (e != cudaSuccess) return e;
-        attention_whole_kernel<T, D, NT, MT><<<(unsigned)items, kThreads, S::SMEM, stream>>>(a, plan);
-        return cudaGetLastError();
+        return launch_chained(attention_whole_kernel<T, D, NT, MT>, (unsigned)items, kThreads, S::SMEM, stream, a, plan);
     }
     set_attention_pieces(plan, workspace, grid);
     cudaError_t e = cudaFuncSetAttribute(attention_share_kernel<T, D, NT, MT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
-    attention_share_kernel<T, D, NT, MT><<<(unsigned)grid, kThreads, S::SMEM, stream>>>(a, plan);
-    e = cudaGetLastError();
+    e = launch_chained(attention_share_kernel<T, D, NT, MT>, (unsigned)grid, kThreads, S::SMEM, stream, a, plan);
     return e != cudaSuccess ? e : run_attention_join(a, plan, sizeof(T) == 2, D, grid, stream);
 }
 
 template <typename T, int D>
 cudaError_t launch_join(const CacheAttention& a, const Plan& plan, int64_t grid, cudaStream_t stream) {
-    // Its CTAs come up while the kernel before ends, and wait for it.  A row a CTA
-    // where the items are so few that each ends in many pieces.
+    // A row a CTA where the items are so few that each ends in many pieces.
     const bool many = grid > kJoinFew * (int64_t)a.B * plan.row_tiles * a.H_kv;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)(many ? plan.stored : (plan.stored + 7) / 8));
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, D>, a, plan);
+    const dim3 ctas((unsigned)grid, (unsigned)(many ? plan.stored : (plan.stored + 7) / 8));
+    return launch_chained(attention_join_kernel<T, D>, ctas, kJoinThreads, 0, stream, a, plan);
 }
 
 }  // namespace

@@ -192,7 +192,7 @@ struct Loader {
         // Lane k < 8: where step k of the tile at step s0 is in the pool, and how many of its tokens exist.
         auto page_of = [&](int s0) -> int {
             const int s = s0 + lane, t = tile.token(s);
-            return lane < kTileSteps && s < to && t < tile.end ? __ldg(table + (t >> a.page_shift)) : -1;
+            return lane < kTileSteps && s < to && t < tile.end ? table[t >> a.page_shift] : -1;
         };
         int id = page_of(from);
         for (int s0 = from; s0 < to && !dead; s0 += kTileSteps) {
@@ -332,7 +332,7 @@ struct Softmax {
         uint4 raw[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x)
-            raw[x] = real && 16 * part < a.d ? __ldg(reinterpret_cast<const uint4*>(q) + x) : make_uint4(0, 0, 0, 0);
+            raw[x] = real && 16 * part < a.d ? reinterpret_cast<const uint4*>(q)[x] : make_uint4(0, 0, 0, 0);
         const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(raw);
         float amax = 0.0f;
         bool finite = true;
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_tc_kernel(const Cac
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Barriers* bar = reinterpret_cast<Barriers*>(sm + kBarriersAt);
     const int warp = threadIdx.x >> 5;
-    if (!WHOLE) asm volatile("griddepcontrol.launch_dependents;");
+    after_the_kernel_before();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSlots; ++i) {
             tc::mbar_init(&bar->full[i], kLoaders);
@@ -731,14 +731,12 @@ cudaError_t run_attention_tc(const CacheAttention& a, void* workspace, cudaStrea
         const int64_t items = (int64_t)a.B * plan.row_tiles * a.H_kv;
         cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
-        attention_tc_kernel<true><<<(unsigned)items, kThreads, kSmem, stream>>>(a, plan);
-        return cudaGetLastError();
+        return launch_chained(attention_tc_kernel<true>, (unsigned)items, kThreads, kSmem, stream, a, plan);
     }
     set_attention_pieces(plan, workspace, grid);
     cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    attention_tc_kernel<false><<<(unsigned)grid, kThreads, kSmem, stream>>>(a, plan);
-    e = cudaGetLastError();
+    e = launch_chained(attention_tc_kernel<false>, (unsigned)grid, kThreads, kSmem, stream, a, plan);
     return e != cudaSuccess ? e : run_attention_join(a, plan, true, 128, grid, stream);
 }
 

@@ -22,6 +22,7 @@
 // vectors in the half layout, rot in the interleaved one), else 8, 4 or 2.
 // Measured: 65536 tokens of 32 + 8 heads of 128 channels, 64 turned, bf16: 202 us, 6.6 TB/s;
 // 4097 tokens of 16 + 16 heads of 64 channels, fp32: 10.7 us, 6.3 TB/s; one token: 2.6 us.
+#include "kda_chained.cuh"
 #include "kda_common.cuh"
 #include "kda_internal.h"
 
@@ -83,13 +84,14 @@ __device__ __forceinline__ typename RawOf<V * sizeof(T)>::type pack_raw(const fl
 // so; wider vectors lose by it, as two passes then write the same sectors).
 template <typename T, bool HALF, int V>
 __global__ void __launch_bounds__(kRotaryThreads)
-rotary_kernel(RotarySide q, RotarySide k, const int32_t* __restrict__ positions,
-              const double* __restrict__ freq, float amplitude, int64_t n_tokens, int d, int rot,
+rotary_kernel(RotarySide q, RotarySide k, const int32_t* positions,
+              const double* freq, float amplitude, int64_t n_tokens, int d, int rot,
               int tile) {
     using Raw = typename RawOf<V * sizeof(T)>::type;
     constexpr int A = HALF ? V : V / 2;                    // angles of a unit
     constexpr int H = rotary_heads(HALF, V * sizeof(T));
     extern __shared__ __align__(16) float2 cs[];           // [tokens][A][turned]
+    after_the_kernel_before();
     const int half = rot / 2, turned = half / A;
     const int64_t t0 = (int64_t)blockIdx.x * tile;
     const int nt = (int)(n_tokens - t0 < tile ? n_tokens - t0 : tile);
@@ -198,9 +200,8 @@ static cudaError_t launch_rotary(const RotarySide& q, const RotarySide& k, const
     int tile = 16;
     while (tile > 1 && (n_tokens + tile - 1) / tile < 4 * num_sms) tile /= 2;
     const unsigned grid = (unsigned)((n_tokens + tile - 1) / tile);
-    rotary_kernel<T, HALF, V><<<grid, kRotaryThreads, (size_t)tile * (rot / 2) * sizeof(float2), stream>>>(
-        q, k, positions, freq, amplitude, n_tokens, d, rot, tile);
-    return cudaGetLastError();
+    return launch_chained(rotary_kernel<T, HALF, V>, grid, kRotaryThreads, (size_t)tile * (rot / 2) * sizeof(float2), stream,
+                          q, k, positions, freq, amplitude, n_tokens, d, rot, tile);
 }
 
 // The widest vector that rot allows; d is whole 16-byte vectors.
