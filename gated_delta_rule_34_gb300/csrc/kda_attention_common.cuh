@@ -112,6 +112,23 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
     return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
 
+// Steps of an item at most.
+inline int64_t most_steps(const CacheAttention& a) {
+    const int64_t held = ((int64_t)a.table_pages << a.page_shift) / kStep;
+    if (a.window == 0) return held;
+    const int64_t seen = (a.window < INT_MAX ? a.window + a.T_q : INT_MAX) / kStep + 2 + (a.sinks + (int64_t)kStep - 1) / kStep;
+    return seen < held ? seen : held;
+}
+
+// Whether one CTA an item is faster than equal shares of all items' steps.  Cutting costs each CTA a second start and
+// end and a kernel that joins, together the time of `cutting` steps; whole items cost what the longest takes beyond
+// the average load of the CTAs, where lengths are even from 0 to the longest: cap - items cap / (2 ctas) steps.
+// No length is known here, only what the block table can hold, so that one long sequence among short ones is not cut then:
+// up to `longest` steps.
+inline bool whole_items_pay(int64_t cap, int64_t items, int64_t ctas, int64_t cutting, int64_t longest) {
+    return cap <= longest && cap * (2 * ctas - items) <= 2 * ctas * cutting;
+}
+
 // A CTA's share of the list of all items' steps: [begin, end), which starts in pair `pair`
 // (-1: nothing), whose first head begins at `base`.
 struct Share {

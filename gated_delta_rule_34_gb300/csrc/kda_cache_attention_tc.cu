@@ -71,7 +71,8 @@ struct alignas(16) Rows {
     float up[kRows];                       // by how much a reference moved,
     float keep_o[kRows], keep_l[kRows];    // and what that multiplies the sums by
     float dm_most[4];                      // of each 16 rows: the largest dm,
-    uint32_t unset[4];                     // and those that have seen no score yet, a bit each: m = 0 is none of theirs
+    uint32_t unset[2];                     // and those that have seen no score yet, a bit each: m = 0 is none of theirs
+    uint32_t empty[2];                     // at the end: those whose sum of weights is 0
     float part[4][kRows], part_e[4][kRows];
     uint32_t nan[kRows][4];                // channels whose output is NaN, a bit each
 };
@@ -583,16 +584,20 @@ struct Softmax {
         if (!dead && vote(bad, kBarSoftmax, kSoftmax)) dead = true;
         rows->part[quarter][r0 + (lane >> 1)] = reduce_rows(l, [](float x, float y) { return x + y; });
         tc::named_bar_sync(kBarSoftmax, kSoftmax);
+        // What a row needs once, not 128 times: the factor that makes its sums outputs (with that worked out in every
+        // thread, and the rows' places by divisions, 2,048 items of 4,096 tokens took 735 us instead of 688).
         const int rows_here = rows_of_tile(plan, rt);
         const int64_t place = ((int64_t)blockIdx.x * 2 + slot) * plan.stored;
-        auto sum_of = [&](int r) {
-            return dead ? NAN : (rows->part[0][r] + rows->part[1][r]) + (rows->part[2][r] + rows->part[3][r]);
-        };
-        if (threadIdx.x < rows_here) {
+        if (threadIdx.x < kRows) {
             const int r = threadIdx.x;
-            const float L = sum_of(r);
-            if (!whole) plan.stats[place + r] = make_float4(rows->unset[r / kMine] >> r % kMine & 1 ? kLowest : rows->m[r], rows->dm[r], L, 0.0f);
-            else if (a.lse) a.lse[output_row(a, plan, b, hk, rt, r)] = row_lse(rows->m[r], L);
+            const float L = dead ? NAN : (rows->part[0][r] + rows->part[1][r]) + (rows->part[2][r] + rows->part[3][r]);
+            const uint32_t empty = __ballot_sync(0xffffffffu, L == 0.0f);
+            if (r % kMine == 0) rows->empty[r / kMine] = empty >> r;
+            rows->keep_o[r] = row_factor(rows->dm[r], L);
+            if (r < rows_here) {
+                if (!whole) plan.stats[place + r] = make_float4(rows->unset[r / kMine] >> r % kMine & 1 ? kLowest : rows->m[r], rows->dm[r], L, 0.0f);
+                else if (a.lse) a.lse[output_row(a, plan, b, hk, rt, r)] = row_lse(rows->m[r], L);
+            }
         }
         float o[16];
         const uint32_t from_o = c.tmem + kTmemO + lanes + r0;
@@ -609,18 +614,28 @@ struct Softmax {
 #pragma unroll
             for (int y = 0; y < 16; ++y) o[y] = fmaf(x[y], part, o[y]);
         }
+        tc::named_bar_sync(kBarSoftmax, kSoftmax);
 #pragma unroll
-        for (int y = 0; y < 16; ++y) {
-            const int r = r0 + y;
-            if (r >= rows_here) break;
-            float v = rows->nan[r][quarter] >> lane & 1 ? NAN : o[y];
-            if (dead) v = NAN;
-            if (!whole) {
-                plan.sums[(place + r) * 128 + t] = v;
-            } else if (t < a.d) {
-                const float L = sum_of(r);
-                v = L == 0.0f ? 0.0f : v * row_factor(rows->dm[r], L);
-                static_cast<__nv_bfloat16*>(a.o)[output_row(a, plan, b, hk, rt, r) * a.d + t] = __float2bfloat16_rn(v);
+        for (int y = 0; y < 16; ++y)
+            if (dead || (rows->nan[r0 + y][quarter] >> lane & 1)) o[y] = NAN;
+        if (!whole) {
+            float* to = plan.sums + (place + r0) * 128 + t;
+#pragma unroll
+            for (int y = 0; y < 16; ++y)
+                if (r0 + y < rows_here) to[y * 128] = o[y];
+        } else if (t < a.d) {
+            const uint32_t empty = rows->empty[half];
+            // row r's place in a query token's heads: after the last one, the next token's first
+            int in_token = (rt * kRows + r0) % plan.group;
+            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.o) + output_row(a, plan, b, hk, rt, r0) * a.d + t;
+#pragma unroll
+            for (int y = 0; y < 16; ++y) {
+                if (r0 + y < rows_here) *to = __float2bfloat16_rn(empty >> y & 1 ? 0.0f : o[y] * rows->keep_o[r0 + y]);
+                to += a.d;
+                if (++in_token == plan.group) {
+                    in_token = 0;
+                    to += (int64_t)(a.H_q - plan.group) * a.d;
+                }
             }
         }
         tc::tc_fence_before();                             // the next piece's products may overwrite the sums
@@ -716,11 +731,17 @@ attn::Plan attention_tc_plan(const CacheAttention& a) {
     return plan;
 }
 
+// A tile of 8 steps is the least that is cut, and a CTA's second start and end cost the time of a dozen.  Measured both ways:
+// 16 tiles (2,048 tokens), 32 items 32 us whole and 24 cut, 128 items 32 and 37, 512 items 85 and 102, 2,048 items 293 and 345;
+// 32 tiles, 256 items 76 and 87 us, lengths that differ 71 and 67.  Very few items are cut from 5 tiles on (8 items of 8
+// tiles: 21 us whole, 18 cut).
 int64_t attention_tc_grid(const CacheAttention& a, const attn::Plan& plan, int num_sms) {
-    const int64_t cap = ((int64_t)a.table_pages << a.page_shift) / kStep;
-    if (cap <= 4 * kTileSteps || (int64_t)a.B * plan.row_tiles > kMaxScan) return 0;
-    const int64_t all = (int64_t)a.B * plan.row_tiles * a.H_kv * (cap + plan.item_cost);
-    const int64_t most = (int64_t)num_sms * kCtas, useful = (all + kMinShare - 1) / kMinShare;
+    const int64_t cap = most_steps(a), items = (int64_t)a.B * plan.row_tiles * a.H_kv, most = (int64_t)num_sms * kCtas;
+    const bool few = 10 * items < most;
+    if (whole_items_pay(cap, items, most, 13 * kTileSteps, (few ? 4 : 32) * kTileSteps) ||
+        (int64_t)a.B * plan.row_tiles > kMaxScan)
+        return 0;
+    const int64_t useful = (items * (cap + plan.item_cost) + kMinShare - 1) / kMinShare;
     return useful < most ? useful : most;
 }
 
