@@ -11,8 +11,8 @@
 //
 // What bounds it: reading the codes, as long as the rows that share a head's
 // keys (T_q times H_q / H_kv) are few.  Measured with 8 heads of keys, 32 of queries, d = 128, bf16: a
-// million tokens 354 us, 6.1 TB/s; 256 sequences of up to 4096 tokens 192 us, 5.7 TB/s; 77 tokens
-// 4.4 us.  Beyond 16 rows the conversion of codes and the products bound it (537 MB of codes: 101 us under
+// million tokens 354 us, 6.1 TB/s; 256 sequences of up to 4096 tokens 189 us, 5.7 TB/s; 77 tokens
+// 4.0 us.  Beyond 16 rows the conversion of codes and the products bound it (537 MB of codes: 101 us under
 // 4 rows, 109 us under 16, 170 us under 32), which is where kda_cache_attention_tc.cu
 // takes over for bf16 rows of more than 64 channels.
 //

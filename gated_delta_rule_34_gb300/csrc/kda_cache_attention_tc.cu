@@ -2,7 +2,7 @@
 // tokens and prompts, whose rows share each head's keys.
 //
 // The mathematics is that of kda_cache_attention.cu.  With more than some 16 rows a head the
-// products there bound it (537 MB of codes under 32 rows: 170 us; here 141 us, 3.8 TB/s; 64 rows 330 and 250 us),
+// products there bound it (537 MB of codes under 32 rows: 170 us; here 135 us, 4.0 TB/s; 64 rows 330 and 241 us),
 // above all the conversion of every code to fp16.  Here the codes go to the tensor cores as they lie in
 // the cache, as e4m3 operands; what is not 8 bits is split instead:
 //
