@@ -16,6 +16,7 @@ constexpr int kStep = 16;             // tokens of a step; a page holds whole st
 constexpr int kMinShare = 16;         // steps below which no item is cut further
 constexpr int kJoinThreads = 256;
 constexpr int kJoinFew = 32;          // pieces up to which a warp joins a row
+constexpr int kAtOnce = 4;            // pieces that a warp loads at once
 constexpr int kMaxScan = 8192;        // (sequence, row tile) pairs that every CTA sums up
 constexpr float kWeightBits = 12.0f;  // log2 of what the largest weight is brought to
 constexpr float kSlack = 2.0f;        // log2 of how far scores may pass the reference

@@ -11,7 +11,7 @@
 //
 // What bounds it: reading the codes, as long as the rows that share a head's
 // keys (T_q times H_q / H_kv) are few.  Measured with 8 heads of keys, 32 of queries, d = 128, bf16: a
-// million tokens 354 us, 6.1 TB/s; 256 sequences of up to 4096 tokens 189 us, 5.7 TB/s; 77 tokens
+// million tokens 351 us, 6.1 TB/s; 256 sequences of up to 4096 tokens 188 us, 5.8 TB/s; 77 tokens
 // 4.0 us.  Beyond 16 rows the conversion of codes and the products bound it (537 MB of codes: 101 us under
 // 4 rows, 109 us under 16, 170 us under 32), which is where kda_cache_attention_tc.cu
 // takes over for bf16 rows of more than 64 channels.
@@ -635,13 +635,16 @@ attention_share_kernel(const CacheAttention a, const Plan plan) {
 // The pieces of the item that begins in CTA blockIdx.x's share and ends in a later
 // one, joined in order: the first from its slot, the later ones from slot 0.  Few
 // pieces: a warp a row, without a barrier; many: eight warps a row, each every
-// eighth piece, their sums joined in shared memory.
+// eighth piece, their sums joined in shared memory.  A piece's statistics and sums are
+// loaded together, the sums so far rescaled as they come, since what it takes is loads that wait for one another
+// (8 sequences of 1,501 tokens, 16 heads, fp32: 14.7 us; 16.2 with the largest of all statistics found first, 15.5 with
+// eight pieces at once, whose registers leave room for fewer CTAs).
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, 4)
 attention_join_kernel(const CacheAttention a, const Plan plan) {
     constexpr int WARPS = kJoinThreads / 32, PER = D / 32;
     __shared__ float4 o_s[WARPS][D / PER];
-    __shared__ float l_s[WARPS];
+    __shared__ float4 stat_s[WARPS];
     after_the_kernel_before();
     const int4 join = plan.joins[blockIdx.x];
     if (join.x < 0) return;
@@ -657,46 +660,59 @@ attention_join_kernel(const CacheAttention a, const Plan plan) {
         auto place = [&](int i) -> int64_t {
             return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? join.w : 0)) * plan.stored + r;
         };
-        float M = kLowest, MO = kLowest;
-        for (int i = lane; i < n; i += 32) {
-            const float4 s = plan.stats[place(i)];
-            M = fmaxf(M, s.x);
-            MO = fmaxf(MO, s.x - s.y);
-        }
+        // Sums (m, dm, l; x) join those so far, whose largest is M and, with the pages' scales, M - DM.
+        float o[4] = {}, M = kLowest, DM = 0.0f, L = 0.0f;
+        auto rise = [&](float m, float mo) {
+            const float m_new = fmaxf(M, m), dm_new = m_new - fmaxf(M - DM, mo);
+            const float keep = ex2(M - m_new + (dm_new - DM));
+            L *= ex2(M - m_new);
 #pragma unroll
-        for (int w = 16; w > 0; w >>= 1) {
-            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-            MO = fmaxf(MO, __shfl_xor_sync(0xffffffffu, MO, w));
-        }
-        const float DM = M - MO;
-        float o[4] = {}, L = 0.0f;
-#pragma unroll 8
-        for (int i = part; i < n; i += parts) {
-            const int64_t at = place(i);
-            const float4 s = plan.stats[at];
+            for (int c = 0; c < 4; ++c) o[c] *= keep;
+            M = m_new;
+            DM = dm_new;
+        };
+        auto add = [&](const float4& s, const float4& x) {
             const float f = ex2(s.x - M + (DM - s.y));
             L += s.z * ex2(s.x - M);
-            const float* from = plan.sums + at * D + PER * lane;
-            if constexpr (PER == 4) {
-                const float4 x = *reinterpret_cast<const float4*>(from);
-                o[0] += f * x.x, o[1] += f * x.y, o[2] += f * x.z, o[3] += f * x.w;
-            } else {
-                const float2 x = *reinterpret_cast<const float2*>(from);
-                o[0] += f * x.x, o[1] += f * x.y;
+            o[0] += f * x.x, o[1] += f * x.y, o[2] += f * x.z, o[3] += f * x.w;
+        };
+        for (int i0 = part; i0 < n; i0 += kAtOnce * parts) {
+            float4 s[kAtOnce], x[kAtOnce];
+            float m = kLowest, mo = kLowest;
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const int i = i0 + j * parts;
+                s[j] = make_float4(kLowest, 0.0f, 0.0f, 0.0f);
+                x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (i >= n) continue;
+                const int64_t at = place(i);
+                const float* from = plan.sums + at * D + PER * lane;
+                s[j] = plan.stats[at];
+                if constexpr (PER == 4) {
+                    x[j] = *reinterpret_cast<const float4*>(from);
+                } else {
+                    const float2 two = *reinterpret_cast<const float2*>(from);
+                    x[j].x = two.x, x[j].y = two.y;
+                }
             }
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                m = fmaxf(m, s[j].x);
+                mo = fmaxf(mo, s[j].x - s[j].y);
+            }
+            rise(m, mo);
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) add(s[j], x[j]);
         }
         if (!few) {
             o_s[warp][lane] = make_float4(o[0], o[1], o[2], o[3]);
-            if (lane == 0) l_s[warp] = L;
+            if (lane == 0) stat_s[warp] = make_float4(M, DM, L, 0.0f);
             __syncthreads();
             if (warp == 0) {
-                L = 0.0f;
-                o[0] = o[1] = o[2] = o[3] = 0.0f;
-#pragma unroll
-                for (int w = 0; w < WARPS; ++w) {
-                    const float4 x = o_s[w][lane];
-                    o[0] += x.x, o[1] += x.y, o[2] += x.z, o[3] += x.w;
-                    L += l_s[w];
+                for (int w = 1; w < WARPS; ++w) {
+                    const float4 s = stat_s[w];
+                    rise(s.x, s.x - s.y);
+                    add(s, o_s[w][lane]);
                 }
             }
             __syncthreads();
