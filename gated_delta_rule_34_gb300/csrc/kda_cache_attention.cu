@@ -767,8 +767,8 @@ Plan make_plan(const CacheAttention& a) {
 }
 
 // CTAs of the shared-out form; 0 where each item is one CTA's.  Measured both ways at 8 to 2,048 items of up to 256 to 4,096
-// tokens: with 32 steps (512 tokens) 8.8 us whole and 10.3 cut (32 items), 9.0 and 13.5 (128), 36 and 38 (1,024); with 128
-// steps 24 and 21 us (128), 64 and 56 (512), 176 and 191 (2,048); with 256 steps and lengths that differ 114 and 106 us (1,024).
+// tokens: with 32 steps (512 tokens) 8.4 us whole and 9.3 cut (32 items), 8.5 and 12.1 (128), 34 and 35 (1,024); with 128
+// steps 23 and 19 us (128), 65 and 54 (512), 175 and 184 (2,048); with 256 steps and lengths that differ 113 and 102 us (1,024).
 int64_t share_grid(const CacheAttention& a, const Plan& plan, int64_t most) {
     const int64_t cap = most_steps(a), items = (int64_t)a.B * plan.row_tiles * a.H_kv;
     if (whole_items_pay(cap, items, most, 32, 128) || (int64_t)a.B * plan.row_tiles > kMaxScan) return 0;

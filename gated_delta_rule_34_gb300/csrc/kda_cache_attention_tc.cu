@@ -732,9 +732,9 @@ attn::Plan attention_tc_plan(const CacheAttention& a) {
 }
 
 // A tile of 8 steps is the least that is cut, and a CTA's second start and end cost the time of a dozen.  Measured both ways:
-// 16 tiles (2,048 tokens), 32 items 32 us whole and 24 cut, 128 items 32 and 37, 512 items 85 and 102, 2,048 items 293 and 345;
-// 32 tiles, 256 items 76 and 87 us, lengths that differ 71 and 67.  Very few items are cut from 5 tiles on (8 items of 8
-// tiles: 21 us whole, 18 cut).
+// 16 tiles (2,048 tokens), 32 items 32 us whole and 23 cut, 128 items 32 and 37, 512 items 86 and 101, 2,048 items 294 and 343;
+// 32 tiles, 256 items 76 and 86 us, lengths that differ 72 and 66.  Very few items are cut from 5 tiles on (8 items of 8
+// tiles: 21 us whole, 17 cut).
 int64_t attention_tc_grid(const CacheAttention& a, const attn::Plan& plan, int num_sms) {
     const int64_t cap = most_steps(a), items = (int64_t)a.B * plan.row_tiles * a.H_kv, most = (int64_t)num_sms * kCtas;
     const bool few = 10 * items < most;
