@@ -5,8 +5,8 @@
 #include <climits>
 
 #include "kda_cache.cuh"
+#include "kda_cache_internal.h"
 #include "kda_chained.cuh"
-#include "kda_internal.h"
 #include "tc_util.cuh"
 
 namespace kda {

@@ -23,8 +23,8 @@
 // 255 us, 6.4 TB/s; 16 of up to 16384 tokens, 8 heads, read in 132 us, 6.5 TB/s; one token of each
 // of 256 sequences, 8 heads, written in 5.6 us, most of it loads that wait for one another.
 #include "kda_cache.cuh"
+#include "kda_cache_internal.h"
 #include "kda_chained.cuh"
-#include "kda_internal.h"
 
 namespace kda {
 

@@ -6,7 +6,7 @@
 #include <cmath>
 #include <cstdint>
 
-#include "kda_internal.h"
+#include "kda_cache_internal.h"
 
 namespace {
 
