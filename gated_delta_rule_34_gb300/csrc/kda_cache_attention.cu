@@ -109,6 +109,14 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// (x, y) += (a, b), each rounded: one instruction.
+__device__ __forceinline__ void add_pair(float& x, float& y, float a, float b) {
+    asm("{\n\t.reg .b64 s, t;\n\tmov.b64 s, {%0, %1};\n\tmov.b64 t, {%2, %3};\n\tadd.rn.f32x2 s, s, t;\n\t"
+        "mov.b64 {%0, %1}, s;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+
 // An 8 x 8 matrix of 16-bit values, a row a quad, transposed.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     uint32_t y;
@@ -586,7 +594,9 @@ struct Piece {
         __syncthreads();
     }
 
-    // acc[y0], acc[y0 + 1] += four channels of four tokens x weights.
+    // acc[y0], acc[y0 + 1] += four channels of four tokens x weights.  The products' own sums are cut off, not rounded, and
+    // all the same way: sums kept in them over 131,072 tokens of one sign came out up to 8.5e-4 too small.  So a product
+    // holds one step's tokens (and both pieces of a weight), and its sum is added to the others' by rounded additions.
     template <int N, int PCS>
     static __device__ __forceinline__ void add_values(float (&acc)[N][NT][4], int y0, const uint32_t (&pf)[PCS][NT][2],
                                                       uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3) {
@@ -598,9 +608,13 @@ struct Piece {
 #pragma unroll
         for (int y = 0; y < 2; ++y)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) {
+                float part[4] = {};
 #pragma unroll
-                for (int pc = 0; pc < PCS; ++pc) mma16816(acc[y0 + y][n], f[y], pf[pc][n][0], pf[pc][n][1]);
+                for (int pc = PCS - 1; pc >= 0; --pc) mma16816(part, f[y], pf[pc][n][0], pf[pc][n][1]);
+                add_pair(acc[y0 + y][n][0], acc[y0 + y][n][1], part[0], part[1]);
+                add_pair(acc[y0 + y][n][2], acc[y0 + y][n][3], part[2], part[3]);
+            }
     }
 
 };
