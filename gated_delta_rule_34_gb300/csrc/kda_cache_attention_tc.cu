@@ -26,6 +26,10 @@
 // score passes them by more than a factor of 128, which a vote of the four warps of its row tells; the sums in
 // TMEM are then multiplied in place.  (A move costs some 3000 cycles; with a factor of 4 every third tile had one.)
 //
+// The products' own sums are cut off, not rounded, all the same way: values of one sign over 131,072 tokens came out 1.2e-4
+// too small, and more so with the length.  So they hold kRun tiles (256 products, cut off by less than 2^-16 in all), then go to
+// sums in TMEM by rounded additions.  (4 x 65,536 tokens under 32 rows: 126.6 us, 126.0 without.)
+//
 // NaN that a row does not see (0 times NaN is NaN): see Softmax::mend_values.  A wait that gives up
 // (about 2 s) makes the outputs of the item and of the CTA's later ones NaN.
 #include "kda_attention_common.cuh"
@@ -83,8 +87,10 @@ struct Barriers {
     uint32_t tmem;
 };
 
-constexpr uint32_t kTmemCols = 256;        // S 2 x 32, O 128
+constexpr uint32_t kTmemCols = 256;        // S 2 x 32, sums 32, O 128
+constexpr uint32_t kTmemSums = 64;
 constexpr uint32_t kTmemO = 128;
+constexpr int kRun = 64;                   // tiles that O sums up before it goes to the rounded sums
 
 // kind::f8f6f4, fp32 sums: M x N, A e4m3; B e4m3 (0) or e5m2 (1); bits 15 and 16: A, B with M, N along
 // the rows.
@@ -409,7 +415,8 @@ struct Softmax {
 
     // The references move to the largest of this tile's scores (the first tile: there are none before).
     // s: scores less m, -inf where unseen, and so again afterwards; this thread's rows start at r0.
-    __device__ __forceinline__ void move_references(float (&s)[kMine], float e, float (&l)[kMine], int r0, bool first) {
+    __device__ __forceinline__ void move_references(float (&s)[kMine], float e, float (&l)[kMine], int r0, int i) {
+        const bool first = i == 0;
         const int lane = threadIdx.x & 31, quarter = threadIdx.x >> 5 & 3;
         Rows* rows = c.rows;
         auto most = [](float x, float y) { return fmaxf(x, y); };
@@ -456,17 +463,58 @@ struct Softmax {
         wait(&c.bar->pv_done, (tile_n - 1) & 1);           // the sums rest until this tile's weights are told
         tc::tc_fence_after();
         if (bad) return;
-        const uint32_t o = c.tmem + kTmemO + r0 + ((uint32_t)(32 * quarter) << 16);
+        const uint32_t at = c.tmem + r0 + ((uint32_t)(32 * quarter) << 16);
+        const int parts = i > kRun ? 5 : 4;                // (the run that ends at this tile is not in the sums yet)
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < parts; ++k) {
+            const uint32_t part = at + (k < 4 ? kTmemO + kRows * k : kTmemSums);
             float v[16];
             uint32_t out[16];
-            tc::tmem_ld16(o + kRows * k, v);
+            tc::tmem_ld16(part, v);
             loaded(v);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) out[i] = __float_as_uint(v[i] * rows->keep_o[r0 + i]);
-            tc::tmem_st16(o + kRows * k, out);
+            for (int r = 0; r < 16; ++r) out[r] = __float_as_uint(v[r] * rows->keep_o[r0 + r]);
+            tc::tmem_st16(part, out);
         }
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+    }
+
+    // This thread's channel of its rows, from the four pieces' sums and the rounded ones.  (Unrolled, it costs the loop over
+    // the tiles registers: 4 x 65,536 tokens under 32 rows 132.6 us, 126.6 so.)
+    static __device__ __forceinline__ void read_sums(uint32_t at, bool summed, float (&o)[kMine]) {
+        tc::tmem_ld16(at + kTmemO, o);
+        loaded(o);
+#pragma unroll 1
+        for (int k = 1; k < 4; ++k) {
+            float x[kMine];
+            tc::tmem_ld16(at + kTmemO + kRows * k, x);
+            loaded(x);
+            const float part = k == 1 ? 0.25f : k == 2 ? 0.0625f : 0.015625f;
+#pragma unroll
+            for (int r = 0; r < kMine; ++r) o[r] = fmaf(x[r], part, o[r]);
+        }
+        if (summed) {
+            float x[kMine];
+            tc::tmem_ld16(at + kTmemSums, x);
+            loaded(x);
+#pragma unroll
+            for (int r = 0; r < kMine; ++r) o[r] += x[r];
+        }
+    }
+
+    // What O holds, all its products ended, goes to the rounded sums, and O begins again from zeros.  (Inline 127.6 us.)
+    static __device__ __noinline__ void add_run(uint32_t at, bool summed) {
+        float o[kMine];
+        read_sums(at, summed, o);
+        uint32_t out[kMine];
+#pragma unroll
+        for (int r = 0; r < kMine; ++r) out[r] = __float_as_uint(o[r]);
+        tc::tmem_st16(at + kTmemSums, out);
+#pragma unroll
+        for (int r = 0; r < kMine; ++r) out[r] = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tc::tmem_st16(at + kTmemO + kRows * k, out);
         tc::tmem_wait_st();
         tc::tc_fence_before();
     }
@@ -535,8 +583,12 @@ struct Softmax {
                         if ((unset >> r & 1) && s[r] != -INFINITY) beyond = INFINITY;
                 }
             }
-            if (vote(beyond > kFar || i == 0, kBarHalf + half, kSoftmax / 2)) move_references(s, e, l, r0, i == 0);
+            if (vote(beyond > kFar || i == 0, kBarHalf + half, kSoftmax / 2)) move_references(s, e, l, r0, i);
             if (i > 0) wait(&c.bar->pv_done, (n - 1) & 1);   // the weights before have been read
+            if (i > 0 && i % kRun == 0 && !bad) {
+                tc::tc_fence_after();
+                add_run(c.tmem + lanes + r0, i > kRun);
+            }
 
             // Weights: the pieces of 16 rows are 16 bytes each.
             uint32_t piece[4][4];
@@ -600,20 +652,9 @@ struct Softmax {
             }
         }
         float o[16];
-        const uint32_t from_o = c.tmem + kTmemO + lanes + r0;
-        tc::tmem_ld16(from_o, o);
-        loaded(o);
+        read_sums(c.tmem + lanes + r0, n_tiles > kRun, o);
 #pragma unroll
         for (int y = 0; y < 16; ++y) o[y] *= kToPlan;
-#pragma unroll
-        for (int k = 1; k < 4; ++k) {
-            float x[16];
-            tc::tmem_ld16(from_o + kRows * k, x);
-            loaded(x);
-            const float part = kToPlan * (k == 1 ? 0.25f : k == 2 ? 0.0625f : 0.015625f);
-#pragma unroll
-            for (int y = 0; y < 16; ++y) o[y] = fmaf(x[y], part, o[y]);
-        }
         tc::named_bar_sync(kBarSoftmax, kSoftmax);
 #pragma unroll
         for (int y = 0; y < 16; ++y)
