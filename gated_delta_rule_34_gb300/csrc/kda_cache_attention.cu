@@ -190,10 +190,12 @@ struct Piece {
             for (int j = 0; j < S::KC; ++j)
 #pragma unroll
                 for (int w = 0; w < 16; ++w)
-                    amax = fmaxf(amax, finite_abs(to_f32(reinterpret_cast<const T*>(raw[j])[w])));
+                    amax = fmaxf(amax, fabsf(to_f32(reinterpret_cast<const T*>(raw[j])[w])));
             amax = quad_max(amax);
-            // 2^ex <= amax < 2^(ex + 1): times 2^(14 - ex), under fp16's largest value
-            int ex = (int)(__float_as_uint(amax) >> 23) - 127;
+            // 2^ex <= amax < 2^(ex + 1): times 2^(14 - ex), under fp16's largest value.  A row with an infinity: its scores
+            // are infinite or no numbers whatever its finite channels hold, so these count as zeros, under no scale.
+            const bool infinite = amax == INFINITY;
+            int ex = infinite ? 14 : (int)(__float_as_uint(amax) >> 23) - 127;
             ex = ex < -112 ? -112 : ex;
             const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
             if (c == 0)
@@ -207,9 +209,13 @@ struct Piece {
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         const T* e = reinterpret_cast<const T*>(raw[j]) + 8 * half + 2 * w;
-                        const float lo = to_f32(e[0]) * up, hi = to_f32(e[1]) * up;
+                        float lo = to_f32(e[0]) * up, hi = to_f32(e[1]) * up;
+                        if (infinite) {
+                            lo = fabsf(lo) < INFINITY ? 0.0f : lo;
+                            hi = fabsf(hi) < INFINITY ? 0.0f : hi;
+                        }
                         bits[w] = half2_bits(lo, hi);
-                        rest[w] = half2_rest(lo, hi, bits[w]);
+                        rest[w] = infinite ? 0 : half2_rest(lo, hi, bits[w]);
                     }
                     const int at = ((rows8 * S::KC + j) * 2 + half) * 32 + lane;
                     to_s[at] = make_uint4(bits[0], bits[1], bits[2], bits[3]);
