@@ -342,23 +342,26 @@ struct Softmax {
             raw[x] = real && 16 * part < a.d ? reinterpret_cast<const uint4*>(q)[x] : make_uint4(0, 0, 0, 0);
         const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(raw);
         float amax = 0.0f;
-        bool finite = true;
+        bool number = true;
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
             const float f = fabsf(to_f32(e[x]));
-            finite &= f <= 3.4028234663852886e38f;
-            amax = fmaxf(amax, finite_abs(f));
+            number &= f <= INFINITY;
+            amax = fmaxf(amax, f);
         }
 #pragma unroll
         for (int w = 1; w < 8; w <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, w));
-        finite = (__ballot_sync(0xffffffffu, !finite) >> (threadIdx.x & 24) & 255u) == 0;
-        // 2^ex <= amax < 2^(ex + 1): times 2^(14 - ex), under e5m2's largest value
-        int ex = (int)(__float_as_uint(amax) >> 23) - 127;
+        number = (__ballot_sync(0xffffffffu, !number) >> (threadIdx.x & 24) & 255u) == 0;
+        // 2^ex <= amax < 2^(ex + 1): times 2^(14 - ex), under e5m2's largest value.  A row with an infinity: its scores are
+        // infinite or no numbers whatever its finite channels hold, so these count as zeros, under no scale.  A row with a
+        // NaN has it from its factor.
+        const bool infinite = amax == INFINITY;
+        int ex = infinite ? 14 : (int)(__float_as_uint(amax) >> 23) - 127;
         ex = ex < -112 ? -112 : ex;
         const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
         float rest[16];
 #pragma unroll
-        for (int x = 0; x < 16; ++x) rest[x] = finite ? to_f32(e[x]) * up : 0.0f;
+        for (int x = 0; x < 16; ++x) rest[x] = number ? to_f32(e[x]) * up : 0.0f;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             uint32_t word[4];
@@ -369,13 +372,22 @@ struct Softmax {
                 from_e5m2x4(word[w], f);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) rest[4 * w + x] -= f[x];
+                if (infinite) {                            // its infinities alone: 7c
+                    uint32_t codes = 0;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t bits = k == 0 ? __float_as_uint(to_f32(e[4 * w + x])) : 0;
+                        if (number && (bits & 0x7fffffffu) == 0x7f800000u) codes |= (bits >> 24 & 0x80u | 0x7cu) << (8 * x);
+                    }
+                    word[w] = codes;
+                }
             }
             *reinterpret_cast<uint4*>(c.sm + kQueriesAt + tc::sw128(k * kRows + row, part)) =
                 make_uint4(word[0], word[1], word[2], word[3]);
         }
         if (part == 0) {
-            c.rows->factor[row] = finite ? a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + ex - 14) << 23)
-                                         : NAN;
+            c.rows->factor[row] = number ? a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + ex - 14) << 23)
+                                          : NAN;
             c.rows->m[row] = 0.0f;                         // until the first tile's scores
         }
         if (part < 4) c.rows->nan[row][part] = 0;

@@ -15,9 +15,9 @@ import gated_delta_rule_34_gb300 as kda
 pytestmark = pytest.mark.gpu
 
 BF16, F32 = torch.bfloat16, torch.float32
-# fp32; bf16 with few rows a head, and with more than 16 of narrow heads; whole items and shares
+# fp32; bf16 with few rows a head, and with more than 16 of narrow and of wide heads; whole items and shares
 CASES = [(F32, 1, 2, 128, 200), (F32, 5, 4, 64, 5000), (F32, 12, 4, 80, 90), (BF16, 1, 2, 128, 200), (BF16, 4, 4, 64, 5000),
-         (BF16, 9, 4, 64, 200)]
+         (BF16, 9, 4, 64, 200), (BF16, 9, 4, 128, 200), (BF16, 12, 4, 96, 9000), (BF16, 70, 1, 128, 300)]
 
 
 def _other_rows(o, lse, want, want_lse):
