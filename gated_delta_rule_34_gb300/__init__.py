@@ -8,7 +8,8 @@ nothing, so the seeded input generator (``.inputs``) can be used without a GPU.
 """
 from .api import (KDAError, auto_segments, chunk_prefill, chunk_prefill_from_host,  # noqa: F401
                   chunk_prefill_segmented, chunk_prefill_static_workspace, decode_step, gate, lib, library_path,
-                  prefill_path, selftest_bounded_wait, set_profile_events, spec_commit,
+                  prefill_path, selftest_attention_stall, selftest_bounded_wait,
+                  set_profile_events, spec_commit,
                   segmented_workspace_size, spec_verify, static_workspace_status,
                   workspace_size)
 from .cache import (PagedCache, cache_attention, cache_attention_workspace_size, cache_new,  # noqa: F401
@@ -16,7 +17,8 @@ from .cache import (PagedCache, cache_attention, cache_attention_workspace_size,
 
 __all__ = ["KDAError", "auto_segments", "chunk_prefill", "chunk_prefill_segmented",
            "segmented_workspace_size", "chunk_prefill_from_host", "chunk_prefill_static_workspace",
-           "decode_step", "gate", "lib", "library_path", "prefill_path", "selftest_bounded_wait",
+           "decode_step", "gate", "lib", "library_path", "prefill_path", "selftest_attention_stall",
+           "selftest_bounded_wait",
            "set_profile_events", "spec_commit", "spec_verify", "static_workspace_status",
            "workspace_size", "PagedCache", "cache_attention", "cache_attention_workspace_size",
            "cache_new", "cache_read", "cache_write", "rotary", "rotary_frequencies"]

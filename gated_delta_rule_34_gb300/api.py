@@ -71,6 +71,8 @@ def _declare(lib):
     lib.kda_set_profile_events.restype = i32
     lib.kda_selftest_bounded_wait.argtypes = [vp, i32, vp]
     lib.kda_selftest_bounded_wait.restype = i32
+    lib.kda_selftest_attention_stall.argtypes = [i32, i32, i32]
+    lib.kda_selftest_attention_stall.restype = i32
     lib.kda_chunk_prefill_segmented.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i64, i32,
                                                 i32, i32, i32, i32, i32, vp, sz, vp]
     lib.kda_chunk_prefill_segmented.restype = i32
@@ -334,6 +336,13 @@ def selftest_bounded_wait(status: torch.Tensor, arrive: bool) -> None:
     with _on(status.device):
         _check(lib().kda_selftest_bounded_wait(_ptr(status), int(bool(arrive)),
                                                _stream(status.device)))
+
+
+def selftest_attention_stall(loads: int = 0, tiles: int = 0, wait_us: int = 0) -> None:
+    """kda_selftest_attention_stall: later cache_attention calls of this thread with many rows a head stop after
+    ``loads`` tiles loaded or ``tiles`` tiles multiplied in a CTA, and their waits run out after ``wait_us``
+    microseconds; 0 (no arguments) switches it off."""
+    _check(lib().kda_selftest_attention_stall(int(loads), int(tiles), int(wait_us)))
 
 
 def chunk_prefill_static_workspace(q, k, v, z, beta, A, initial_state=None, cu_seqlens=None,

@@ -22,6 +22,13 @@ constexpr float kWeightBits = 12.0f;  // log2 of what the largest weight is brou
 constexpr float kSlack = 2.0f;        // log2 of how far scores may pass the reference
 constexpr float kLowest = -3.402823466e38f;   // the reference before any score
 
+// Where the many-row kernel's loaders and products stop (a self-test's; else never), and the limit of its waits.
+struct Stall {
+    int loads = INT_MAX;     // tiles that a CTA's loaders load
+    int tiles = INT_MAX;     // tiles of which a CTA's products are issued
+    int wait_us = 2000000;
+};
+
 struct Plan {
     int group;          // query heads of a head of keys
     int rows;           // T_q * group
@@ -33,6 +40,7 @@ struct Plan {
     float* sums;        // [grid][2][stored][D]
     float4* stats;      // [grid][2][stored]: m, dm, l
     int4* joins;        // [grid]: pair (sequence, row tile), head, last CTA, slot; pair < 0: none
+    Stall stall;
 };
 
 // What a row tile of a sequence sees, in steps.

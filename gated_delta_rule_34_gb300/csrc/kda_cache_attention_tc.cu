@@ -30,8 +30,12 @@
 // too small, and more so with the length.  So they hold kRun tiles (256 products, cut off by less than 2^-16 in all), then go to
 // sums in TMEM by rounded additions.  (4 x 65,536 tokens under 32 rows: 126.6 us, 126.0 without.)
 //
-// NaN that a row does not see (0 times NaN is NaN): see Softmax::mend_values.  A wait that gives up
-// (about 2 s) makes the outputs of the item and of the CTA's later ones NaN.
+// NaN that a row does not see (0 times NaN is NaN): see Softmax::mend_values.
+//
+// A wait that gives up (about 2 s) makes the outputs of the item and of the CTA's later ones NaN.  The lanes of a warp give up
+// together, since what follows a wait is done by whole warps (loads from TMEM, shuffles); a warp that gave up waits no
+// more, but still arrives where others wait; and TMEM is given back after the end of all products that were issued, by a barrier of
+// their own.  kda_selftest_attention_stall has them run out.
 #include "kda_attention_common.cuh"
 
 namespace kda {
@@ -49,8 +53,10 @@ constexpr int kSoftmax = 256;              // threads of warps 0-7; then the loa
 constexpr int kLoaders = 64;               // eight rows at a time
 constexpr int kThreads = kSoftmax + 128;   // (whole warpgroups, for setmaxnreg: the last warp has no role)
 constexpr int kIssuerWarp = (kSoftmax + kLoaders) / 32;
-// Registers: 80 a thread at launch, then 96 for softmax and 40 for the others: 256 x 96 + 128 x 40 <= 384 x 80.
-constexpr int kSoftmaxRegs = 96, kOtherRegs = 40;
+// Registers: 80 a thread at launch, then 96 for softmax and 48 for the others, all there are: 256 x 96 + 128 x 48 = 384 x 80.
+// (40 for the others: their loops spill, 4 x 65,536 tokens under 32 rows 129.9 us, 123.1 so.)
+constexpr int kSoftmaxRegs = 96, kOtherRegs = 48;
+static_assert(kSoftmax * kSoftmaxRegs + (kThreads - kSoftmax) * kOtherRegs <= kThreads * 80, "registers at launch");
 constexpr int kMine = kRows / 2;           // rows of a softmax thread
 constexpr float kBits = 8.0f, kFar = 7.0f;    // log2 of the largest weight at its reference, and of how far above it
 constexpr float kToPlan = 16.0f;           // 2^(kWeightBits - kBits)
@@ -83,7 +89,7 @@ struct alignas(16) Rows {
 static_assert(sizeof(Rows) <= kRowsBytes, "Rows");
 
 struct Barriers {
-    uint64_t full[kSlots], empty[kSlots], s_full[2], s_free[2], w_full, pv_done, q_full;
+    uint64_t full[kSlots], empty[kSlots], s_full[2], s_free[2], w_full, pv_done, q_full, drained;
     uint32_t tmem;
 };
 
@@ -172,6 +178,17 @@ __device__ __forceinline__ void loaded(float (&v)[16]) {
                  : "memory");
 }
 
+// tc::mbar_wait with a limit of the caller's, in microseconds.
+__device__ __forceinline__ bool wait_up_to(uint64_t* bar, uint32_t parity, int limit) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = tc::global_ns();
+    for (uint32_t i = 0; i < (1u << 30); ++i) {
+        if (tc::mbar_try_wait(bar, parity)) return true;
+        if ((i & 15u) == 15u && tc::global_ns() - t0 > 1000ull * limit) break;
+    }
+    return false;
+}
+
 struct Cta {
     const CacheAttention& a;
     const Plan& plan;
@@ -216,7 +233,8 @@ struct Loader {
 #pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
                 const int slot = next % kSlots;
-                if (next >= kSlots && !tc::mbar_wait(&c.bar->empty[slot], (next / kSlots - 1) & 1)) {
+                if (next >= kSlots && !__all_sync(0xffffffffu, wait_up_to(&c.bar->empty[slot], (next / kSlots - 1) & 1,
+                                                                         c.plan.stall.wait_us))) {
                     dead = true;
                     break;
                 }
@@ -264,11 +282,12 @@ struct Issuer {
     bool dead = false;
 
     __device__ __forceinline__ void wait(uint64_t* b, uint32_t parity) {
-        if (!dead && !tc::mbar_wait(b, parity)) dead = true;
+        if (!dead && !wait_up_to(b, parity, c.plan.stall.wait_us)) dead = true;
     }
     // S[n & 1] = K (q1 + q2 + q3)^T of tile n.
     __device__ __forceinline__ void scores(int n) {
         const int j = 2 * n, slot = j % kSlots;
+        if (n >= c.plan.stall.tiles) dead = true;
         wait(&c.bar->full[slot], (j / kSlots) & 1);
         if (n >= 2) wait(&c.bar->s_free[n & 1], ((n >> 1) - 1) & 1);
         if (dead) return;
@@ -310,9 +329,10 @@ struct Issuer {
         }
         tile_n += n;
     }
-    // Every product issued has ended (the last pv_done), so that TMEM may go.
+    // Every product issued has ended, whether or not a wait gave up before, so that TMEM may go.
     __device__ __forceinline__ void finish() {
-        if (tile_n > 0) wait(&c.bar->pv_done, (tile_n - 1) & 1);
+        tc::mma_commit(&c.bar->drained);
+        tc::mbar_wait(&c.bar->drained, 0);
     }
 };
 
@@ -320,11 +340,11 @@ struct Issuer {
 struct Softmax {
     Cta c;
     int tile_n = 0;
-    bool bad = false;                      // a wait of this thread gave up: it waits no more, its numbers are none
+    bool bad = false;                      // a wait of this warp gave up: it waits no more, its numbers are none
     bool dead = false;                     // some thread's did, as found at the piece's end: the same in all
 
     __device__ __forceinline__ void wait(uint64_t* b, uint32_t parity) {
-        if (!bad && !dead && !tc::mbar_wait(b, parity)) bad = true;
+        if (!bad && !dead && !__all_sync(0xffffffffu, wait_up_to(b, parity, c.plan.stall.wait_us))) bad = true;
     }
 
     // The item's queries: eight threads a row, 16 channels each.
@@ -714,6 +734,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_tc_kernel(const Cac
         tc::mbar_init(&bar->w_full, kSoftmax);
         tc::mbar_init(&bar->pv_done, 1);
         tc::mbar_init(&bar->q_full, kSoftmax);
+        tc::mbar_init(&bar->drained, 1);
         tc::fence_mbar_init();
     }
     if (warp == kIssuerWarp) tc::tmem_alloc<kTmemCols>(&bar->tmem);
@@ -744,7 +765,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_tc_kernel(const Cac
         if (warp < kIssuerWarp) {
             Loader role{cta};
             pieces([&](int pair, int hk, const Tile& tile, int from, int to, int, bool) {
-                if (!role.dead) role.piece(pair, hk, tile, from, to);
+                if (role.dead) return;
+                const int left = plan.stall.loads - role.next / 2, most = from + (left < 1 << 24 ? left : 1 << 24) * kTileSteps;
+                role.piece(pair, hk, tile, from, to < most ? to : most);
+                if (most < to) role.dead = true;
             });
             role.finish();
         } else if (threadIdx.x == 32 * kIssuerWarp) {
@@ -798,8 +822,13 @@ int64_t attention_tc_grid(const CacheAttention& a, const attn::Plan& plan, int n
     return useful < most ? useful : most;
 }
 
+namespace {
+thread_local Stall stall;
+}
+
 cudaError_t run_attention_tc(const CacheAttention& a, void* workspace, cudaStream_t stream, int num_sms) {
     Plan plan = attention_tc_plan(a);
+    plan.stall = stall;
     const int64_t grid = attention_tc_grid(a, plan, num_sms);
     if (grid == 0) {
         const int64_t items = (int64_t)a.B * plan.row_tiles * a.H_kv;
@@ -815,3 +844,14 @@ cudaError_t run_attention_tc(const CacheAttention& a, void* workspace, cudaStrea
 }
 
 }  // namespace kda
+
+extern "C" kda_status kda_selftest_attention_stall(int loads, int tiles, int wait_us) {
+    if (wait_us == 0) {
+        kda::stall = kda::attn::Stall{};
+        return kda::report(KDA_OK, "%s", "");
+    }
+    if (loads < 0 || tiles < 0 || wait_us < 0 || wait_us > 2000000)
+        return kda::report(KDA_ERR_INVALID_ARG, "bad arguments loads=%d tiles=%d wait_us=%d", loads, tiles, wait_us);
+    kda::stall = kda::attn::Stall{loads, tiles, wait_us};
+    return kda::report(KDA_OK, "%s", "");
+}

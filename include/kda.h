@@ -528,6 +528,18 @@ kda_status kda_set_profile_events(cudaEvent_t *events, int n_events);
  */
 kda_status kda_selftest_bounded_wait(uint32_t *status, int arrive, cudaStream_t stream);
 
+/*
+ * kda_selftest_attention_stall -- the same for kda_cache_attention with more
+ * than 16 bf16 rows a head of more than 64 channels.  While set, every later
+ * such call made on this thread stops short in each CTA: its loaders after
+ * `loads` tiles of 128 tokens, its products after `tiles` tiles; its waits
+ * then run out after wait_us microseconds (1 to 2,000,000) instead of 2 s.
+ * The call returns, with NaN where what is missing was needed, and the context
+ * stays usable.  wait_us == 0 switches it off.
+ * Returns KDA_ERR_INVALID_ARG for other arguments.
+ */
+kda_status kda_selftest_attention_stall(int loads, int tiles, int wait_us);
+
 #ifdef __cplusplus
 }
 #endif
