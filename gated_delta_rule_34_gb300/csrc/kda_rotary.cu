@@ -8,9 +8,10 @@
 // The angle.  p f_i in 32 bits has lost the turn's fraction by p = 2^20, so the
 // angle is kept as a fraction of a turn in 64-bit fixed point: f_i / 2 pi (its
 // whole part dropped) becomes a multiple of 2^-64, the product with p wraps
-// modulo one turn by itself, and the top 32 bits go to sincospif.  One 64-bit
+// modulo one turn by itself.  The nearest quarter is taken from the top 32 bits, of what remains (an eighth of a turn at
+// most) cos and sin are taken at its first 24 bits and corrected by the others: (c - s x, s + c x).  One 64-bit
 // multiply an angle and three 64-bit float operations; the angle is off by at
-// most 2^-32 turns plus p 2^-53.
+// most 2^-32 turns plus p 2^-53.  (The top 32 bits as one fp32 number: off by up to 2^-26 turns near half a turn.)
 //
 // The split.  Bound by memory: every element is read and written once.  A CTA
 // takes a few tokens with all their heads and works out their rot / 2 angles once
@@ -45,9 +46,15 @@ __device__ __forceinline__ float2 rotary_angle(double turns_per_position, int32_
     const double frac = turns_per_position - floor(turns_per_position);
     const uint64_t fixed = __double2ull_rz(frac * 18446744073709551616.0);
     const uint64_t phase = fixed * (uint64_t)(int64_t)position;
+    const uint32_t top = (uint32_t)(phase >> 32), quarter = (top + 0x20000000u) >> 30;
+    const int32_t rest = (int32_t)(top - (quarter << 30));                 // of 2^-32 turns, within 2^29
+    const float first = (float)rest;
+    const float more = (float)(rest - (int32_t)first) * 1.4629180792671596e-9f;   // 2 pi 2^-32
     float s, c;
-    sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31
-    return make_float2(c, s);
+    sincospif(first * 4.656612873077393e-10f, &s, &c);                     // 2^-31
+    const float cx = fmaf(-s, more, c), sx = fmaf(c, more, s);
+    const float x = quarter & 1 ? sx : cx, y = quarter & 1 ? cx : sx;
+    return make_float2(quarter + 1 & 2 ? -x : x, quarter & 2 ? -y : y);
 }
 
 // A vector of N elements of T as one load or store.
