@@ -460,15 +460,17 @@ struct Piece {
                         const bool seen[2] = {(sight >> (4 * n + r) & 1) != 0, (sight >> (4 * n + 2 + r) & 1) != 0};
                         const float top = column_max(fmaxf(seen[0] ? sc[n][r] * f : -INFINITY,
                                                            seen[1] ? sc[n][2 + r] * f : -INFINITY));
+                        // (Differences of the large numbers first, of the products as rounded for `top`: with scores beyond
+                        // 2^23 in size, whose last places are whole numbers, weights would pass fp16's range otherwise.)
                         const float m_new = fmaxf(m[n][r], top);
-                        const float dm_new = m_new - fmaxf(m[n][r] - dm[n][r], top + e);
+                        const float dm_new = -fmaxf((m[n][r] - m_new) - dm[n][r], (top - m_new) + e);
                         keep[r] = ex2(m[n][r] - m_new + (dm_new - dm[n][r]));
                         l[n][r] *= ex2(m[n][r] - m_new);
                         m[n][r] = m_new;
                         dm[n][r] = dm_new;
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            x[n][2 * h + r] = seen[h] ? fmaf(sc[n][2 * h + r], f, -m_new) : -INFINITY;
+                            x[n][2 * h + r] = seen[h] ? __fsub_rn(__fmul_rn(sc[n][2 * h + r], f), m_new) : -INFINITY;
                     }
 #pragma unroll
                     for (int y = 0; y < S::TILES; ++y)
@@ -569,15 +571,15 @@ struct Piece {
         const int rows_here = rows_of_tile(plan, rt);
         for (int u = threadIdx.x; u < rows_here * (D / 4); u += kThreads) {
             const int r = u / (D / 4), ch = u % (D / 4) * 4;
-            float M = kLowest, MO = kLowest, L = 0.0f;
+            float M = kLowest, DM = INFINITY, L = 0.0f;
             float4 stat[S::NG];
 #pragma unroll
             for (int i = 0; i < S::NG; ++i) {
                 stat[i] = stat_s[i * S::ROWS + r];
                 M = fmaxf(M, stat[i].x);
-                MO = fmaxf(MO, stat[i].x - stat[i].y);
             }
-            const float DM = M - MO;
+#pragma unroll
+            for (int i = 0; i < S::NG; ++i) DM = fminf(DM, stat[i].y + (M - stat[i].x));
             float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int i = 0; i < S::NG; ++i) {
@@ -680,10 +682,11 @@ attention_join_kernel(const CacheAttention a, const Plan plan) {
         auto place = [&](int i) -> int64_t {
             return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? join.w : 0)) * plan.stored + r;
         };
-        // Sums (m, dm, l; x) join those so far, whose largest is M and, with the pages' scales, M - DM.
+        // Sums (m, dm, l; x) join those so far, whose largest is M and, with the pages' scales, M - DM.  To M and DM from
+        // m at least M and the least of dm over what joins, as seen from m.
         float o[4] = {}, M = kLowest, DM = 0.0f, L = 0.0f;
-        auto rise = [&](float m, float mo) {
-            const float m_new = fmaxf(M, m), dm_new = m_new - fmaxf(M - DM, mo);
+        auto rise = [&](float m_new, float dm) {
+            const float dm_new = fminf(DM + (m_new - M), dm);
             const float keep = ex2(M - m_new + (dm_new - DM));
             L *= ex2(M - m_new);
 #pragma unroll
@@ -698,7 +701,7 @@ attention_join_kernel(const CacheAttention a, const Plan plan) {
         };
         for (int i0 = part; i0 < n; i0 += kAtOnce * parts) {
             float4 s[kAtOnce], x[kAtOnce];
-            float m = kLowest, mo = kLowest;
+            float m = M, dm = INFINITY;
 #pragma unroll
             for (int j = 0; j < kAtOnce; ++j) {
                 const int i = i0 + j * parts;
@@ -716,11 +719,10 @@ attention_join_kernel(const CacheAttention a, const Plan plan) {
                 }
             }
 #pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) {
-                m = fmaxf(m, s[j].x);
-                mo = fmaxf(mo, s[j].x - s[j].y);
-            }
-            rise(m, mo);
+            for (int j = 0; j < kAtOnce; ++j) m = fmaxf(m, s[j].x);
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) dm = fminf(dm, s[j].y + (m - s[j].x));
+            rise(m, dm);
 #pragma unroll
             for (int j = 0; j < kAtOnce; ++j) add(s[j], x[j]);
         }
@@ -731,7 +733,8 @@ attention_join_kernel(const CacheAttention a, const Plan plan) {
             if (warp == 0) {
                 for (int w = 1; w < WARPS; ++w) {
                     const float4 s = stat_s[w];
-                    rise(s.x, s.x - s.y);
+                    const float m = fmaxf(M, s.x);
+                    rise(m, s.y + (m - s.x));
                     add(s, o_s[w][lane]);
                 }
             }
