@@ -451,6 +451,7 @@ struct Piece {
                 for (int r = 0; r < 2; ++r)
                     beyond = fmaxf(beyond, fmaxf(x[n][r], x[n][2 + r]) + fmaxf(dm[n][r] + e, 0.0f));
             if (__any_sync(0xffffffffu, beyond > kSlack)) {
+                bool large = false;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float keep[2];
@@ -460,9 +461,8 @@ struct Piece {
                         const bool seen[2] = {(sight >> (4 * n + r) & 1) != 0, (sight >> (4 * n + 2 + r) & 1) != 0};
                         const float top = column_max(fmaxf(seen[0] ? sc[n][r] * f : -INFINITY,
                                                            seen[1] ? sc[n][2 + r] * f : -INFINITY));
-                        // (Differences of the large numbers first, of the products as rounded for `top`: with scores beyond
-                        // 2^23 in size, whose last places are whole numbers, weights would pass fp16's range otherwise.)
                         const float m_new = fmaxf(m[n][r], top);
+                        large |= fabsf(m_new) >= 65536.0f && m_new != kLowest;
                         const float dm_new = -fmaxf((m[n][r] - m_new) - dm[n][r], (top - m_new) + e);
                         keep[r] = ex2(m[n][r] - m_new + (dm_new - dm[n][r]));
                         l[n][r] *= ex2(m[n][r] - m_new);
@@ -470,12 +470,21 @@ struct Piece {
                         dm[n][r] = dm_new;
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            x[n][2 * h + r] = seen[h] ? __fsub_rn(__fmul_rn(sc[n][2 * h + r], f), m_new) : -INFINITY;
+                            x[n][2 * h + r] = seen[h] ? fmaf(sc[n][2 * h + r], f, -m_new) : -INFINITY;
                     }
 #pragma unroll
                     for (int y = 0; y < S::TILES; ++y)
 #pragma unroll
                         for (int w = 0; w < 4; ++w) acc[y][n][w] *= keep[w & 1];
+                }
+                // Scores beyond 2^23 have whole numbers for last places: less a maximum that is a rounded product they
+                // would be that far off, and weights beyond fp16's range, were they not rounded products too.
+                if (__any_sync(0xffffffffu, large)) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+                            if (x[n][w] != -INFINITY) x[n][w] = __fsub_rn(__fmul_rn(sc[n][w], factor[n][w & 1] * scales.x), m[n][w & 1]);
                 }
             }
             uint32_t pf[S::PIECES][NT][2];                 // weights: tokens 2 c .. of row g, then 8 more
