@@ -19,9 +19,12 @@
 // the next sequence's start is at least floor((len + 2 P - 2) / P) further, which
 // no run of len tokens, wherever it starts in a page, needs more of.
 //
-// Measured with heads of 128 channels, bf16: 64 packed sequences of up to 4096 tokens, 16 heads, written in
-// 255 us, 6.4 TB/s; 16 of up to 16384 tokens, 8 heads, read in 132 us, 6.5 TB/s; one token of each
-// of 256 sequences, 8 heads, written in 5.6 us, most of it loads that wait for one another.
+// Measured with heads of 128 channels and pages of 64 tokens, bf16: 64 packed sequences of up to 4096 tokens, 16 heads,
+// written in 255 us, 6.4 TB/s; 16 of up to 16384 tokens, 8 heads, read in 132 us, 6.5 TB/s; one token of each of 256
+// sequences, 8 heads, written in 5.6 us packed and 3.6 us as a batch, most of it loads that wait for one another.  That is
+// the size these numbers of threads suit.  Smaller items leave threads idle and pay each item's search, offsets, table and
+// barrier for less: the same bytes in pages of 16 tokens take 2.5 times as long to write and 1.8 times to read, with heads of
+// 16 channels 4.8 and 2.9 times; pages of 128 tokens, more than is held, 1.3 times to write.
 #include "kda_cache.cuh"
 #include "kda_cache_internal.h"
 #include "kda_chained.cuh"

@@ -11,9 +11,9 @@
 //
 // What bounds it: reading the codes, as long as the rows that share a head's
 // keys (T_q times H_q / H_kv) are few.  Measured with 8 heads of keys, 32 of queries, d = 128, bf16: a
-// million tokens 351 us, 6.1 TB/s; 256 sequences of up to 4096 tokens 188 us, 5.8 TB/s; 77 tokens
-// 4.0 us.  Beyond 16 rows the conversion of codes and the products bound it (537 MB of codes: 101 us under
-// 4 rows, 109 us under 16, 170 us under 32), which is where kda_cache_attention_tc.cu
+// million tokens 349 us, 6.2 TB/s; 256 sequences of up to 4096 tokens 186 us, 5.8 TB/s; 77 tokens
+// 4.0 us (8.2 to 8.9 under a block table with room for 1,024 to a million).  Beyond 16 rows the conversion of codes and
+// the products bound it (537 MB of codes: 99 us under 4 rows, 108 us under 16, 170 us under 32), which is where kda_cache_attention_tc.cu
 // takes over for bf16 rows of more than 64 channels.
 //
 // The tile.  16 tokens a step against NT tiles of 8 rows, on m16n8k16 products of
@@ -668,8 +668,8 @@ attention_share_kernel(const CacheAttention a, const Plan plan) {
 // pieces: a warp a row, without a barrier; many: eight warps a row, each every
 // eighth piece, their sums joined in shared memory.  A piece's statistics and sums are
 // loaded together, the sums so far rescaled as they come, since what it takes is loads that wait for one another
-// (8 sequences of 1,501 tokens, 16 heads, fp32: 14.7 us; 16.2 with the largest of all statistics found first, 15.5 with
-// eight pieces at once, whose registers leave room for fewer CTAs).
+// (8 sequences of 1,501 tokens, 16 heads, fp32: 15.3 us; 1.5 more with the largest of all statistics found first, 0.8 more
+// with eight pieces at once, whose registers leave room for fewer CTAs).
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads, 4)
 attention_join_kernel(const CacheAttention a, const Plan plan) {

@@ -2,7 +2,7 @@
 // tokens and prompts, whose rows share each head's keys.
 //
 // The mathematics is that of kda_cache_attention.cu.  With more than some 16 rows a head the
-// products there bound it (537 MB of codes under 32 rows: 170 us; here 135 us, 4.0 TB/s; 64 rows 330 and 241 us),
+// products there bound it (537 MB of codes under 32 rows: 170 us; here 134 us, 4.0 TB/s; 64 rows 330 and 240 us),
 // above all the conversion of every code to fp16.  Here the codes go to the tensor cores as they lie in
 // the cache, as e4m3 operands; what is not 8 bits is split instead:
 //
@@ -24,11 +24,12 @@
 //   1 issuer    the score product of the next tile, then the value product of this one
 // The maximum m and the reference of v's sums (kept as dm) are common to the CTA and move only when a
 // score passes them by more than a factor of 128, which a vote of the four warps of its row tells; the sums in
-// TMEM are then multiplied in place.  (A move costs some 3000 cycles; with a factor of 4 every third tile had one.)
+// TMEM are then multiplied in place.  (A move takes 2,750 cycles, its wait for the products before it included; of pages
+// that differ by 2^6 in size 19% of the tiles have one, with a factor of 4 every third had.)
 //
 // The products' own sums are cut off, not rounded, all the same way: values of one sign over 131,072 tokens came out 1.2e-4
-// too small, and more so with the length.  So they hold kRun tiles (256 products, cut off by less than 2^-16 in all), then go to
-// sums in TMEM by rounded additions.  (4 x 65,536 tokens under 32 rows: 126.6 us, 126.0 without.)
+// too small, and more so with the length.  So they hold kRun tiles (256 products, cut off by less than 2^-15 of their sum), then go to
+// sums in TMEM by rounded additions.  (0.5 to 1% of the time of 65,536 tokens.)
 //
 // NaN that a row does not see (0 times NaN is NaN): see Softmax::mend_values.
 //
@@ -54,7 +55,7 @@ constexpr int kLoaders = 64;               // eight rows at a time
 constexpr int kThreads = kSoftmax + 128;   // (whole warpgroups, for setmaxnreg: the last warp has no role)
 constexpr int kIssuerWarp = (kSoftmax + kLoaders) / 32;
 // Registers: 80 a thread at launch, then 96 for softmax and 48 for the others, all there are: 256 x 96 + 128 x 48 = 384 x 80.
-// (40 for the others: their loops spill, 4 x 65,536 tokens under 32 rows 129.9 us, 123.1 so.)
+// (40 for the others: their loops spill; 4 x 65,536 tokens of one size under 32 rows 129.9 us, 123.1 so.)
 constexpr int kSoftmaxRegs = 96, kOtherRegs = 48;
 static_assert(kSoftmax * kSoftmaxRegs + (kThreads - kSoftmax) * kOtherRegs <= kThreads * 80, "registers at launch");
 constexpr int kMine = kRows / 2;           // rows of a softmax thread
@@ -513,7 +514,7 @@ struct Softmax {
     }
 
     // This thread's channel of its rows, from the four pieces' sums and the rounded ones.  (Unrolled, it costs the loop over
-    // the tiles registers: 4 x 65,536 tokens under 32 rows 132.6 us, 126.6 so.)
+    // the tiles registers: 5% of 4 x 65,536 tokens under 32 rows.)
     static __device__ __forceinline__ void read_sums(uint32_t at, bool summed, float (&o)[kMine]) {
         tc::tmem_ld16(at + kTmemO, o);
         loaded(o);
@@ -535,7 +536,7 @@ struct Softmax {
         }
     }
 
-    // What O holds, all its products ended, goes to the rounded sums, and O begins again from zeros.  (Inline 127.6 us.)
+    // What O holds, all its products ended, goes to the rounded sums, and O begins again from zeros.  (Inline, 1% slower.)
     static __device__ __noinline__ void add_run(uint32_t at, bool summed) {
         float o[kMine];
         read_sums(at, summed, o);

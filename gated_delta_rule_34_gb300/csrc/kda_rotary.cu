@@ -22,7 +22,7 @@
 // turned, 16384 tokens; 80% so.)  The vector is 16 bytes where rot allows it (rot / 2 whole
 // vectors in the half layout, rot in the interleaved one), else 8, 4 or 2.
 // Measured: 65536 tokens of 32 + 8 heads of 128 channels, 64 turned, bf16: 202 us, 6.6 TB/s;
-// 4097 tokens of 16 + 16 heads of 64 channels, fp32: 10.4 us, 6.4 TB/s; one token: 2.3 us.
+// 4097 tokens of 16 + 16 heads of 64 channels, fp32: 10.5 us, 6.4 TB/s; one token: 2.4 us.
 #include "kda_cache_internal.h"
 #include "kda_chained.cuh"
 #include "kda_common.cuh"

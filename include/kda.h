@@ -381,10 +381,14 @@ kda_status kda_spec_commit(const void *k, const void *v, const void *z, const vo
  * layers with one layer of global attention ("How Kimi K3 is built", section
  * "Sequence: three KDA to one global MLA"), and its section "How to serve two
  * different caches" sets the recurrent state beside the attention layer's
- * cache.  The pages give no formulas for positions or for a cache in 8 bits;
- * the definitions below are this library's own.  The operators are those a step
- * of such a layer needs around its projections: kda_rotary, kda_cache_write,
- * kda_cache_attention, and kda_cache_read to take cached tokens out again.
+ * cache.  The page's own global layer attends over latents and takes no
+ * positions, which come from the recurrent layers' decay.  The operators here
+ * are for hybrids whose global layers are ordinary ones: grouped heads in the
+ * cache and, where a model has them, rotary positions on all or part of a head.
+ * A cache of latents is not among them.  The pages give no formulas for
+ * positions or for a cache in 8 bits; the definitions below are this library's
+ * own: kda_rotary, kda_cache_write, kda_cache_attention, and kda_cache_read to
+ * take cached tokens out again.
  *
  * Token strides.  Where an argument x has a companion x_stride, x is
  * [tokens, H, d] with H * d dense elements for each token and x_stride
@@ -416,8 +420,9 @@ typedef enum { KDA_ROTARY_HALF = 0, KDA_ROTARY_INTERLEAVED = 1 } kda_rotary_layo
  * channels of every head:
  *   (x, y) <- amplitude * (x cos a - y sin a, y cos a + x sin a)
  * and the channels past rot are copied.  Scaling for long contexts is a matter of
- * freq and amplitude alone.  The angle is reduced in 64 bits, so that far
- * positions lose nothing; x, cos and sin are fp32, rounded once to dtype.
+ * freq and amplitude alone.  The angle is reduced in 64 bits and is off by at
+ * most 2^-32 turns, and by 2^-53 turns a position; x, cos and sin are fp32,
+ * rounded once to dtype.
  *   q, k       [n_tokens, H, d] with token strides; H_k may be 0 (k unused)
  *   q_out, k_out  likewise (written); may be q and k with the same strides,
  *              and must not overlap them otherwise
@@ -441,7 +446,9 @@ kda_status kda_rotary(const void *q, int64_t q_stride, void *q_out, int64_t q_ou
  * scale and the new tokens' own; where that grows it, the older codes are
  * rounded again to the new scale, which is exact but for values below
  * 2^-6 of it.  code = e4m3(x / scale), nearest, ties to even; infinities
- * become 448, NaN stays NaN, and neither counts for the scale.
+ * become 448, NaN stays NaN, and neither counts for the scale.  Writing is
+ * appending: codes that lie behind the new tokens in their page do not follow
+ * a scale that grew.
  * No two sequences may write to the same page in one call.  Malformed
  * cu_seqlens are clamped into [0, T]: results are then unspecified, but no
  * access leaves the buffers.
@@ -471,8 +478,9 @@ kda_status kda_cache_read(const void *k_codes, const void *v_codes, const float 
  *              page is held
  *   o[b, i, h] = sum_t w_t v_t,  w = softmax over the seen t of scale * q . k_t
  *   lse[b, i, h] = log sum_t exp(scale * q . k_t)
- * A row that sees no token, or whose scores are all -inf, gives o = 0 and
- * lse = -inf.  What lies in tokens that a row does not see (NaN included) does
+ * A row that sees no token, or whose scores are all -inf (an infinite channel
+ * of its query against keys of one sign), gives o = 0 and lse = -inf; one with
+ * a score of +inf or NaN gives NaN for both.  What lies in tokens that a row does not see (NaN included) does
  * not reach it.
  *   q          [B * T_q, H_q, d] with a token stride
  *   lengths    device int32 [B], tokens of each sequence with the T_q newest;
@@ -483,7 +491,10 @@ kda_status kda_cache_read(const void *k_codes, const void *v_codes, const float 
  *              contents on entry are ignored
  * If one of the bounded waits (about 2 s) of the kernel for more than 16 rows gives
  * up, the outputs of that item and of its CTA's later ones are NaN.
- * Scores, sums and outputs are fp32 until the one rounding to dtype.  Weights
+ * Scores, sums and outputs are fp32 until the one rounding to dtype.  Sums over
+ * tokens are added with rounding, 16 tokens at a time; with more than 16 bf16
+ * rows a head of more than 64 channels 8,192 tokens at a time, within which the
+ * matrix products cut their sums off, by less than 2^-15 of them.  Weights
  * meet the values as fp16 numbers (two of them, 22 bits, where dtype is fp32) relative
  * to the row's largest w_t times its page's scale of v: what lies below 2^-36 of
  * that is lost (below 2^-30 with more than 16 bf16 rows a head, T_q * H_q / H_kv, of
