@@ -264,7 +264,8 @@ kda_status kda_cache_attention(const void* q, int64_t q_stride, const void* k_co
     a.o = o;
     a.lse = lse;
     a.scale = scale;
-    a.window = window;
+    // (positions are below 2^31: a wider window is none, and differences with it stay in range)
+    a.window = window > INT32_MAX ? 0 : window;
     a.sinks = sinks;
     const int sms = sm_count();
     const size_t need = kda::cache_attention_workspace_bytes(a, sms);
