@@ -203,8 +203,9 @@ static kda_status attention_sizes(kda::CacheAttention& a, int B, int T_q, int H_
     KDA_REQUIRE(H_q % H_kv == 0, KDA_ERR_INVALID_ARG, "H_q must be a multiple of H_kv (%d, %d)", H_q,
                 H_kv);
     KDA_REQUIRE(H_q <= 65535 && B <= 65535, KDA_ERR_UNSUPPORTED, "B and H_q must be <= 65535");
-    KDA_REQUIRE((int64_t)B * T_q * H_q <= INT32_MAX, KDA_ERR_UNSUPPORTED,
-                "B * T_q * H_q must be below 2^31");
+    // (less than a tile below 2^31, so that counts of row tiles do not overflow)
+    KDA_REQUIRE((int64_t)B * T_q * H_q <= INT32_MAX - 255, KDA_ERR_UNSUPPORTED,
+                "B * T_q * H_q must be at most 2^31 - 256");
     KDA_REQUIRE((int64_t)table_pages * page <= INT32_MAX, KDA_ERR_UNSUPPORTED,
                 "table_pages * page must be below 2^31");
     a.B = B;
