@@ -11,7 +11,7 @@
 // modulo one turn by itself.  The nearest quarter is taken from the top 32 bits, of what remains (an eighth of a turn at
 // most) cos and sin are taken at its first 24 bits and corrected by the others: (c - s x, s + c x).  One 64-bit
 // multiply an angle and three 64-bit float operations; the angle is off by at
-// most 2^-32 turns plus p 2^-53.  (The top 32 bits as one fp32 number: off by up to 2^-26 turns near half a turn.)
+// most 2^-32 turns plus p 2^-53, times f above 1.  (The top 32 bits as one fp32 number: off by up to 2^-26 turns near half a turn.)
 //
 // The split.  Bound by memory: every element is read and written once.  A CTA
 // takes a few tokens with all their heads and works out their rot / 2 angles once

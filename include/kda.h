@@ -421,8 +421,8 @@ typedef enum { KDA_ROTARY_HALF = 0, KDA_ROTARY_INTERLEAVED = 1 } kda_rotary_layo
  *   (x, y) <- amplitude * (x cos a - y sin a, y cos a + x sin a)
  * and the channels past rot are copied.  Scaling for long contexts is a matter of
  * freq and amplitude alone.  The angle is reduced in 64 bits and is off by at
- * most 2^-32 turns, and by 2^-53 turns a position; x, cos and sin are fp32,
- * rounded once to dtype.
+ * most 2^-32 turns, and by 2^-53 turns a position (times freq, where that is
+ * above a radian); x, cos and sin are fp32, rounded once to dtype.
  *   q, k       [n_tokens, H, d] with token strides; H_k may be 0 (k unused)
  *   q_out, k_out  likewise (written); may be q and k with the same strides,
  *              and must not overlap them otherwise
