@@ -12,8 +12,9 @@ from .api import (KDAError, auto_segments, chunk_prefill, chunk_prefill_from_hos
                   set_profile_events, spec_commit,
                   segmented_workspace_size, spec_verify, static_workspace_status,
                   workspace_size)
-from .cache import (PagedCache, cache_attention, cache_attention_workspace_size, cache_new,  # noqa: F401
-                    cache_read, cache_write, rotary, rotary_frequencies)
+from .cache import (PagedCache, cache_attention, cache_attention_workspace_size, cache_compact,  # noqa: F401
+                    cache_copy, cache_fork, cache_new, cache_pages_workspace_size, cache_read, cache_resize,
+                    cache_write, rotary, rotary_frequencies)
 
 __all__ = ["KDAError", "auto_segments", "chunk_prefill", "chunk_prefill_segmented",
            "segmented_workspace_size", "chunk_prefill_from_host", "chunk_prefill_static_workspace",
@@ -21,4 +22,5 @@ __all__ = ["KDAError", "auto_segments", "chunk_prefill", "chunk_prefill_segmente
            "selftest_bounded_wait",
            "set_profile_events", "spec_commit", "spec_verify", "static_workspace_status",
            "workspace_size", "PagedCache", "cache_attention", "cache_attention_workspace_size",
-           "cache_new", "cache_read", "cache_write", "rotary", "rotary_frequencies"]
+           "cache_compact", "cache_copy", "cache_fork", "cache_new", "cache_pages_workspace_size",
+           "cache_read", "cache_resize", "cache_write", "rotary", "rotary_frequencies"]

@@ -96,6 +96,16 @@ def _declare(lib):
     lib.kda_cache_attention.restype = i32
     lib.kda_cache_attention_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
     lib.kda_cache_attention_workspace_size.restype = sz
+    lib.kda_cache_copy.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i64, i32, vp]
+    lib.kda_cache_copy.restype = i32
+    lib.kda_cache_resize.argtypes = [vp, i64, vp, i32, i32, vp, vp, i32, i32, vp, vp, sz, vp]
+    lib.kda_cache_resize.restype = i32
+    lib.kda_cache_fork.argtypes = [vp, i64, vp, i32, i32, vp, vp, vp, i32, i32, vp, vp, vp, vp, sz, vp]
+    lib.kda_cache_fork.restype = i32
+    lib.kda_cache_compact.argtypes = [vp, vp, i64, vp, vp, i32, i32, vp, vp, vp, vp, vp]
+    lib.kda_cache_compact.restype = i32
+    lib.kda_cache_pages_workspace_size.argtypes = [i64]
+    lib.kda_cache_pages_workspace_size.restype = sz
     lib.kda_static_workspace_status.argtypes = [vp, vp]
     lib.kda_static_workspace_status.restype = i32
     return lib

@@ -1,5 +1,5 @@
 """Thin Python binding of the global-attention operators: rotary positions, the paged
-8-bit cache and the attention over it (include/kda.h, "The global-attention layer").
+8-bit cache, its pages' sharing and the attention over it (include/kda.h, "The global-attention layer").
 
 Argument marshalling only, as in ``api``: tensors are checked for device, dtype, shape and
 layout, and their data pointers plus the current CUDA stream are handed to ``libkda.so``.
@@ -29,7 +29,9 @@ E4M3, F32, F64, I32 = torch.float8_e4m3fn, torch.float32, torch.float64, torch.i
 def _binding():
     """The compiled marshalling, calling the library that ``lib`` has loaded; raises if it has not been built."""
     entries = [getattr(lib(), name) for name in ("kda_rotary", "kda_cache_write", "kda_cache_read",
-                                                 "kda_cache_attention", "kda_cache_attention_workspace_size")]
+                                                 "kda_cache_attention", "kda_cache_attention_workspace_size",
+                                                 "kda_cache_copy", "kda_cache_resize", "kda_cache_fork",
+                                                 "kda_cache_compact", "kda_cache_pages_workspace_size")]
     if not os.path.exists(_build.BINDING):
         raise RuntimeError(
             f"KDA binding not found at {_build.BINDING}; build it with "
@@ -299,3 +301,108 @@ def cache_attention(q, cache: PagedCache, block_table, lengths, scale: float | N
     if workspace is not None and (workspace.get_device() != index or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be a contiguous CUDA tensor on {q.device}")
     _not_understood("cache_attention")
+
+
+def _workspace(workspace, index):
+    if workspace is not None and (workspace.get_device() != index or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{index}")
+
+
+def cache_copy(cache: PagedCache, src, dst) -> PagedCache:
+    """Page src[i] copied to page dst[i], codes and scales of all heads, through kda_cache_copy; returns the cache.
+
+    src, dst: int32 [n]; pairs with an entry outside [0, n_pages) (-1) are skipped.  No page may be the target of two pairs, or of
+    one and the source of another.
+    """
+    done = _binding().cache_copy(cache, src, dst)
+    if done is not None:
+        return done
+    index = src.get_device()
+    if _is_elsewhere(index):
+        with torch.cuda.device(index):
+            return cache_copy(cache, src, dst)
+    _pool(cache, index)
+    _tensor("src", src, I32, (-1,), index)
+    _tensor("dst", dst, I32, src.shape, index)
+    _not_understood("cache_copy")
+
+
+def cache_pages_workspace_size(n_pages: int) -> int:
+    return int(lib().kda_cache_pages_workspace_size(n_pages))
+
+
+def cache_resize(refs, block_table, rows, tokens, page: int, missing=None, workspace=None):
+    """The listed rows of the block table brought to the pages that their tokens need, through kda_cache_resize: pages past
+    these are given back, missing ones taken, the lowest free ones first.  In place.
+
+    refs: int32 [n_pages], how many entries hold each page (a new pool: torch.zeros); block_table: int32 [n_rows, table_pages];
+    rows, tokens: int32 [n]; page: tokens of a page.  Returns missing, int32 [1]: pages wanted when the pool had no more
+    (their entries are -1).  A workspace of the required size is allocated with torch if none is given.
+    """
+    done = _binding().cache_resize(refs, block_table, rows, tokens, page, missing, workspace)
+    if done is not None:
+        return done
+    index = rows.get_device()
+    if _is_elsewhere(index):
+        with torch.cuda.device(index):
+            return cache_resize(refs, block_table, rows, tokens, page, missing, workspace)
+    _tensor("refs", refs, I32, (-1,), index)
+    _tensor("block_table", block_table, I32, (-1, -1), index)
+    _tensor("rows", rows, I32, (-1,), index)
+    _tensor("tokens", tokens, I32, rows.shape, index)
+    if missing is not None:
+        _tensor("missing", missing, I32, (1,), index)
+    _workspace(workspace, index)
+    _not_understood("cache_resize")
+
+
+def cache_fork(refs, block_table, lengths, src, dst, page: int, from_pages=None, to_pages=None, missing=None, workspace=None):
+    """Rows dst[i] of the block table become the sequences of rows src[i], through kda_cache_fork: full pages are shared, a
+    partly filled last page is replaced by a free one.  In place; dst rows must hold nothing (cache_resize to 0 gives back).
+
+    refs, block_table, page: as in cache_resize; lengths: int32 [n_rows], tokens of each row (dst's are set); src, dst: int32 [n],
+    a source may stand in many pairs.  Returns (from_pages, to_pages, missing): the pages to copy, int32 [n], -1 where there is none
+    (cache_copy, for the pool of each layer that has this table), and int32 [1], pages wanted when the pool had no more.
+    """
+    done = _binding().cache_fork(refs, block_table, lengths, src, dst, page, from_pages, to_pages, missing, workspace)
+    if done is not None:
+        return done
+    index = src.get_device()
+    if _is_elsewhere(index):
+        with torch.cuda.device(index):
+            return cache_fork(refs, block_table, lengths, src, dst, page, from_pages, to_pages, missing, workspace)
+    _tensor("refs", refs, I32, (-1,), index)
+    _tensor("block_table", block_table, I32, (-1, -1), index)
+    _tensor("lengths", lengths, I32, block_table.shape[:1], index)
+    _tensor("src", src, I32, (-1,), index)
+    _tensor("dst", dst, I32, src.shape, index)
+    for name, t, n in (("from_pages", from_pages, src.numel()), ("to_pages", to_pages, src.numel()), ("missing", missing, 1)):
+        if t is not None:
+            _tensor(name, t, I32, (n,), index)
+    _workspace(workspace, index)
+    _not_understood("cache_fork")
+
+
+def cache_compact(refs, block_table, refs_out=None, table_out=None, page_map=None, from_pages=None, to_pages=None, held=None):
+    """The held pages brought to the front of the pool, through kda_cache_compact: refs and the block table are changed in
+    place, or written to refs_out and table_out where these are given.
+
+    Returns (page_map, from_pages, to_pages, held): int32 [n_pages], where each held page is now (-1: not held), for other tables;
+    int32 [n_pages // 2], the pages to copy (cache_copy, for the pool of each layer that has this table), -1 past the last; int32 [1],
+    how many pages are held.
+    """
+    done = _binding().cache_compact(refs, block_table, refs_out, table_out, page_map, from_pages, to_pages, held)
+    if done is not None:
+        return done
+    index = refs.get_device()
+    if _is_elsewhere(index):
+        with torch.cuda.device(index):
+            return cache_compact(refs, block_table, refs_out, table_out, page_map, from_pages, to_pages, held)
+    _tensor("refs", refs, I32, (-1,), index)
+    _tensor("block_table", block_table, I32, (-1, -1), index)
+    n = refs.numel()
+    for name, t, shape in (("refs_out", refs_out, refs.shape), ("table_out", table_out, block_table.shape), ("page_map", page_map, (n,)),
+                           ("from_pages", from_pages, (n // 2,)), ("to_pages", to_pages, (n // 2,)), ("held", held, (1,))):
+        if t is not None:
+            _tensor(name, t, I32, shape, index)
+    _not_understood("cache_compact")

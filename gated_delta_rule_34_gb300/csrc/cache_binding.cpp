@@ -32,6 +32,11 @@ decltype(&kda_cache_write) write_entry;
 decltype(&kda_cache_read) read_entry;
 decltype(&kda_cache_attention) attention_entry;
 decltype(&kda_cache_attention_workspace_size) workspace_entry;
+decltype(&kda_cache_copy) copy_entry;
+decltype(&kda_cache_resize) resize_entry;
+decltype(&kda_cache_fork) fork_entry;
+decltype(&kda_cache_compact) compact_entry;
+decltype(&kda_cache_pages_workspace_size) pages_workspace_entry;
 PyObject* check;                           // api._check
 
 const at::Tensor* tensor(PyObject* x) { return THPVariable_Check(x) ? &THPVariable_Unpack(x) : nullptr; }
@@ -341,12 +346,177 @@ PyObject* cache_attention(PyObject*, PyObject* const* arg, Py_ssize_t n_args) {
     END_HANDLE_TH_ERRORS
 }
 
-// The addresses of kda_rotary, kda_cache_write, kda_cache_read, kda_cache_attention and
-// kda_cache_attention_workspace_size, and api._check
+// cache, src, dst -> cache
+PyObject* cache_copy(PyObject*, PyObject* const* arg, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    if (!takes("cache_copy", n_args, 3)) return nullptr;
+    const at::Tensor *src = tensor(arg[1]), *dst = tensor(arg[2]);
+    const int index = current_device_of(src);
+    Pool pool;
+    if (index < 0 || !pool.read(arg[0], index) || !dense(src, at::kInt, index) || src->dim() != 1 || src->numel() > INT_MAX ||
+        !dense(dst, at::kInt, index, src->sizes()))
+        Py_RETURN_NONE;
+    const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(index).stream();
+    kda_status status;
+    Py_BEGIN_ALLOW_THREADS
+    status = copy_entry(pool.k->mutable_data_ptr(), pool.v->mutable_data_ptr(), pool.k_scale->mutable_data_ptr<float>(),
+                        pool.v_scale->mutable_data_ptr<float>(), src->const_data_ptr<int32_t>(),
+                        dst->const_data_ptr<int32_t>(), (int)src->numel(), (int)pool.h, (int)pool.d, pool.n_pages,
+                        (int)pool.page, stream);
+    Py_END_ALLOW_THREADS
+    if (failed(status)) return nullptr;
+    return Py_NewRef(arg[0]);
+    END_HANDLE_TH_ERRORS
+}
+
+// A dense list of int32, given or to be made; false where what is given is not one.
+struct List {
+    at::Tensor made;
+    const at::Tensor* at = &made;
+
+    bool read(PyObject* given, int64_t n, int index, const at::Tensor& like) {
+        if (given == Py_None) {
+            made = empty({n}, at::kInt, like);
+            return true;
+        }
+        return dense(at = tensor(given), at::kInt, index, {n});
+    }
+    int32_t* ptr() const { return at->mutable_data_ptr<int32_t>(); }
+};
+
+// The counts and a block table.
+struct Rows {
+    const at::Tensor *refs, *table;
+    int64_t n_pages;
+
+    bool read(PyObject* refs_obj, PyObject* table_obj, int index) {
+        refs = tensor(refs_obj);
+        table = tensor(table_obj);
+        if (!dense(refs, at::kInt, index) || refs->dim() != 1 || !dense(table, at::kInt, index) || table->dim() != 2 ||
+            table->size(0) > INT_MAX || table->size(1) > INT_MAX)
+            return false;
+        n_pages = refs->numel();
+        return true;
+    }
+};
+
+struct Workspace {
+    at::Tensor made;
+    const at::Tensor* at = &made;
+
+    bool read(PyObject* given, size_t need, int index, const at::Tensor& like) {
+        if (given == Py_None) {
+            if (need) made = empty({(int64_t)need}, at::kByte, like);
+            return true;
+        }
+        at = tensor(given);
+        return at && at->is_cuda() && at->get_device() == index && at->is_contiguous();
+    }
+    size_t bytes() const { return at->defined() ? at->nbytes() : 0; }
+    void* ptr() const { return at->defined() ? at->mutable_data_ptr() : nullptr; }
+};
+
+// refs, block_table, rows, tokens, page, missing, workspace -> missing
+PyObject* cache_resize(PyObject*, PyObject* const* arg, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    if (!takes("cache_resize", n_args, 7)) return nullptr;
+    const at::Tensor *rows = tensor(arg[2]), *tokens = tensor(arg[3]);
+    const int index = current_device_of(rows);
+    Rows table;
+    if (index < 0 || !table.read(arg[0], arg[1], index) || !dense(rows, at::kInt, index) || rows->dim() != 1 ||
+        rows->numel() > INT_MAX || !dense(tokens, at::kInt, index, rows->sizes()))
+        Py_RETURN_NONE;
+    int page;
+    if (!integer32(arg[4], page)) return nullptr;
+    List missing;
+    Workspace ws;
+    if (!missing.read(arg[5], 1, index, *rows) || !ws.read(arg[6], pages_workspace_entry(table.n_pages), index, *rows))
+        Py_RETURN_NONE;
+    const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(index).stream();
+    kda_status status;
+    Py_BEGIN_ALLOW_THREADS
+    status = resize_entry(table.refs->mutable_data_ptr<int32_t>(), table.n_pages,
+                          table.table->mutable_data_ptr<int32_t>(), (int)table.table->size(0),
+                          (int)table.table->size(1), rows->const_data_ptr<int32_t>(), tokens->const_data_ptr<int32_t>(),
+                          (int)rows->numel(), page, missing.ptr(), ws.ptr(), ws.bytes(), stream);
+    Py_END_ALLOW_THREADS
+    if (failed(status)) return nullptr;
+    return result(arg[5], missing.made);
+    END_HANDLE_TH_ERRORS
+}
+
+// refs, block_table, lengths, src, dst, page, from_pages, to_pages, missing, workspace -> (from_pages, to_pages, missing)
+PyObject* cache_fork(PyObject*, PyObject* const* arg, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    if (!takes("cache_fork", n_args, 10)) return nullptr;
+    const at::Tensor *lengths = tensor(arg[2]), *src = tensor(arg[3]), *dst = tensor(arg[4]);
+    const int index = current_device_of(src);
+    Rows table;
+    if (index < 0 || !table.read(arg[0], arg[1], index) || !dense(src, at::kInt, index) || src->dim() != 1 ||
+        src->numel() > INT_MAX || !dense(dst, at::kInt, index, src->sizes()) ||
+        !dense(lengths, at::kInt, index, {table.table->size(0)}))
+        Py_RETURN_NONE;
+    int page;
+    if (!integer32(arg[5], page)) return nullptr;
+    List from, to, missing;
+    Workspace ws;
+    if (!from.read(arg[6], src->numel(), index, *src) || !to.read(arg[7], src->numel(), index, *src) ||
+        !missing.read(arg[8], 1, index, *src) || !ws.read(arg[9], pages_workspace_entry(table.n_pages), index, *src))
+        Py_RETURN_NONE;
+    const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(index).stream();
+    kda_status status;
+    Py_BEGIN_ALLOW_THREADS
+    status = fork_entry(table.refs->mutable_data_ptr<int32_t>(), table.n_pages, table.table->mutable_data_ptr<int32_t>(),
+                        (int)table.table->size(0), (int)table.table->size(1), lengths->mutable_data_ptr<int32_t>(),
+                        src->const_data_ptr<int32_t>(), dst->const_data_ptr<int32_t>(), (int)src->numel(), page,
+                        from.ptr(), to.ptr(), missing.ptr(), ws.ptr(), ws.bytes(), stream);
+    Py_END_ALLOW_THREADS
+    if (failed(status)) return nullptr;
+    PyObject *a = result(arg[6], from.made), *b = result(arg[7], to.made), *c = result(arg[8], missing.made);
+    PyObject* t = a && b && c ? PyTuple_Pack(3, a, b, c) : nullptr;
+    Py_XDECREF(a);
+    Py_XDECREF(b);
+    Py_XDECREF(c);
+    return t;
+    END_HANDLE_TH_ERRORS
+}
+
+// refs, block_table, refs_out, table_out, page_map, from_pages, to_pages, held -> (page_map, from_pages, to_pages, held)
+PyObject* cache_compact(PyObject*, PyObject* const* arg, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    if (!takes("cache_compact", n_args, 8)) return nullptr;
+    const int index = current_device_of(tensor(arg[0]));
+    Rows table;
+    if (index < 0 || !table.read(arg[0], arg[1], index)) Py_RETURN_NONE;
+    const at::Tensor *refs_out = table.refs, *table_out = table.table;
+    if (arg[2] != Py_None && !dense(refs_out = tensor(arg[2]), at::kInt, index, table.refs->sizes())) Py_RETURN_NONE;
+    if (arg[3] != Py_None && !dense(table_out = tensor(arg[3]), at::kInt, index, table.table->sizes())) Py_RETURN_NONE;
+    List map, from, to, held;
+    if (!map.read(arg[4], table.n_pages, index, *table.refs) || !from.read(arg[5], table.n_pages / 2, index, *table.refs) ||
+        !to.read(arg[6], table.n_pages / 2, index, *table.refs) || !held.read(arg[7], 1, index, *table.refs))
+        Py_RETURN_NONE;
+    const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(index).stream();
+    kda_status status;
+    Py_BEGIN_ALLOW_THREADS
+    status = compact_entry(table.refs->const_data_ptr<int32_t>(), refs_out->mutable_data_ptr<int32_t>(), table.n_pages,
+                           table.table->const_data_ptr<int32_t>(), table_out->mutable_data_ptr<int32_t>(),
+                           (int)table.table->size(0), (int)table.table->size(1), map.ptr(), from.ptr(), to.ptr(),
+                           held.ptr(), stream);
+    Py_END_ALLOW_THREADS
+    if (failed(status)) return nullptr;
+    PyObject* all[4] = {result(arg[4], map.made), result(arg[5], from.made), result(arg[6], to.made), result(arg[7], held.made)};
+    PyObject* t = all[0] && all[1] && all[2] && all[3] ? PyTuple_Pack(4, all[0], all[1], all[2], all[3]) : nullptr;
+    for (PyObject* x : all) Py_XDECREF(x);
+    return t;
+    END_HANDLE_TH_ERRORS
+}
+
+// The addresses of the entries, in the order of cache.py's list, and api._check
+constexpr int kEntries = 10;
 PyObject* bind(PyObject*, PyObject* const* arg, Py_ssize_t n_args) {
-    if (!takes("bind", n_args, 6)) return nullptr;
-    void* at[5];
-    for (int i = 0; i < 5; ++i) {
+    if (!takes("bind", n_args, kEntries + 1)) return nullptr;
+    void* at[kEntries];
+    for (int i = 0; i < kEntries; ++i) {
         at[i] = PyLong_AsVoidPtr(arg[i]);
         if (PyErr_Occurred()) return nullptr;
     }
@@ -355,8 +525,13 @@ PyObject* bind(PyObject*, PyObject* const* arg, Py_ssize_t n_args) {
     read_entry = reinterpret_cast<decltype(read_entry)>(at[2]);
     attention_entry = reinterpret_cast<decltype(attention_entry)>(at[3]);
     workspace_entry = reinterpret_cast<decltype(workspace_entry)>(at[4]);
+    copy_entry = reinterpret_cast<decltype(copy_entry)>(at[5]);
+    resize_entry = reinterpret_cast<decltype(resize_entry)>(at[6]);
+    fork_entry = reinterpret_cast<decltype(fork_entry)>(at[7]);
+    compact_entry = reinterpret_cast<decltype(compact_entry)>(at[8]);
+    pages_workspace_entry = reinterpret_cast<decltype(pages_workspace_entry)>(at[9]);
     Py_XDECREF(check);
-    check = Py_NewRef(arg[5]);
+    check = Py_NewRef(arg[kEntries]);
     Py_RETURN_NONE;
 }
 
@@ -368,6 +543,10 @@ PyMethodDef methods[] = {{"bind", method(bind), METH_FASTCALL, nullptr},
                          {"cache_write", method(cache_write), METH_FASTCALL, nullptr},
                          {"cache_read", method(cache_read), METH_FASTCALL, nullptr},
                          {"cache_attention", method(cache_attention), METH_FASTCALL, nullptr},
+                         {"cache_copy", method(cache_copy), METH_FASTCALL, nullptr},
+                         {"cache_resize", method(cache_resize), METH_FASTCALL, nullptr},
+                         {"cache_fork", method(cache_fork), METH_FASTCALL, nullptr},
+                         {"cache_compact", method(cache_compact), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "kda_cache_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -279,4 +279,133 @@ kda_status kda_cache_attention(const void* q, int64_t q_stride, const void* k_co
                     "kda_cache_attention launch");
 }
 
+static kda_status check_rows(int64_t n_pages, int n_rows, int table_pages, int n) {
+    KDA_REQUIRE(n_pages >= 0 && n_rows >= 0 && table_pages >= 0 && n >= 0, KDA_ERR_INVALID_ARG,
+                "bad sizes n_pages=%lld n_rows=%d table_pages=%d n=%d", (long long)n_pages, n_rows, table_pages, n);
+    KDA_REQUIRE(n_pages <= INT32_MAX, KDA_ERR_UNSUPPORTED, "n_pages must be below 2^31");
+    KDA_REQUIRE(n <= kda::cache_pages_most_rows(), KDA_ERR_UNSUPPORTED, "at most %d rows a call (%d)",
+                kda::cache_pages_most_rows(), n);
+    KDA_REQUIRE((int64_t)n * table_pages <= INT32_MAX, KDA_ERR_UNSUPPORTED, "n * table_pages must be below 2^31");
+    return KDA_OK;
+}
+
+static kda_status make_pages(kda::CachePages& p, int32_t* refs, int64_t n_pages, int32_t* table, int n_rows,
+                             int table_pages, int n, int page, int32_t* missing) {
+    const kda_status st = check_rows(n_pages, n_rows, table_pages, n);
+    if (st != KDA_OK) return st;
+    KDA_REQUIRE(page >= 16 && page <= 256 && (page & (page - 1)) == 0, KDA_ERR_UNSUPPORTED,
+                "a page is 16, 32, 64, 128 or 256 tokens (%d)", page);
+    KDA_REQUIRE((int64_t)table_pages * page <= INT32_MAX, KDA_ERR_UNSUPPORTED,
+                "table_pages * page must be below 2^31");
+    KDA_REQUIRE(aligned(missing, 4), KDA_ERR_INVALID_ARG, "missing is not 4-byte aligned");
+    p.refs = refs;
+    p.table = table;
+    p.missing = missing;
+    p.n_pages = n_pages;
+    p.n_rows = n_rows;
+    p.table_pages = table_pages;
+    p.page_shift = log2_of(page);
+    p.n = n;
+    return KDA_OK;
+}
+
+static kda_status check_pages_workspace(int64_t n_pages, const void* workspace, size_t workspace_bytes) {
+    const size_t need = kda::cache_pages_workspace_bytes(n_pages);
+    if (need == 0) return KDA_OK;
+    KDA_REQUIRE(workspace != nullptr && workspace_bytes >= need, KDA_ERR_WORKSPACE,
+                "workspace of %zu bytes required, got %zu at %p", need, workspace_bytes, workspace);
+    KDA_REQUIRE(aligned(workspace, 256), KDA_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+    return KDA_OK;
+}
+
+size_t kda_cache_pages_workspace_size(int64_t n_pages) {
+    return n_pages < 0 || n_pages > INT32_MAX ? 0 : kda::cache_pages_workspace_bytes(n_pages);
+}
+
+kda_status kda_cache_copy(void* k_codes, void* v_codes, float* k_scale, float* v_scale, const int32_t* src,
+                          const int32_t* dst, int n, int H_kv, int d, int64_t n_pages, int page, cudaStream_t stream) {
+    KDA_REQUIRE(n >= 0, KDA_ERR_INVALID_ARG, "bad size n=%d", n);
+    const kda_status st = check_pool(H_kv, d, n_pages, page, 0);
+    if (st != KDA_OK) return st;
+    KDA_REQUIRE((int64_t)n * H_kv <= INT32_MAX / 16, KDA_ERR_UNSUPPORTED,
+                "too many pages and heads for one call (%d pages, %d heads)", n, H_kv);
+    if (n == 0 || n_pages == 0) return ok();
+    KDA_POINTER(k_codes, 16);
+    KDA_POINTER(v_codes, 16);
+    KDA_POINTER(k_scale, 4);
+    KDA_POINTER(v_scale, 4);
+    KDA_POINTER(src, 4);
+    KDA_POINTER(dst, 4);
+    return launched(kda::run_cache_copy(k_codes, v_codes, k_scale, v_scale, src, dst, n, H_kv, d, n_pages, page, stream),
+                    "kda_cache_copy launch");
+}
+
+kda_status kda_cache_resize(int32_t* refs, int64_t n_pages, int32_t* block_table, int n_rows, int table_pages,
+                            const int32_t* rows, const int32_t* tokens, int n, int page, int32_t* missing,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    kda::CachePages p;
+    kda_status st = make_pages(p, refs, n_pages, block_table, n_rows, table_pages, n, page, missing);
+    if (st != KDA_OK) return st;
+    if (n > 0) {
+        KDA_POINTER(rows, 4);
+        KDA_POINTER(tokens, 4);
+    }
+    if (n_rows > 0 && table_pages > 0) KDA_POINTER(block_table, 4);
+    if (n_pages > 0) KDA_POINTER(refs, 4);
+    st = check_pages_workspace(n_pages, workspace, workspace_bytes);
+    if (st != KDA_OK) return st;
+    if (!missing && (n == 0 || n_rows == 0 || table_pages == 0)) return ok();
+    return launched(kda::run_cache_resize(p, rows, tokens, workspace, stream), "kda_cache_resize launch");
+}
+
+kda_status kda_cache_fork(int32_t* refs, int64_t n_pages, int32_t* block_table, int n_rows, int table_pages,
+                          int32_t* lengths, const int32_t* src, const int32_t* dst, int n, int page,
+                          int32_t* from_pages, int32_t* to_pages, int32_t* missing, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream) {
+    kda::CachePages p;
+    kda_status st = make_pages(p, refs, n_pages, block_table, n_rows, table_pages, n, page, missing);
+    if (st != KDA_OK) return st;
+    if (n > 0) {
+        KDA_POINTER(src, 4);
+        KDA_POINTER(dst, 4);
+        KDA_POINTER(from_pages, 4);
+        KDA_POINTER(to_pages, 4);
+    }
+    if (n_rows > 0) KDA_POINTER(lengths, 4);
+    if (n_rows > 0 && table_pages > 0) KDA_POINTER(block_table, 4);
+    if (n_pages > 0) KDA_POINTER(refs, 4);
+    st = check_pages_workspace(n_pages, workspace, workspace_bytes);
+    if (st != KDA_OK) return st;
+    if (!missing && n == 0) return ok();
+    return launched(kda::run_cache_fork(p, lengths, src, dst, from_pages, to_pages, workspace, stream),
+                    "kda_cache_fork launch");
+}
+
+kda_status kda_cache_compact(const int32_t* refs, int32_t* refs_out, int64_t n_pages, const int32_t* block_table,
+                             int32_t* block_table_out, int n_rows, int table_pages, int32_t* page_map,
+                             int32_t* from_pages, int32_t* to_pages, int32_t* held, cudaStream_t stream) {
+    KDA_REQUIRE(n_pages >= 0 && n_rows >= 0 && table_pages >= 0, KDA_ERR_INVALID_ARG,
+                "bad sizes n_pages=%lld n_rows=%d table_pages=%d", (long long)n_pages, n_rows, table_pages);
+    KDA_REQUIRE(n_pages <= INT32_MAX - 4096, KDA_ERR_UNSUPPORTED, "n_pages must be below 2^31 - 4096");
+    const int64_t entries = (int64_t)n_rows * table_pages;
+    KDA_REQUIRE(entries <= (int64_t)INT32_MAX * 64, KDA_ERR_UNSUPPORTED, "the block table must have less than 2^37 entries");
+    KDA_POINTER(held, 4);
+    if (n_pages > 0) {
+        KDA_POINTER(refs, 4);
+        KDA_POINTER(refs_out, 4);
+        KDA_POINTER(page_map, 4);
+    }
+    if (n_pages > 1) {
+        KDA_POINTER(from_pages, 4);
+        KDA_POINTER(to_pages, 4);
+    }
+    if (entries > 0) {
+        KDA_POINTER(block_table, 4);
+        KDA_POINTER(block_table_out, 4);
+    }
+    return launched(kda::run_cache_compact(refs, refs_out, n_pages, block_table, block_table_out, entries, page_map,
+                                           from_pages, to_pages, held, stream),
+                    "kda_cache_compact launch");
+}
+
 }  // extern "C"

@@ -513,6 +513,76 @@ size_t kda_cache_attention_workspace_size(int B, int T_q, int H_q, int H_kv, int
                                           int table_pages);
 
 /*
+ * Sequences that share pages.  A block table's rows may hold the same page; beside the table the caller keeps
+ *   refs  device int32 [n_pages]: how many entries of block tables hold each page (and one more for each further
+ *         holder of the caller's own); a page with 0 is free.  A new pool's are all 0.
+ * The calls below keep refs and one table [n_rows, table_pages] in step, on the device: nothing is read back, so they
+ * can be captured.  Layers that share a block table share refs; their pools' pages are copied layer by layer, by
+ * kda_cache_copy with the lists of pages that kda_cache_fork and kda_cache_compact write.  Pages are taken lowest first in the order
+ * of what asks, so results do not depend on timing.  An entry outside [0, n_pages) holds nothing.
+ *   workspace  kda_cache_pages_workspace_size(n_pages) bytes, 256-byte aligned; contents on entry are ignored
+ *   missing    nullable; device int32 [1] (written): pages that were wanted and not there
+ * All tables, lists and counts are dense and apart from one another unless stated; at most 65536 rows or pairs a call,
+ * and n * table_pages below 2^31.
+ */
+
+/*
+ * kda_cache_copy -- copies page src[i] to page dst[i] (device int32 [n]), codes and scales of all heads, for each i
+ * whose two pages are in the pool.  No page may be the target of two pairs, or of one and the source of another (the contents
+ * of such pages are unspecified); a pair of one page twice changes nothing.
+ */
+kda_status kda_cache_copy(void *k_codes, void *v_codes, float *k_scale, float *v_scale,
+                          const int32_t *src, const int32_t *dst, int n, int H_kv, int d,
+                          int64_t n_pages, int page, cudaStream_t stream);
+
+/*
+ * kda_cache_resize -- takes and gives back: each listed row comes to hold ceil(tokens / page) pages (at most
+ * table_pages; tokens below 1: none).  Entries past these are given back (refs less one, the entry -1); entries
+ * among these that hold nothing get free pages, in the order of (listed row, entry), the lowest
+ * page first, after all that goes back has gone; where the pool has no more they become -1 and count as missing.
+ *   rows, tokens  device int32 [n]; a row outside the table is skipped, and of a row listed twice the first counts
+ */
+kda_status kda_cache_resize(int32_t *refs, int64_t n_pages, int32_t *block_table, int n_rows,
+                            int table_pages, const int32_t *rows, const int32_t *tokens, int n,
+                            int page, int32_t *missing, void *workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
+
+/*
+ * kda_cache_fork -- row dst[i] becomes the sequence of row src[i], of lengths[src[i]] tokens: its full pages are shared
+ * (refs and one), a partly filled last page is replaced by a free one, the rest of the row holds nothing, and
+ * lengths[dst[i]] is set.  What row dst[i] held is not given back (resize it to 0 first).  For each i
+ *   from_pages[i], to_pages[i]  (written) the page to copy before the row's next token, and where to; -1 and -1
+ *                               where there is none: full pages only, a last page that is not held, or no free page (the
+ *                               row's entry is then -1 and counts as missing)
+ *   lengths   device int32 [n_rows], clamped into [0, table_pages * page]
+ *   src, dst  device int32 [n]; a source may stand in many pairs.  A pair is skipped where a row is outside the table,
+ *             where dst[i] is an earlier pair's, or some pair's source.
+ */
+kda_status kda_cache_fork(int32_t *refs, int64_t n_pages, int32_t *block_table, int n_rows,
+                          int table_pages, int32_t *lengths, const int32_t *src,
+                          const int32_t *dst, int n, int page, int32_t *from_pages,
+                          int32_t *to_pages, int32_t *missing, void *workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes of kda_cache_resize and kda_cache_fork (0 for sizes they do not take). */
+size_t kda_cache_pages_workspace_size(int64_t n_pages);
+
+/*
+ * kda_cache_compact -- brings the held pages (refs > 0), `held` in number, to [0, held): the k-th of them from page
+ * `held` on moves to the k-th free page before it; the others stay.
+ *   refs, refs_out                int32 [n_pages], may be one buffer
+ *   block_table, block_table_out  int32 [n_rows, table_pages], may be one buffer; entries that hold nothing become -1
+ *   page_map                      int32 [n_pages] (written): where each held page is now, -1 for the others; for tables
+ *                                 of the caller's own
+ *   from_pages, to_pages          int32 [n_pages / 2] (written): the moves, in order, for kda_cache_copy; -1 past the last
+ *   held                          int32 [1] (written)
+ */
+kda_status kda_cache_compact(const int32_t *refs, int32_t *refs_out, int64_t n_pages,
+                             const int32_t *block_table, int32_t *block_table_out, int n_rows,
+                             int table_pages, int32_t *page_map, int32_t *from_pages,
+                             int32_t *to_pages, int32_t *held, cudaStream_t stream);
+
+/*
  * Instrumentation (not part of the layer's arithmetic).  While `events` is
  * non-NULL, every later prefill, decode or speculative call made on this
  * thread records events[0] on its stream before its first kernel and
