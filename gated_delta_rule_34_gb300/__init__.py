@@ -12,7 +12,8 @@ from .api import (KDAError, auto_segments, chunk_prefill, chunk_prefill_from_hos
                   set_profile_events, spec_commit,
                   segmented_workspace_size, spec_verify, static_workspace_status,
                   workspace_size)
-from .cache import (PagedCache, cache_attention, cache_attention_workspace_size, cache_compact,  # noqa: F401
+from .cache import (PagedCache, cache_attention, cache_attention_shared,  # noqa: F401
+                    cache_attention_shared_workspace_size, cache_attention_workspace_size, cache_compact,
                     cache_copy, cache_fork, cache_new, cache_pages_workspace_size, cache_read, cache_resize,
                     cache_write, rotary, rotary_frequencies)
 
@@ -22,5 +23,5 @@ __all__ = ["KDAError", "auto_segments", "chunk_prefill", "chunk_prefill_segmente
            "selftest_bounded_wait",
            "set_profile_events", "spec_commit", "spec_verify", "static_workspace_status",
            "workspace_size", "PagedCache", "cache_attention", "cache_attention_workspace_size",
-           "cache_compact", "cache_copy", "cache_fork", "cache_new", "cache_pages_workspace_size",
+           "cache_attention_shared", "cache_attention_shared_workspace_size", "cache_compact", "cache_copy", "cache_fork", "cache_new", "cache_pages_workspace_size",
            "cache_read", "cache_resize", "cache_write", "rotary", "rotary_frequencies"]

@@ -96,6 +96,11 @@ def _declare(lib):
     lib.kda_cache_attention.restype = i32
     lib.kda_cache_attention_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
     lib.kda_cache_attention_workspace_size.restype = sz
+    lib.kda_cache_attention_shared.argtypes = [vp, i64, vp, vp, vp, vp, vp, i32, vp, vp, i32, vp, vp, i32, vp, vp, i32,
+                                               i32, i32, i32, i32, i64, i32, f32, i32, vp, sz, vp]
+    lib.kda_cache_attention_shared.restype = i32
+    lib.kda_cache_attention_shared_workspace_size.argtypes = [i32] * 9
+    lib.kda_cache_attention_shared_workspace_size.restype = sz
     lib.kda_cache_copy.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i64, i32, vp]
     lib.kda_cache_copy.restype = i32
     lib.kda_cache_resize.argtypes = [vp, i64, vp, i32, i32, vp, vp, i32, i32, vp, vp, sz, vp]

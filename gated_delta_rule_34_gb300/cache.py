@@ -31,7 +31,9 @@ def _binding():
     entries = [getattr(lib(), name) for name in ("kda_rotary", "kda_cache_write", "kda_cache_read",
                                                  "kda_cache_attention", "kda_cache_attention_workspace_size",
                                                  "kda_cache_copy", "kda_cache_resize", "kda_cache_fork",
-                                                 "kda_cache_compact", "kda_cache_pages_workspace_size")]
+                                                 "kda_cache_compact", "kda_cache_pages_workspace_size",
+                                                 "kda_cache_attention_shared",
+                                                 "kda_cache_attention_shared_workspace_size")]
     if not os.path.exists(_build.BINDING):
         raise RuntimeError(
             f"KDA binding not found at {_build.BINDING}; build it with "
@@ -301,6 +303,50 @@ def cache_attention(q, cache: PagedCache, block_table, lengths, scale: float | N
     if workspace is not None and (workspace.get_device() != index or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be a contiguous CUDA tensor on {q.device}")
     _not_understood("cache_attention")
+
+
+def cache_attention_shared_workspace_size(B: int, T_q: int, H_q: int, H_kv: int, d: int, page: int, table_pages: int,
+                                          prefix_pages: int, n_groups: int) -> int:
+    return int(lib().kda_cache_attention_shared_workspace_size(B, T_q, H_q, H_kv, d, page, table_pages, prefix_pages, n_groups))
+
+
+def cache_attention_shared(q, cache: PagedCache, block_table, lengths, prefix_table, prefix_lengths, cu_groups,
+                           scale: float | None = None, out=None, lse=None, return_lse: bool = False, workspace=None):
+    """cache_attention (without a window) for sequences in groups that share a prefix, which is read once for each group,
+    through kda_cache_attention_shared.
+
+    q, cache, block_table, lengths, scale, out, lse, return_lse, workspace: as in cache_attention; the rows of block_table hold
+    each sequence from its first token on, as cache_fork leaves them.  prefix_table: int32 [G, prefix_pages], the pages of each
+    group's prefix; prefix_lengths: int32 [G], its tokens, of which whole pages are shared; cu_groups: int32 [G + 1], group g
+    is sequences cu_groups[g] .. cu_groups[g + 1] - 1.  A sequence some of whose queries do not see all of the prefix attends
+    over its own row alone.
+    """
+    done = _binding().cache_attention_shared(q, cache, block_table, lengths, prefix_table, prefix_lengths, cu_groups, scale, out, lse,
+                                             return_lse, workspace)
+    if done is not None:
+        return done
+    index = q.get_device()
+    if _is_elsewhere(index):
+        with torch.cuda.device(index):
+            return cache_attention_shared(q, cache, block_table, lengths, prefix_table, prefix_lengths, cu_groups, scale, out, lse,
+                                          return_lse, workspace)
+    shape, dtype = q.shape, q.dtype
+    _dtype_code(dtype)
+    _rows("q", q, dtype, index)
+    n_pages, h, page, d = _pool(cache, index)
+    if len(shape) != 4 or shape[3] != d:
+        raise ValueError(f"q must be [B, T_q, H_q, {d}], got {tuple(shape)}")
+    _tensor("block_table", block_table, I32, (shape[0], block_table.shape[-1]), index)
+    _tensor("lengths", lengths, I32, (shape[0],), index)
+    _tensor("prefix_table", prefix_table, I32, (-1, -1), index)
+    _tensor("prefix_lengths", prefix_lengths, I32, prefix_table.shape[:1], index)
+    _tensor("cu_groups", cu_groups, I32, (prefix_table.shape[0] + 1,), index)
+    if out is not None:
+        _tensor("out", out, dtype, shape, index)
+    if lse is not None:
+        _tensor("lse", lse, F32, shape[:3], index)
+    _workspace(workspace, index)
+    _not_understood("cache_attention_shared")
 
 
 def _workspace(workspace, index):

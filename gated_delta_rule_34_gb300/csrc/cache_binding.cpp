@@ -37,6 +37,8 @@ decltype(&kda_cache_resize) resize_entry;
 decltype(&kda_cache_fork) fork_entry;
 decltype(&kda_cache_compact) compact_entry;
 decltype(&kda_cache_pages_workspace_size) pages_workspace_entry;
+decltype(&kda_cache_attention_shared) shared_entry;
+decltype(&kda_cache_attention_shared_workspace_size) shared_workspace_entry;
 PyObject* check;                           // api._check
 
 const at::Tensor* tensor(PyObject* x) { return THPVariable_Check(x) ? &THPVariable_Unpack(x) : nullptr; }
@@ -511,8 +513,62 @@ PyObject* cache_compact(PyObject*, PyObject* const* arg, Py_ssize_t n_args) {
     END_HANDLE_TH_ERRORS
 }
 
+// q, cache, block_table, lengths, prefix_table, prefix_lengths, cu_groups, scale, out, lse, return_lse, workspace -> o or (o, lse)
+PyObject* cache_attention_shared(PyObject*, PyObject* const* arg, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    if (!takes("cache_attention_shared", n_args, 12)) return nullptr;
+    const at::Tensor *q = tensor(arg[0]), *table = tensor(arg[2]), *lengths = tensor(arg[3]);
+    const at::Tensor *prefix = tensor(arg[4]), *prefix_len = tensor(arg[5]), *cu = tensor(arg[6]);
+    const int index = current_device_of(q);
+    kda_dtype code;
+    if (index < 0 || !code_of(q->scalar_type(), code) || q->dim() != 4) Py_RETURN_NONE;
+    const at::ScalarType type = q->scalar_type();
+    const int64_t q_stride = token_stride(q, type, index);
+    Pool pool;
+    if (q_stride < 0 || !pool.read(arg[1], index) || q->size(3) != pool.d) Py_RETURN_NONE;
+    const int64_t B = q->size(0), t_q = q->size(1), h_q = q->size(2);
+    if (!dense(table, at::kInt, index) || table->dim() != 2 || table->size(0) != B || !dense(lengths, at::kInt, index, {B}) ||
+        B > INT_MAX || t_q > INT_MAX || h_q > INT_MAX || table->size(1) > INT_MAX)
+        Py_RETURN_NONE;
+    if (!dense(prefix, at::kInt, index) || prefix->dim() != 2 || prefix->size(0) >= INT_MAX || prefix->size(1) > INT_MAX ||
+        !dense(prefix_len, at::kInt, index, {prefix->size(0)}) || !dense(cu, at::kInt, index, {prefix->size(0) + 1}))
+        Py_RETURN_NONE;
+    const int wide = (int)table->size(1), d = (int)pool.d, groups = (int)prefix->size(0), prefix_wide = (int)prefix->size(1);
+    float scale = (float)(1.0 / std::sqrt((double)d));
+    if (arg[7] != Py_None && !real(arg[7], scale)) return nullptr;
+    const int with_lse = PyObject_IsTrue(arg[10]);
+    if (with_lse < 0) return nullptr;
+
+    at::Tensor o_made, lse_made;
+    const at::Tensor *o = &o_made, *lse = arg[9] != Py_None ? tensor(arg[9]) : with_lse ? &lse_made : nullptr;
+    if (arg[8] != Py_None && !dense(o = tensor(arg[8]), type, index, q->sizes())) Py_RETURN_NONE;
+    if (arg[9] != Py_None && !dense(lse, at::kFloat, index, q->sizes().slice(0, 3))) Py_RETURN_NONE;
+    Workspace ws;
+    const size_t need = arg[11] == Py_None ? shared_workspace_entry((int)B, (int)t_q, (int)h_q, (int)pool.h, d,
+                                                                    (int)pool.page, wide, prefix_wide, groups)
+                                           : 0;
+    if (!ws.read(arg[11], need, index, *q)) Py_RETURN_NONE;
+    if (arg[8] == Py_None) o_made = empty(q->sizes(), type, *q);
+    if (lse == &lse_made) lse_made = empty(q->sizes().slice(0, 3), at::kFloat, *q);
+    const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(index).stream();
+    kda_status status;
+    Py_BEGIN_ALLOW_THREADS
+    status = shared_entry(q->const_data_ptr(), q_stride, pool.k->const_data_ptr(), pool.v->const_data_ptr(),
+                          pool.k_scale->const_data_ptr<float>(), pool.v_scale->const_data_ptr<float>(),
+                          table->const_data_ptr<int32_t>(), wide, lengths->const_data_ptr<int32_t>(),
+                          prefix->const_data_ptr<int32_t>(), prefix_wide, prefix_len->const_data_ptr<int32_t>(),
+                          cu->const_data_ptr<int32_t>(), groups, o->mutable_data_ptr(),
+                          lse ? lse->mutable_data_ptr<float>() : nullptr, (int)B, (int)t_q, (int)h_q, (int)pool.h, d,
+                          pool.n_pages, (int)pool.page, scale, code, ws.ptr(), ws.bytes(), stream);
+    Py_END_ALLOW_THREADS
+    if (failed(status)) return nullptr;
+    PyObject* out = result(arg[8], o_made);
+    return with_lse ? pair_of(out, result(arg[9], lse_made)) : out;
+    END_HANDLE_TH_ERRORS
+}
+
 // The addresses of the entries, in the order of cache.py's list, and api._check
-constexpr int kEntries = 10;
+constexpr int kEntries = 12;
 PyObject* bind(PyObject*, PyObject* const* arg, Py_ssize_t n_args) {
     if (!takes("bind", n_args, kEntries + 1)) return nullptr;
     void* at[kEntries];
@@ -530,6 +586,8 @@ PyObject* bind(PyObject*, PyObject* const* arg, Py_ssize_t n_args) {
     fork_entry = reinterpret_cast<decltype(fork_entry)>(at[7]);
     compact_entry = reinterpret_cast<decltype(compact_entry)>(at[8]);
     pages_workspace_entry = reinterpret_cast<decltype(pages_workspace_entry)>(at[9]);
+    shared_entry = reinterpret_cast<decltype(shared_entry)>(at[10]);
+    shared_workspace_entry = reinterpret_cast<decltype(shared_workspace_entry)>(at[11]);
     Py_XDECREF(check);
     check = Py_NewRef(arg[kEntries]);
     Py_RETURN_NONE;
@@ -543,6 +601,7 @@ PyMethodDef methods[] = {{"bind", method(bind), METH_FASTCALL, nullptr},
                          {"cache_write", method(cache_write), METH_FASTCALL, nullptr},
                          {"cache_read", method(cache_read), METH_FASTCALL, nullptr},
                          {"cache_attention", method(cache_attention), METH_FASTCALL, nullptr},
+                         {"cache_attention_shared", method(cache_attention_shared), METH_FASTCALL, nullptr},
                          {"cache_copy", method(cache_copy), METH_FASTCALL, nullptr},
                          {"cache_resize", method(cache_resize), METH_FASTCALL, nullptr},
                          {"cache_fork", method(cache_fork), METH_FASTCALL, nullptr},

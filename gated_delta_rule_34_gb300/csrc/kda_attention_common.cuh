@@ -12,6 +12,10 @@
 namespace kda {
 namespace attn {
 
+// What a launch attends over: a sequence's whole cache; the prefix that a group of sequences shares, all their rows as one
+// item's, whose sums are carried on; the rest of a sequence, joined with what its rows carry.
+enum Part { kAll, kPrefix, kRest };
+
 constexpr int kStep = 16;             // tokens of a step; a page holds whole steps
 constexpr int kMinShare = 16;         // steps below which no item is cut further
 constexpr int kJoinThreads = 256;
@@ -34,6 +38,7 @@ struct Plan {
     int rows;           // T_q * group
     int tile_rows;      // rows of a tile
     int row_tiles;
+    int pairs;          // kPrefix: (group, row tile) places, as groups_tile deals them out
     int stored;         // rows of a tile that exist
     int item_cost;      // what an item's start and end cost, in steps
     int cut;            // items are cut at multiples of this many steps
@@ -49,13 +54,80 @@ struct Tile {
     int end;            // tokens [0, end) at most
     int first_step;     // of the window (or 0), after sink_steps steps from 0
     int sink_steps;
-    int steps;          // at least 1, so that a row that sees nothing is written too
+    int steps;          // at least 1, so that a row that sees nothing is written too (kPrefix: 0 where there are no rows)
+    bool carried;       // kRest: rows go on from what they carry
     __device__ __forceinline__ int token(int s) const {
         return (s < sink_steps ? s : first_step + s - sink_steps) * kStep;
     }
 };
 
-__device__ __forceinline__ Tile make_tile(const CacheAttention& a, const Plan& plan, int len, int rt) {
+// Sequences of group g, and the tokens that they share: whole pages, and none for fewer than two sequences.
+__device__ __forceinline__ int2 group_range(const CacheAttention& a, int g, int n_seqs) {
+    int lo = a.cu_groups[g], hi = a.cu_groups[g + 1];
+    lo = lo < 0 ? 0 : lo > n_seqs ? n_seqs : lo;
+    hi = hi < lo ? lo : hi > n_seqs ? n_seqs : hi;
+    return make_int2(lo, hi);
+}
+__device__ __forceinline__ int shared_tokens(const CacheAttention& a, int g, int2 range) {
+    const int cap = a.prefix_pages << a.page_shift, n = a.prefix_len[g];
+    if (range.y - range.x < 2 || n <= 0) return 0;
+    return (n < cap ? n : cap) >> a.page_shift << a.page_shift;
+}
+// kRest: how many of sequence b's tokens its rows carry the sums of.  All of them must see all of the prefix; a
+// sequence whose rows do not attends over all of its own table.
+__device__ __forceinline__ int carried_tokens(const CacheAttention& a, int b, int len) {
+    int g = 0, end = a.n_groups;                           // the last group that starts at b or before
+    while (end - g > 1) {
+        const int mid = (g + end) >> 1;
+        if (a.cu_groups[mid] <= b) g = mid;
+        else end = mid;
+    }
+    const int2 range = group_range(a, g, a.B);
+    if (b < range.x || b >= range.y) return 0;
+    const int n = shared_tokens(a, g, range);
+    return len - a.T_q + 1 >= n ? n : 0;
+}
+
+// kPrefix: place `pair` of plan.pairs is row tile .y of group .x.  Group g's start at floor(rows before it / tile_rows) + g, which
+// leaves each room enough wherever its rows begin.  (a.B: sequences, as everywhere.)
+__device__ __forceinline__ int groups_first(const CacheAttention& a, const Plan& plan, int g) {
+    int lo = a.cu_groups[g];
+    lo = lo < 0 ? 0 : lo > a.B ? a.B : lo;
+    return (int)((int64_t)lo * plan.group * a.T_q / plan.tile_rows) + g;
+}
+__device__ __forceinline__ int2 groups_tile(const CacheAttention& a, const Plan& plan, int pair) {
+    int g = 0, end = a.n_groups;
+    while (end - g > 1) {
+        const int mid = (g + end) >> 1;
+        if (groups_first(a, plan, mid) <= pair) g = mid;
+        else end = mid;
+    }
+    return make_int2(g, pair - groups_first(a, plan, g));
+}
+
+// (sequence or group, row tile) of a pair.
+template <Part P>
+__device__ __forceinline__ int2 split_pair(const CacheAttention& a, const Plan& plan, int pair) {
+    if constexpr (P == kPrefix) return groups_tile(a, plan, pair);
+    else return make_int2(pair / plan.row_tiles, pair % plan.row_tiles);
+}
+// The first query token of sequence or group b, and its rows.
+template <Part P>
+__device__ __forceinline__ int64_t first_query(const CacheAttention& a, int b) {
+    if constexpr (P == kPrefix) return (int64_t)group_range(a, b, a.B).x * a.T_q;
+    else return (int64_t)b * a.T_q;
+}
+template <Part P>
+__device__ __forceinline__ int item_rows(const CacheAttention& a, const Plan& plan, int b) {
+    if constexpr (P == kPrefix) {
+        const int2 range = group_range(a, b, a.B);
+        return (range.y - range.x) * a.T_q * plan.group;
+    } else {
+        return plan.rows;
+    }
+}
+
+__device__ __forceinline__ Tile make_tile(const CacheAttention& a, const Plan& plan, int len, int rt, int carried = 0) {
     Tile t;
     if (plan.row_tiles == 1) {                             // no division on the way to a decode step's first loads
         t.p0 = len - a.T_q;
@@ -67,7 +139,8 @@ __device__ __forceinline__ Tile make_tile(const CacheAttention& a, const Plan& p
         t.p1 = len - a.T_q + r1 / plan.group;
     }
     t.end = t.p1 + 1 > 0 ? t.p1 + 1 : 0;
-    int lo = 0, sink_end = 0;
+    int lo = carried, sink_end = 0;
+    t.carried = carried > 0;
     if (a.window > 0) {
         const int64_t l = (int64_t)t.p0 - a.window + 1;
         lo = l > 0 ? (int)l : 0;
@@ -93,9 +166,29 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 // The tile of pair (sequence, row tile).
+template <Part P = kAll>
 __device__ __forceinline__ Tile tile_of(const CacheAttention& a, const Plan& plan, int pair) {
-    if (plan.row_tiles == 1) return make_tile(a, plan, length_of(a, pair), 0);
-    return make_tile(a, plan, length_of(a, pair / plan.row_tiles), pair % plan.row_tiles);
+    if constexpr (P == kPrefix) {                          // every row sees all of the prefix
+        const int2 at = groups_tile(a, plan, pair);
+        const int2 range = group_range(a, at.x, a.B);
+        const int64_t rows = (int64_t)(range.y - range.x) * a.T_q * plan.group;
+        Tile t;
+        t.end = at.y >= 0 && (int64_t)at.y * plan.tile_rows < rows ? shared_tokens(a, at.x, range) : 0;
+        t.p0 = t.p1 = t.end - 1;
+        t.first_step = t.sink_steps = 0;
+        t.steps = t.end / kStep;
+        t.carried = false;
+        return t;
+    } else {
+        const int b = plan.row_tiles == 1 ? pair : pair / plan.row_tiles, len = length_of(a, b);
+        return make_tile(a, plan, len, plan.row_tiles == 1 ? 0 : pair % plan.row_tiles,
+                         P == kRest ? carried_tokens(a, b, len) : 0);
+    }
+}
+// What an item takes of the list of all items' steps: its cost first.
+template <Part P>
+__device__ __forceinline__ int span_of(const Plan& plan, const Tile& tile) {
+    return P == kPrefix && tile.steps == 0 ? 0 : tile.steps + plan.item_cost;
 }
 
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
@@ -146,16 +239,16 @@ struct Share {
 };
 
 // Every thread of the CTA calls it; each sums up some pairs' steps.
-template <int THREADS>
+template <int THREADS, Part P = kAll>
 __device__ __forceinline__ Share find_share(const CacheAttention& a, const Plan& plan) {
     __shared__ int64_t warp_sum_s[THREADS / 32];
     __shared__ int64_t found_base;
     __shared__ int found_pair;
-    const int pairs = a.B * plan.row_tiles;
+    const int pairs = P == kPrefix ? plan.pairs : a.B * plan.row_tiles;
     const int each = (pairs + THREADS - 1) / THREADS;
     const int q0 = threadIdx.x * each;
     int64_t mine = 0;
-    for (int q = q0; q < q0 + each && q < pairs; ++q) mine += tile_of(a, plan, q).steps + plan.item_cost;
+    for (int q = q0; q < q0 + each && q < pairs; ++q) mine += span_of<P>(plan, tile_of<P>(a, plan, q));
     int64_t before = mine;                                 // steps of one head, up to this thread's end
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) {
@@ -182,7 +275,7 @@ __device__ __forceinline__ Share find_share(const CacheAttention& a, const Plan&
         int64_t base = before;
         for (int q = q0; q < pairs; ++q) {
             // (its only pair: the one that its sum says)
-            const int64_t w = each == 1 ? mine * a.H_kv : (int64_t)a.H_kv * (tile_of(a, plan, q).steps + plan.item_cost);
+            const int64_t w = each == 1 ? mine * a.H_kv : (int64_t)a.H_kv * span_of<P>(plan, tile_of<P>(a, plan, q));
             if (s.begin < base + w) {
                 found_pair = q;
                 found_base = base;
@@ -200,14 +293,14 @@ __device__ __forceinline__ Share find_share(const CacheAttention& a, const Plan&
 // Calls f(pair, head, tile, from, to, slot, whole) for each piece of the share: steps [from, to) of
 // an item; `whole` where that is all of it, else its sums go to the CTA's slot.  Returns the
 // entry of `joins` for the item that begins here and ends in a later share.
-template <typename F>
+template <Part P = kAll, typename F>
 __device__ __forceinline__ int4 for_each_piece(const CacheAttention& a, const Plan& plan, const Share& s, F f) {
     int4 join = make_int4(-1, 0, 0, 0);
     if (s.pair < 0) return join;
     int pair = s.pair;
     int64_t base = s.base, at = s.begin;
-    Tile tile = tile_of(a, plan, pair);
-    int span = tile.steps + plan.item_cost;                // of an item in the list, its cost first
+    Tile tile = tile_of<P>(a, plan, pair);
+    int span = span_of<P>(plan, tile);                     // of an item in the list
     int hk = (int)((s.begin - base) / span);
     base += (int64_t)hk * span;                            // where the item begins
     auto step_at = [&](int64_t x) {
@@ -228,22 +321,30 @@ __device__ __forceinline__ int4 for_each_piece(const CacheAttention& a, const Pl
         base = item_end;
         if (++hk == a.H_kv && at < s.end) {
             hk = 0;
-            ++pair;
-            tile = tile_of(a, plan, pair);
-            span = tile.steps + plan.item_cost;
+            do {
+                ++pair;
+                tile = tile_of<P>(a, plan, pair);
+                span = span_of<P>(plan, tile);
+            } while (P == kPrefix && span == 0);           // (the share goes on: there is one)
         }
     }
     return join;
 }
 
 // Row r of a tile, as a row of o and lse.
+template <Part P = kAll>
 __device__ __forceinline__ int64_t output_row(const CacheAttention& a, const Plan& plan, int b, int hk, int rt,
                                               int r) {
     const int row = rt * plan.tile_rows + r, i = row / plan.group;
-    return ((int64_t)b * a.T_q + i) * a.H_q + hk * plan.group + row - i * plan.group;
+    return (first_query<P>(a, b) + i) * a.H_q + hk * plan.group + row - i * plan.group;
 }
 __device__ __forceinline__ int rows_of_tile(const Plan& plan, int rt) {
     const int n = plan.rows - rt * plan.tile_rows;
+    return n < plan.tile_rows ? n : plan.tile_rows;
+}
+template <Part P>
+__device__ __forceinline__ int rows_of_tile(const CacheAttention& a, const Plan& plan, int b, int rt) {
+    const int n = item_rows<P>(a, plan, b) - rt * plan.tile_rows;
     return n < plan.tile_rows ? n : plan.tile_rows;
 }
 
@@ -271,6 +372,29 @@ __device__ __forceinline__ void write_row(const CacheAttention& a, int64_t row, 
     if (ch == 0 && a.lse) a.lse[row] = row_lse(M, L);
 }
 
+// Sums (m, dm, l; o, four channels) and the sums (s; x) of other tokens: o becomes both's, (M, DM, L) their statistics.
+__device__ __forceinline__ void join_sums(float4& o, float& M, float& DM, float& L, const float4& s, const float4& x) {
+    const float m = fmaxf(M, s.x), dm = fminf(DM + (m - M), s.y + (m - s.x));
+    const float keep = ex2(M - m + (dm - DM)), add = ex2(s.x - m + (dm - s.y));
+    L = L * ex2(M - m) + s.z * ex2(s.x - m);
+    o = make_float4(o.x * keep + x.x * add, o.y * keep + x.y * add, o.z * keep + x.z * add, o.w * keep + x.w * add);
+    M = m;
+    DM = dm;
+}
+// What becomes of a finished row's sums: outputs (kRest: with what the row carries), or (kPrefix) what it carries.
+template <typename T, Part P, int D>
+__device__ __forceinline__ void finish_row(const CacheAttention& a, int64_t row, int ch, float4 o, float M, float DM, float L,
+                                           bool carried) {
+    if constexpr (P == kPrefix) {
+        *reinterpret_cast<float4*>(a.carry_sums + row * D + ch) = o;
+        if (ch == 0) a.carry_stats[row] = make_float4(M, DM, L, 0.0f);
+    } else {
+        if (P == kRest && carried)
+            join_sums(o, M, DM, L, a.carry_stats[row], *reinterpret_cast<const float4*>(a.carry_sums + row * D + ch));
+        write_row<T>(a, row, ch, o, M, DM, L);
+    }
+}
+
 }  // namespace attn
 
 // Bytes of the pieces' sums behind `grid` CTAs, their division into plan.joins, stats and sums,
@@ -279,6 +403,16 @@ size_t attention_piece_bytes(int64_t grid, int stored, int D);
 void set_attention_pieces(attn::Plan& plan, void* workspace, int64_t grid);
 cudaError_t run_attention_join(const CacheAttention& a, const attn::Plan& plan, bool bf16, int D, int64_t grid,
                                cudaStream_t stream);
+cudaError_t run_attention_join_rest(const CacheAttention& a, const attn::Plan& plan, bool bf16, int D, int64_t grid,
+                                    cudaStream_t stream);
+
+// The kernels for few rows, by what they attend over (one source file each, so that they compile side by side).
+size_t attention_rows_workspace_bytes(const CacheAttention& a, int num_sms);
+size_t attention_rest_rows_workspace_bytes(const CacheAttention& a, int num_sms);
+size_t attention_prefix_rows_workspace_bytes(const CacheAttention& a, int num_sms);
+cudaError_t run_attention_rows(const CacheAttention& a, bool bf16, void* workspace, cudaStream_t stream, int num_sms);
+cudaError_t run_attention_rest_rows(const CacheAttention& a, bool bf16, void* workspace, cudaStream_t stream, int num_sms);
+cudaError_t run_attention_prefix_rows(const CacheAttention& a, bool bf16, void* workspace, cudaStream_t stream, int num_sms);
 
 // The kernel for many bf16 rows (kda_cache_attention_tc.cu): its plan for these queries, how many CTAs share
 // the work out (0: each item is one CTA's), and the launch.
@@ -286,5 +420,6 @@ bool attention_tc_takes(const CacheAttention& a, bool bf16);
 attn::Plan attention_tc_plan(const CacheAttention& a);
 int64_t attention_tc_grid(const CacheAttention& a, const attn::Plan& plan, int num_sms);
 cudaError_t run_attention_tc(const CacheAttention& a, void* workspace, cudaStream_t stream, int num_sms);
+cudaError_t run_attention_tc_rest(const CacheAttention& a, void* workspace, cudaStream_t stream, int num_sms);
 
 }  // namespace kda

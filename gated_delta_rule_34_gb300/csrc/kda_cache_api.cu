@@ -226,22 +226,17 @@ size_t kda_cache_attention_workspace_size(int B, int T_q, int H_q, int H_kv, int
     return kda::cache_attention_workspace_bytes(a, sm_count());
 }
 
-kda_status kda_cache_attention(const void* q, int64_t q_stride, const void* k_codes,
-                               const void* v_codes, const float* k_scale, const float* v_scale,
-                               const int32_t* block_table, int table_pages, const int32_t* lengths,
-                               void* o, float* lse, int B, int T_q, int H_q, int H_kv, int d,
-                               int64_t n_pages, int page, float scale, int64_t window, int sinks,
-                               kda_dtype dtype, void* workspace, size_t workspace_bytes,
-                               cudaStream_t stream) {
-    KDA_REQUIRE(valid_dtype(dtype), KDA_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
-    kda::CacheAttention a = {};
-    const kda_status st = attention_sizes(a, B, T_q, H_q, H_kv, d, n_pages, page, table_pages);
-    if (st != KDA_OK) return st;
+// The rest of an attention call's checks, and its pointers.
+static kda_status attention_call(kda::CacheAttention& a, const void* q, int64_t q_stride, const void* k_codes,
+                                 const void* v_codes, const float* k_scale, const float* v_scale,
+                                 const int32_t* block_table, const int32_t* lengths, void* o, float* lse, float scale,
+                                 int64_t window, int sinks, kda_dtype dtype) {
+    const int64_t n_pages = a.n_pages;
     KDA_REQUIRE(window >= 0 && sinks >= 0, KDA_ERR_INVALID_ARG,
                 "window and sinks must not be negative (%lld, %d)", (long long)window, sinks);
     KDA_REQUIRE(std::isfinite(scale), KDA_ERR_INVALID_ARG, "scale is not finite");
-    KDA_STRIDE(q_stride, (int64_t)H_q * d);
-    if (B == 0 || T_q == 0) return ok();
+    KDA_STRIDE(q_stride, (int64_t)a.H_q * a.d);
+    if (a.B == 0 || a.T_q == 0) return KDA_OK;
     KDA_POINTER(q, 16);
     KDA_POINTER(o, 16);
     KDA_POINTER(lengths, 4);
@@ -252,7 +247,7 @@ kda_status kda_cache_attention(const void* q, int64_t q_stride, const void* k_co
         KDA_POINTER(k_scale, 4);
         KDA_POINTER(v_scale, 4);
     }
-    if (table_pages > 0) KDA_POINTER(block_table, 4);
+    if (a.table_pages > 0) KDA_POINTER(block_table, 4);
     a.q = q;
     a.q_stride = q_stride;
     // (a pool without pages is not read, but its address goes into empty copies)
@@ -268,15 +263,89 @@ kda_status kda_cache_attention(const void* q, int64_t q_stride, const void* k_co
     // (positions are below 2^31: a wider window is none, and differences with it stay in range)
     a.window = window > INT32_MAX ? 0 : window;
     a.sinks = sinks;
+    return KDA_OK;
+}
+
+static kda_status check_workspace(size_t need, const void* workspace, size_t workspace_bytes) {
+    if (need == 0) return KDA_OK;
+    KDA_REQUIRE(workspace != nullptr && workspace_bytes >= need, KDA_ERR_WORKSPACE,
+                "workspace of %zu bytes required, got %zu at %p", need, workspace_bytes, workspace);
+    KDA_REQUIRE(aligned(workspace, 256), KDA_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+    return KDA_OK;
+}
+
+kda_status kda_cache_attention(const void* q, int64_t q_stride, const void* k_codes,
+                               const void* v_codes, const float* k_scale, const float* v_scale,
+                               const int32_t* block_table, int table_pages, const int32_t* lengths,
+                               void* o, float* lse, int B, int T_q, int H_q, int H_kv, int d,
+                               int64_t n_pages, int page, float scale, int64_t window, int sinks,
+                               kda_dtype dtype, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream) {
+    KDA_REQUIRE(valid_dtype(dtype), KDA_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    kda::CacheAttention a = {};
+    kda_status st = attention_sizes(a, B, T_q, H_q, H_kv, d, n_pages, page, table_pages);
+    if (st == KDA_OK)
+        st = attention_call(a, q, q_stride, k_codes, v_codes, k_scale, v_scale, block_table, lengths, o, lse, scale,
+                            window, sinks, dtype);
+    if (st != KDA_OK) return st;
+    if (B == 0 || T_q == 0) return ok();
     const int sms = sm_count();
-    const size_t need = kda::cache_attention_workspace_bytes(a, sms);
-    if (need > 0) {
-        KDA_REQUIRE(workspace != nullptr && workspace_bytes >= need, KDA_ERR_WORKSPACE,
-                    "workspace of %zu bytes required, got %zu at %p", need, workspace_bytes, workspace);
-        KDA_REQUIRE(aligned(workspace, 256), KDA_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
-    }
+    st = check_workspace(kda::cache_attention_workspace_bytes(a, sms), workspace, workspace_bytes);
+    if (st != KDA_OK) return st;
     return launched(kda::run_cache_attention(a, dtype == KDA_DTYPE_BF16, workspace, stream, sms),
                     "kda_cache_attention launch");
+}
+
+static kda_status shared_sizes(kda::CacheAttention& a, int prefix_pages, int n_groups) {
+    KDA_REQUIRE(prefix_pages >= 0 && n_groups >= 0, KDA_ERR_INVALID_ARG, "bad sizes prefix_pages=%d n_groups=%d",
+                prefix_pages, n_groups);
+    KDA_REQUIRE(n_groups <= a.B, KDA_ERR_INVALID_ARG, "more groups than sequences (%d, %d)", n_groups, a.B);
+    KDA_REQUIRE((int64_t)n_groups * a.H_kv <= 1 << 30, KDA_ERR_UNSUPPORTED, "n_groups * H_kv must be at most 2^30");
+    KDA_REQUIRE(((int64_t)prefix_pages << a.page_shift) <= INT32_MAX, KDA_ERR_UNSUPPORTED,
+                "prefix_pages * page must be below 2^31");
+    a.prefix_pages = prefix_pages;
+    a.n_groups = n_groups;
+    return KDA_OK;
+}
+
+size_t kda_cache_attention_shared_workspace_size(int B, int T_q, int H_q, int H_kv, int d, int page, int table_pages,
+                                                 int prefix_pages, int n_groups) {
+    kda::CacheAttention a = {};
+    if (attention_sizes(a, B, T_q, H_q, H_kv, d, 0, page, table_pages) != KDA_OK ||
+        shared_sizes(a, prefix_pages, n_groups) != KDA_OK || B == 0 || T_q == 0)
+        return 0;
+    return kda::cache_attention_shared_workspace_bytes(a, sm_count());
+}
+
+kda_status kda_cache_attention_shared(const void* q, int64_t q_stride, const void* k_codes, const void* v_codes,
+                                      const float* k_scale, const float* v_scale, const int32_t* block_table,
+                                      int table_pages, const int32_t* lengths, const int32_t* prefix_table,
+                                      int prefix_pages, const int32_t* prefix_lengths, const int32_t* cu_groups,
+                                      int n_groups, void* o, float* lse, int B, int T_q, int H_q, int H_kv, int d,
+                                      int64_t n_pages, int page, float scale, kda_dtype dtype, void* workspace,
+                                      size_t workspace_bytes, cudaStream_t stream) {
+    KDA_REQUIRE(valid_dtype(dtype), KDA_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    kda::CacheAttention a = {};
+    kda_status st = attention_sizes(a, B, T_q, H_q, H_kv, d, n_pages, page, table_pages);
+    if (st == KDA_OK) st = shared_sizes(a, prefix_pages, n_groups);
+    if (st == KDA_OK)
+        st = attention_call(a, q, q_stride, k_codes, v_codes, k_scale, v_scale, block_table, lengths, o, lse, scale, 0, 0,
+                            dtype);
+    if (st != KDA_OK) return st;
+    if (B == 0 || T_q == 0) return ok();
+    if (n_groups > 0) {
+        KDA_POINTER(cu_groups, 4);
+        KDA_POINTER(prefix_lengths, 4);
+        if (prefix_pages > 0) KDA_POINTER(prefix_table, 4);
+    }
+    a.prefix_table = prefix_table;
+    a.prefix_len = prefix_lengths;
+    a.cu_groups = cu_groups;
+    const int sms = sm_count();
+    st = check_workspace(kda::cache_attention_shared_workspace_bytes(a, sms), workspace, workspace_bytes);
+    if (st != KDA_OK) return st;
+    return launched(kda::run_cache_attention_shared(a, dtype == KDA_DTYPE_BF16, workspace, stream, sms),
+                    "kda_cache_attention_shared launch");
 }
 
 static kda_status check_rows(int64_t n_pages, int n_rows, int table_pages, int n) {
@@ -306,15 +375,6 @@ static kda_status make_pages(kda::CachePages& p, int32_t* refs, int64_t n_pages,
     p.table_pages = table_pages;
     p.page_shift = log2_of(page);
     p.n = n;
-    return KDA_OK;
-}
-
-static kda_status check_pages_workspace(int64_t n_pages, const void* workspace, size_t workspace_bytes) {
-    const size_t need = kda::cache_pages_workspace_bytes(n_pages);
-    if (need == 0) return KDA_OK;
-    KDA_REQUIRE(workspace != nullptr && workspace_bytes >= need, KDA_ERR_WORKSPACE,
-                "workspace of %zu bytes required, got %zu at %p", need, workspace_bytes, workspace);
-    KDA_REQUIRE(aligned(workspace, 256), KDA_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
     return KDA_OK;
 }
 
@@ -352,7 +412,7 @@ kda_status kda_cache_resize(int32_t* refs, int64_t n_pages, int32_t* block_table
     }
     if (n_rows > 0 && table_pages > 0) KDA_POINTER(block_table, 4);
     if (n_pages > 0) KDA_POINTER(refs, 4);
-    st = check_pages_workspace(n_pages, workspace, workspace_bytes);
+    st = check_workspace(kda::cache_pages_workspace_bytes(n_pages), workspace, workspace_bytes);
     if (st != KDA_OK) return st;
     if (!missing && (n == 0 || n_rows == 0 || table_pages == 0)) return ok();
     return launched(kda::run_cache_resize(p, rows, tokens, workspace, stream), "kda_cache_resize launch");
@@ -374,7 +434,7 @@ kda_status kda_cache_fork(int32_t* refs, int64_t n_pages, int32_t* block_table, 
     if (n_rows > 0) KDA_POINTER(lengths, 4);
     if (n_rows > 0 && table_pages > 0) KDA_POINTER(block_table, 4);
     if (n_pages > 0) KDA_POINTER(refs, 4);
-    st = check_pages_workspace(n_pages, workspace, workspace_bytes);
+    st = check_workspace(kda::cache_pages_workspace_bytes(n_pages), workspace, workspace_bytes);
     if (st != KDA_OK) return st;
     if (!missing && n == 0) return ok();
     return launched(kda::run_cache_fork(p, lengths, src, dst, from_pages, to_pages, workspace, stream),

@@ -338,6 +338,7 @@ struct Issuer {
 };
 
 // ------------------------------------------------------------------ softmax
+template <Part P>
 struct Softmax {
     Cta c;
     int tile_n = 0;
@@ -676,12 +677,22 @@ struct Softmax {
         if (threadIdx.x < kRows) {
             const int r = threadIdx.x;
             const float L = dead ? NAN : (rows->part[0][r] + rows->part[1][r]) + (rows->part[2][r] + rows->part[3][r]);
-            const uint32_t empty = __ballot_sync(0xffffffffu, L == 0.0f);
+            float L_all = L, M_all = rows->m[r], DM_all = rows->dm[r], keep = 1.0f;
+            if (P == kRest && whole && tile.carried && r < rows_here) {   // with what the row carries
+                const float4 s = a.carry_stats[output_row(a, plan, b, hk, rt, r)];
+                const float m = rows->unset[r / kMine] >> r % kMine & 1 ? kLowest : M_all;
+                M_all = fmaxf(m, s.x);
+                DM_all = fminf(rows->dm[r] + (M_all - m), s.y + (M_all - s.x));
+                L_all = L * ex2(m - M_all) + s.z * ex2(s.x - M_all);
+                keep = ex2(m - M_all + (DM_all - rows->dm[r]));
+                rows->lift[r] = row_factor(DM_all, L_all) * ex2(s.x - M_all + (DM_all - s.y));
+            }
+            const uint32_t empty = __ballot_sync(0xffffffffu, L_all == 0.0f);
             if (r % kMine == 0) rows->empty[r / kMine] = empty >> r;
-            rows->keep_o[r] = row_factor(rows->dm[r], L);
+            rows->keep_o[r] = P == kRest ? row_factor(DM_all, L_all) * keep : row_factor(rows->dm[r], L);
             if (r < rows_here) {
                 if (!whole) plan.stats[place + r] = make_float4(rows->unset[r / kMine] >> r % kMine & 1 ? kLowest : rows->m[r], rows->dm[r], L, 0.0f);
-                else if (a.lse) a.lse[output_row(a, plan, b, hk, rt, r)] = row_lse(rows->m[r], L);
+                else if (a.lse) a.lse[output_row(a, plan, b, hk, rt, r)] = row_lse(M_all, L_all);
             }
         }
         float o[16];
@@ -702,13 +713,20 @@ struct Softmax {
             // row r's place in a query token's heads: after the last one, the next token's first
             int in_token = (rt * kRows + r0) % plan.group;
             __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.o) + output_row(a, plan, b, hk, rt, r0) * a.d + t;
+            const float* carry = P == kRest && tile.carried ? a.carry_sums + output_row(a, plan, b, hk, rt, r0) * 128 + t : nullptr;
 #pragma unroll
             for (int y = 0; y < 16; ++y) {
-                if (r0 + y < rows_here) *to = __float2bfloat16_rn(empty >> y & 1 ? 0.0f : o[y] * rows->keep_o[r0 + y]);
+                if (r0 + y < rows_here) {
+                    float x = o[y] * rows->keep_o[r0 + y];
+                    if (P == kRest && carry) x = fmaf(*carry, rows->lift[r0 + y], x);
+                    *to = __float2bfloat16_rn(empty >> y & 1 ? 0.0f : x);
+                }
                 to += a.d;
+                if (P == kRest && carry) carry += 128;
                 if (++in_token == plan.group) {
                     in_token = 0;
                     to += (int64_t)(a.H_q - plan.group) * a.d;
+                    if (P == kRest && carry) carry += (int64_t)(a.H_q - plan.group) * 128;
                 }
             }
         }
@@ -716,7 +734,7 @@ struct Softmax {
     }
 };
 
-template <bool WHOLE>
+template <bool WHOLE, Part P>
 __global__ void __launch_bounds__(kThreads, kCtas) attention_tc_kernel(const CacheAttention a, const Plan plan) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -743,21 +761,21 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_tc_kernel(const Cac
     __syncthreads();
     tc::tc_fence_after();
     Share share = {};
-    if (!WHOLE) share = find_share<kThreads>(a, plan);
+    if (!WHOLE) share = find_share<kThreads, P>(a, plan);
     const Cta cta{a, plan, sm, bar, reinterpret_cast<Rows*>(sm + kRowsAt), bar->tmem};
     auto pieces = [&](auto f) {
         if constexpr (WHOLE) {
             const int pair = blockIdx.x / a.H_kv;
-            const Tile tile = tile_of(a, plan, pair);
+            const Tile tile = tile_of<P>(a, plan, pair);
             f(pair, (int)(blockIdx.x % a.H_kv), tile, 0, tile.steps, 0, true);
         } else {
-            const int4 join = for_each_piece(a, plan, share, f);
+            const int4 join = for_each_piece<P>(a, plan, share, f);
             if (threadIdx.x == 0) plan.joins[blockIdx.x] = join;
         }
     };
     if (warp < kSoftmax / 32) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        Softmax role{cta};
+        Softmax<P> role{cta};
         pieces([&](int pair, int hk, const Tile& tile, int from, int to, int slot, bool whole) {
             role.piece(pair, hk, tile, from, to, slot, whole);
         });
@@ -827,21 +845,33 @@ namespace {
 thread_local Stall stall;
 }
 
-cudaError_t run_attention_tc(const CacheAttention& a, void* workspace, cudaStream_t stream, int num_sms) {
+namespace {
+template <Part P>
+cudaError_t launch_tc(const CacheAttention& a, void* workspace, cudaStream_t stream, int num_sms) {
     Plan plan = attention_tc_plan(a);
     plan.stall = stall;
     const int64_t grid = attention_tc_grid(a, plan, num_sms);
     if (grid == 0) {
         const int64_t items = (int64_t)a.B * plan.row_tiles * a.H_kv;
-        cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<true, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
-        return launch_chained(attention_tc_kernel<true>, (unsigned)items, kThreads, kSmem, stream, a, plan);
+        return launch_chained(attention_tc_kernel<true, P>, (unsigned)items, kThreads, kSmem, stream, a, plan);
     }
     set_attention_pieces(plan, workspace, grid);
-    cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<false, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_chained(attention_tc_kernel<false>, (unsigned)grid, kThreads, kSmem, stream, a, plan);
-    return e != cudaSuccess ? e : run_attention_join(a, plan, true, 128, grid, stream);
+    e = launch_chained(attention_tc_kernel<false, P>, (unsigned)grid, kThreads, kSmem, stream, a, plan);
+    if (e != cudaSuccess) return e;
+    return P == kRest ? run_attention_join_rest(a, plan, true, 128, grid, stream)
+                      : run_attention_join(a, plan, true, 128, grid, stream);
+}
+}  // namespace
+
+cudaError_t run_attention_tc(const CacheAttention& a, void* workspace, cudaStream_t stream, int num_sms) {
+    return launch_tc<kAll>(a, workspace, stream, num_sms);
+}
+cudaError_t run_attention_tc_rest(const CacheAttention& a, void* workspace, cudaStream_t stream, int num_sms) {
+    return launch_tc<kRest>(a, workspace, stream, num_sms);
 }
 
 }  // namespace kda

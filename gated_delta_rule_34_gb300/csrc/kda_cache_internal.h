@@ -56,10 +56,21 @@ struct CacheAttention {
     int page_shift;
     int sinks;
     float scale;               // of the scores
+    // Groups of sequences that share a prefix: null where there are none.
+    const int32_t* prefix_table;   // [n_groups][prefix_pages]
+    const int32_t* prefix_len;     // [n_groups]
+    const int32_t* cu_groups;      // [n_groups + 1]
+    float4* carry_stats;           // of each row of o over its group's prefix: m, dm, l
+    float* carry_sums;             // and its sums of v, rows of 64 or 128
+    int n_groups;
+    int prefix_pages;
 };
 size_t cache_attention_workspace_bytes(const CacheAttention& a, int num_sms);
 cudaError_t run_cache_attention(const CacheAttention& a, bool bf16, void* workspace,
                                 cudaStream_t stream, int num_sms);
+// The same where groups of sequences share a prefix (a.prefix_table, prefix_len, cu_groups; no window): each group's is read once.
+size_t cache_attention_shared_workspace_bytes(const CacheAttention& a, int num_sms);
+cudaError_t run_cache_attention_shared(CacheAttention a, bool bf16, void* workspace, cudaStream_t stream, int num_sms);
 
 // Pages of a pool that rows of a block table hold, and how many entries hold each.
 struct CachePages {

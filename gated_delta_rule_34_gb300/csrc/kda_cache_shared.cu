@@ -1,0 +1,53 @@
+// kda_cache_shared.cu -- attention over the paged 8-bit cache for groups of sequences that share a prefix.
+//
+// softmax over two sets of tokens is that over each, joined: with (m, l, x) a row's largest score, its sum of
+// weights 2^(s - m) and its sum of weighted values over one set,
+//
+//   m = max(m1, m2),   l = l1 2^(m1 - m) + l2 2^(m2 - m),   x = x1 2^(m1 - m) + x2 2^(m2 - m),   o = x / l
+//
+// so a group's rows, all sequences' and all query tokens', meet its prefix once, as the rows of one product, and each
+// sequence the rest of its tokens by itself.  The first leaves (m, l, x) for each row in the workspace, the
+// second goes on from them where it writes its outputs.  The lengths are on the device, and so is the choice of what
+// is shared: whole pages, where two sequences or more share them, for the sequences all of whose queries see all of them.
+#include "kda_attention_common.cuh"
+
+namespace kda {
+namespace {
+
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
+int padded(const CacheAttention& a) { return a.d <= 64 ? 64 : 128; }
+size_t rows_of(const CacheAttention& a) { return (size_t)a.B * a.T_q * a.H_q; }
+size_t carry_bytes(const CacheAttention& a) {
+    return up(rows_of(a) * sizeof(float4)) + up(rows_of(a) * padded(a) * sizeof(float));
+}
+bool nothing_shared(const CacheAttention& a) { return a.n_groups == 0 || a.prefix_pages == 0; }
+
+size_t most(size_t x, size_t y) { return x > y ? x : y; }
+
+}  // namespace
+
+size_t cache_attention_shared_workspace_bytes(const CacheAttention& a, int num_sms) {
+    if (nothing_shared(a)) return cache_attention_workspace_bytes(a, num_sms);
+    // the two passes' pieces follow one another in the same place
+    size_t pieces = most(attention_prefix_rows_workspace_bytes(a, num_sms), attention_rest_rows_workspace_bytes(a, num_sms));
+    if (attention_tc_takes(a, true)) {
+        const attn::Plan plan = attention_tc_plan(a);
+        pieces = most(pieces, attention_piece_bytes(attention_tc_grid(a, plan, num_sms), plan.stored, 128));
+    }
+    // (a pool without pages holds nothing to share)
+    return most(carry_bytes(a) + pieces, cache_attention_workspace_bytes(a, num_sms));
+}
+
+cudaError_t run_cache_attention_shared(CacheAttention a, bool bf16, void* workspace, cudaStream_t stream, int num_sms) {
+    if (nothing_shared(a) || a.n_pages == 0) return run_cache_attention(a, bf16, workspace, stream, num_sms);
+    uint8_t* at = static_cast<uint8_t*>(workspace);
+    a.carry_stats = reinterpret_cast<float4*>(at);
+    a.carry_sums = reinterpret_cast<float*>(at + up(rows_of(a) * sizeof(float4)));
+    void* pieces = at + carry_bytes(a);
+    cudaError_t e = run_attention_prefix_rows(a, bf16, pieces, stream, num_sms);
+    if (e != cudaSuccess) return e;
+    if (attention_tc_takes(a, bf16)) return run_attention_tc_rest(a, pieces, stream, num_sms);
+    return run_attention_rest_rows(a, bf16, pieces, stream, num_sms);
+}
+
+}  // namespace kda

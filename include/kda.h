@@ -513,6 +513,38 @@ size_t kda_cache_attention_workspace_size(int B, int T_q, int H_q, int H_kv, int
                                           int table_pages);
 
 /*
+ * kda_cache_attention_shared -- kda_cache_attention (without a window) where groups of sequences share a prefix, whose
+ * keys and values are read and multiplied once for each group instead of once for each sequence.  Group g is sequences
+ * cu_groups[g] .. cu_groups[g + 1] - 1; its first prefix_lengths[g] tokens are those of the pages prefix_table[g].
+ *   prefix_table    device int32 [n_groups, prefix_pages]
+ *   prefix_lengths  device int32 [n_groups], clamped into [0, prefix_pages * page] and taken down to whole pages
+ *   cu_groups       device int32 [n_groups + 1], n_groups at most B, not decreasing.  Sequences before the first and behind the last
+ *                   share nothing, nor does a group of one.  Malformed ones are clamped: results are then unspecified, but
+ *                   no access leaves the buffers.
+ *   block_table     device int32 [B, table_pages]: each sequence's pages from its first token on, the prefix's among
+ *                   them, as kda_cache_fork leaves them.
+ * A sequence whose T_q queries all see all of the prefix takes it from prefix_table and the later tokens from its row of block_table;
+ * any other (a shorter one, a place not in use with length 0) takes all from its row.  So where both
+ * name the same pages, the results are those of kda_cache_attention but for the order of the sums.  Other arguments,
+ * roundings, rows that see nothing and waits as there.
+ *   workspace  kda_cache_attention_shared_workspace_size() bytes, 256-byte aligned; contents on entry are ignored
+ */
+kda_status kda_cache_attention_shared(const void *q, int64_t q_stride, const void *k_codes,
+                                      const void *v_codes, const float *k_scale,
+                                      const float *v_scale, const int32_t *block_table,
+                                      int table_pages, const int32_t *lengths,
+                                      const int32_t *prefix_table, int prefix_pages,
+                                      const int32_t *prefix_lengths, const int32_t *cu_groups,
+                                      int n_groups, void *o, float *lse, int B, int T_q, int H_q,
+                                      int H_kv, int d, int64_t n_pages, int page, float scale,
+                                      kda_dtype dtype, void *workspace, size_t workspace_bytes,
+                                      cudaStream_t stream);
+
+/* Workspace bytes of kda_cache_attention_shared (0 for sizes it does not take). */
+size_t kda_cache_attention_shared_workspace_size(int B, int T_q, int H_q, int H_kv, int d, int page,
+                                                 int table_pages, int prefix_pages, int n_groups);
+
+/*
  * Sequences that share pages.  A block table's rows may hold the same page; beside the table the caller keeps
  *   refs  device int32 [n_pages]: how many entries of block tables hold each page (and one more for each further
  *         holder of the caller's own); a page with 0 is free.  A new pool's are all 0.

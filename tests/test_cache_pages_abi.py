@@ -70,6 +70,30 @@ def test_compact_refusals(L, kw, status):
     assert L.kda_cache_compact(*a.values(), None) == status
 
 
+@pytest.mark.parametrize("kw, status", [
+    (dict(q=None), INVALID), (dict(o=P + 4), INVALID), (dict(lengths=None), INVALID), (dict(table=None), INVALID),
+    (dict(prefix=None), INVALID), (dict(prefix_len=P + 2), INVALID), (dict(cu=None), INVALID), (dict(prefix_pages=-1), INVALID),
+    (dict(groups=-1), INVALID), (dict(groups=3), INVALID), (dict(prefix_pages=1 << 26), UNSUPPORTED), (dict(dtype=3), INVALID),
+    (dict(scale=float("nan")), INVALID), (dict(hq=9), INVALID), (dict(d=136), UNSUPPORTED), (dict(qs=1028), INVALID),
+    (dict(B=65536), UNSUPPORTED), (dict(ws=None), WORKSPACE), (dict(ws_bytes=256), WORKSPACE), (dict(ws=P + 128), INVALID),
+    (dict(B=0, groups=0), OK), (dict(T_q=0), OK), (dict(lse=P + 1), INVALID),
+])
+def test_shared_refusals(L, kw, status):
+    a = dict(q=P, qs=1024, kc=P, vc=P, ksc=P, vsc=P, table=P, wide=8, lengths=P, prefix=P, prefix_pages=4, prefix_len=P, cu=P,
+             groups=2, o=P, lse=None, B=2, T_q=1, hq=8, hkv=2, d=128, pages=100, page=64, scale=1.0, dtype=1, ws=P,
+             ws_bytes=1 << 40)
+    a.update(kw)
+    assert L.kda_cache_attention_shared(*a.values(), None) == status
+
+
+def test_shared_workspace_size(L):
+    size = kda.cache_attention_shared_workspace_size
+    rows = 4 * 3 * 8
+    assert size(4, 3, 8, 2, 128, 64, 10, 5, 2) >= rows * (16 + 512)
+    assert size(4, 3, 8, 2, 128, 64, 10, 0, 2) == size(4, 3, 8, 2, 128, 64, 10, 5, 0) == kda.cache_attention_workspace_size(4, 3, 8, 2, 128, 64, 10)
+    assert size(4, 3, 8, 3, 128, 64, 10, 5, 2) == size(4, 3, 8, 2, 128, 64, 10, 5, 5) == size(0, 3, 8, 2, 128, 64, 10, 5, 0) == 0
+
+
 def test_workspace_size(L):
     assert kda.cache_pages_workspace_size(0) == 0
     assert kda.cache_pages_workspace_size(1) == 256
@@ -77,7 +101,7 @@ def test_workspace_size(L):
     assert kda.cache_pages_workspace_size(-1) == kda.cache_pages_workspace_size(1 << 31) == 0
 
 
-@pytest.mark.parametrize("name", ["cache_copy", "cache_resize", "cache_fork", "cache_compact"])
+@pytest.mark.parametrize("name", ["cache_copy", "cache_resize", "cache_fork", "cache_compact", "cache_attention_shared"])
 def test_odd_arguments_are_left_alone(L, name):
     entry, public = getattr(cache._binding(), name), getattr(kda, name)
     n = len(inspect.signature(public).parameters)
@@ -95,6 +119,7 @@ def test_public_calls_name_what_is_wrong(L):
     pool = kda.cache_new(2, 4, 16, 64, device="cpu")
     i = torch.zeros(1, dtype=torch.int32)
     for call in (lambda: kda.cache_copy(pool, i, i), lambda: kda.cache_resize(i, i[None], i, i, 16),
-                 lambda: kda.cache_fork(i, i[None], i, i, i, 16), lambda: kda.cache_compact(i, i[None])):
+                 lambda: kda.cache_fork(i, i[None], i, i, i, 16), lambda: kda.cache_compact(i, i[None]),
+                 lambda: kda.cache_attention_shared(torch.zeros(1, 1, 4, 64), pool, i[None], i, i[None], i, i)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
