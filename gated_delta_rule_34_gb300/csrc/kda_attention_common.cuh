@@ -414,6 +414,14 @@ cudaError_t run_attention_rows(const CacheAttention& a, bool bf16, void* workspa
 cudaError_t run_attention_rest_rows(const CacheAttention& a, bool bf16, void* workspace, cudaStream_t stream, int num_sms);
 cudaError_t run_attention_prefix_rows(const CacheAttention& a, bool bf16, void* workspace, cudaStream_t stream, int num_sms);
 
+// What kda_selftest_attention_stall has set on this thread.
+attn::Stall attention_stall();
+
+// The kernel for the prefixes of bf16 rows (kda_cache_prefix_tc.cu).
+bool attention_prefix_tc_takes(const CacheAttention& a, bool bf16);
+size_t attention_prefix_tc_workspace_bytes(const CacheAttention& a, int num_sms);
+cudaError_t run_attention_prefix_tc(const CacheAttention& a, void* workspace, cudaStream_t stream, int num_sms);
+
 // The kernel for many bf16 rows (kda_cache_attention_tc.cu): its plan for these queries, how many CTAs share
 // the work out (0: each item is one CTA's), and the launch.
 bool attention_tc_takes(const CacheAttention& a, bool bf16);

@@ -844,6 +844,7 @@ int64_t attention_tc_grid(const CacheAttention& a, const attn::Plan& plan, int n
 namespace {
 thread_local Stall stall;
 }
+attn::Stall attention_stall() { return stall; }
 
 namespace {
 template <Part P>

@@ -30,6 +30,7 @@ size_t cache_attention_shared_workspace_bytes(const CacheAttention& a, int num_s
     if (nothing_shared(a)) return cache_attention_workspace_bytes(a, num_sms);
     // the two passes' pieces follow one another in the same place
     size_t pieces = most(attention_prefix_rows_workspace_bytes(a, num_sms), attention_rest_rows_workspace_bytes(a, num_sms));
+    if (attention_prefix_tc_takes(a, true)) pieces = most(pieces, attention_prefix_tc_workspace_bytes(a, num_sms));
     if (attention_tc_takes(a, true)) {
         const attn::Plan plan = attention_tc_plan(a);
         pieces = most(pieces, attention_piece_bytes(attention_tc_grid(a, plan, num_sms), plan.stored, 128));
@@ -44,7 +45,8 @@ cudaError_t run_cache_attention_shared(CacheAttention a, bool bf16, void* worksp
     a.carry_stats = reinterpret_cast<float4*>(at);
     a.carry_sums = reinterpret_cast<float*>(at + up(rows_of(a) * sizeof(float4)));
     void* pieces = at + carry_bytes(a);
-    cudaError_t e = run_attention_prefix_rows(a, bf16, pieces, stream, num_sms);
+    cudaError_t e = attention_prefix_tc_takes(a, bf16) ? run_attention_prefix_tc(a, pieces, stream, num_sms)
+                                                       : run_attention_prefix_rows(a, bf16, pieces, stream, num_sms);
     if (e != cudaSuccess) return e;
     if (attention_tc_takes(a, bf16)) return run_attention_tc_rest(a, pieces, stream, num_sms);
     return run_attention_rest_rows(a, bf16, pieces, stream, num_sms);
