@@ -57,7 +57,9 @@ static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= kThreads * 128, "register
 constexpr int kItemCost = 4;               // what an item's start and end cost, in tiles of a stream
 constexpr int kLeastShare = 8;
 constexpr int kRun = 64;                   // tiles that O sums up
-constexpr float kBits = 8.0f, kFar = 7.0f; // log2 of the largest weight at its reference, and of how far above it
+// log2 of the largest weight at its reference; and what no 16 weights may sum up to, so that each is an fp16 number.
+constexpr float kBits = 7.0f, kMost = 60000.0f;
+constexpr float kNear = 4194304.0f;        // 2^22: below, scores have places behind the point
 constexpr int kBarBoth = 3;                // named barriers: 1 and 2 of a stream's threads, 3 of both
 
 // Shared memory, from a 1024-byte boundary.
@@ -69,9 +71,9 @@ constexpr int kValueTile = 2 * kTile;
 constexpr int kSmallAt = kValuesAt + kValueSlots * kValueTile;
 
 struct Scales {
-    float2 step[kSteps];                   // of keys; log2 of that of values
+    alignas(16) float2 step[kSteps];       // of keys; log2 of that of values
     uint32_t mask;                         // steps that exist, a bit each
-    uint32_t pad[3];
+    float lowest;                          // of their values' logarithms
 };
 struct Small {
     Scales scales[kScaleSlots];
@@ -146,6 +148,19 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
     return r;
 }
 
+__device__ __forceinline__ void store8(float* to, const float4& a, const float4& b) {
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "f"(a.x), "f"(a.y), "f"(a.z), "f"(a.w),
+                 "f"(b.x), "f"(b.y), "f"(b.z), "f"(b.w)
+                 : "memory");
+}
+// The two fp16 pairs of a word of four codes.
+__device__ __forceinline__ void word_to_half2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
 // Four values to e5m2 (nearest) and back: an e5m2 code is the upper byte of an fp16 number.
 __device__ __forceinline__ uint32_t to_e5m2x4(float a, float b, float c, float d) {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E5M2);
@@ -157,6 +172,13 @@ __device__ __forceinline__ void from_e5m2x4(uint32_t four, float* f) {
     const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
     const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
     f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+}
+
+// One lane of the warp, the same each time.
+__device__ __forceinline__ bool elected() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
 
 // tc::mbar_wait with a limit of the caller's, in microseconds.
@@ -392,7 +414,13 @@ struct Loader {
             const uint32_t mask = held & __ballot_sync(0xffffffffu, real);
             Scales* to = &c.small->scales[scale.slot];
             if (lane < kSteps) to->step[lane] = make_float2(real ? ks_now : 0.0f, real ? log_vs : 0.0f);
-            if (lane == 0) to->mask = mask;
+            float lowest = real && id_now >= 0 ? log_vs : INFINITY;
+#pragma unroll
+            for (int x = 1; x < kSteps; x <<= 1) lowest = fminf(lowest, __shfl_xor_sync(0xffffffffu, lowest, x));
+            if (lane == 0) {
+                to->mask = mask;
+                to->lowest = lowest;
+            }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&c.small->scale_full[scale.slot]);
             scale.next();
@@ -445,16 +473,18 @@ struct Converter {
             uint4 code[kSteps];
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) code[j] = *reinterpret_cast<const uint4*>(from + tc::sw128(j * kStep + row0, chunk));
+            if (mask != (1u << kSteps) - 1) {
+#pragma unroll
+                for (int j = 0; j < kSteps; ++j)
+                    if (!(mask >> j & 1)) code[j] = make_uint4(0, 0, 0, 0);
+            }
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) {
                 const int t = j * kStep + row0;
                 const uint32_t word[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
                 uint32_t half[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    half[2 * i] = mask >> j & 1 ? e4m3x2_to_half2(word[i] & 0xffffu) : 0u;
-                    half[2 * i + 1] = mask >> j & 1 ? e4m3x2_to_half2(word[i] >> 16) : 0u;
-                }
+                for (int i = 0; i < 4; ++i) word_to_half2x2(word[i], half[2 * i], half[2 * i + 1]);
                 // (the upper four threads of a token store their second piece first: no two meet in a bank)
                 const int c0 = 2 * (chunk & 3), late = chunk >> 2;
                 const uint4 first = late ? make_uint4(half[4], half[5], half[6], half[7]) : make_uint4(half[0], half[1], half[2], half[3]);
@@ -484,8 +514,19 @@ struct Issuer {
     int tiles = 0;
     bool dead = false;
 
+    // All lanes call everything, and agree; one of them issues.
     __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
-        if (!dead && !wait_up_to(bar, parity, c.plan.stall.wait_us)) dead = true;
+        if (!dead && !__all_sync(0xffffffffu, wait_up_to(bar, parity, c.plan.stall.wait_us))) dead = true;
+    }
+    // Products that follow one another without a loop's instructions between them: each takes 64 cycles, and one thread
+    // issues them all.
+    template <int CHUNKS>
+    static __device__ __forceinline__ void score_products(uint32_t d_tmem, uint64_t q, uint64_t keys) {
+#pragma unroll
+        for (int x = 0; x < CHUNKS; ++x) mma_f8(d_tmem, q + 2 * x, keys + 2 * x, idesc(128, kTokens, 1, false), x > 0);
+#pragma unroll
+        for (int x = 0; x < CHUNKS; ++x)
+            mma_f8(d_tmem, q + (kTile >> 4) + 2 * x, keys + 2 * x, idesc(128, kTokens, 0, false), true);
     }
     __device__ __forceinline__ void scores(int u, bool two) {
         const int stream = u & 1;
@@ -497,18 +538,20 @@ struct Issuer {
         if (u >= 2) wait(&c.small->o_done[stream], (s_phases >> stream & 1) ^ 1);
         if (dead) return;
         tc::tc_fence_after();
-        const int chunks = (c.a.d + 31) / 32;              // 32 channels a product
         const uint64_t keys = tc::desc_sw128(smem_u32(c.sm + kKeysAt + k.slot * kTile));
         const uint64_t q = tc::desc_sw128(smem_u32(c.sm + kQueriesAt + 2 * stream * kTile));
-        for (int x = 0; x < chunks; ++x)
-            mma_f8(c.tmem + 128 * stream, q + 2 * x, keys + 2 * x, idesc(128, kTokens, 1, false), x > 0);
-        for (int x = 0; x < chunks; ++x)
-            mma_f8(c.tmem + 128 * stream, q + (kTile >> 4) + 2 * x, keys + 2 * x, idesc(128, kTokens, 0, false), true);
-        tc::mma_commit(&c.small->s_full[stream]);
-        if (!two || stream == 1) {
-            tc::mma_commit(&c.small->k_empty[k.slot]);
-            k.next();
+        const uint32_t to = c.tmem + 128 * stream;
+        const bool last = !two || stream == 1;             // that reads the keys
+        const int chunks = (c.a.d + 31) / 32;              // 32 channels a product
+        if (elected()) {
+            if (chunks == 4) score_products<4>(to, q, keys);
+            else if (chunks == 3) score_products<3>(to, q, keys);
+            else if (chunks == 2) score_products<2>(to, q, keys);
+            else score_products<1>(to, q, keys);
+            tc::mma_commit(&c.small->s_full[stream]);
+            if (last) tc::mma_commit(&c.small->k_empty[k.slot]);
         }
+        if (last) k.next();
     }
     __device__ __forceinline__ void values(int u, bool two) {
         const int stream = u & 1, nth = u >> 1;            // nth of the stream's units
@@ -517,17 +560,18 @@ struct Issuer {
         if (dead) return;
         s_phases ^= 1u << stream;
         tc::tc_fence_after();
-        const uint32_t values = smem_u32(c.sm + kValuesAt + v.slot * kValueTile);
+        const uint64_t values = tc::desc_sw128_mn(smem_u32(c.sm + kValuesAt + v.slot * kValueTile), kTile, 1024);
+        const uint32_t from = c.tmem + 128 * stream, to = from + kTmemO, desc = idesc(128, c.a.d, 0, true);
+        const bool last = !two || stream == 1;             // that reads the values
+        if (elected()) {
+            mma_f16_ta(to, from, values, desc, nth % kRun != 0);
 #pragma unroll
-        for (int x = 0; x < kSteps; ++x)                   // 16 tokens a product
-            mma_f16_ta(c.tmem + kTmemO + 128 * stream, c.tmem + 128 * stream + 8 * x,
-                       tc::desc_sw128_mn(values + x * kStep * 128, kTile, 1024), idesc(128, c.a.d, 0, true),
-                       nth % kRun != 0 || x > 0);
-        tc::mma_commit(&c.small->o_done[stream]);
-        if (!two || stream == 1) {
-            tc::mma_commit(&c.small->v_empty[v.slot]);
-            v.next();
+            for (int x = 1; x < kSteps; ++x)               // 16 tokens a product
+                mma_f16_ta(to, from + 8 * x, values + x * (kStep * 128 >> 4), desc, true);
+            tc::mma_commit(&c.small->o_done[stream]);
+            if (last) tc::mma_commit(&c.small->v_empty[v.slot]);
         }
+        if (last) v.next();
     }
     __device__ __forceinline__ void piece(const PrefixPiece& p) {
         const int units = (p.to - p.from) * (p.two ? 2 : 1);
@@ -542,7 +586,7 @@ struct Issuer {
     }
     // Every product issued has ended, whether or not a wait gave up before, so that TMEM may go.
     __device__ __forceinline__ void finish() {
-        tc::mma_commit(&c.small->drained);
+        if (elected()) tc::mma_commit(&c.small->drained);
         tc::mbar_wait(&c.small->drained, 0);
     }
 };
@@ -566,17 +610,23 @@ struct Softmax {
         const int64_t first = (int64_t)p.rows256 * kPair + (p.two ? stream * kRows : 0);
         const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
         uint8_t* to = c.sm + kQueriesAt + 2 * stream * kTile;
-#pragma unroll 2
-        for (int r = tid >> 3; r < kRows; r += kWarpgroup / 8) {
-            const int64_t at = first + r;
+        constexpr int kTurns = kRows * 8 / kWarpgroup;
+        uint4 all[kTurns][2];                              // all loads before the first is used
+#pragma unroll
+        for (int n = 0; n < kTurns; ++n) {
+            const int64_t at = first + n * (kWarpgroup / 8) + (tid >> 3);
             const bool real = at < w.rows;
             const int64_t i = real ? at / c.plan.group : 0;
             const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + ((int64_t)w.range.x * a.T_q + i) * a.q_stride +
                                      (int64_t)(p.hk * c.plan.group + (real ? (int)(at - i * c.plan.group) : 0)) * a.d + 16 * part;
-            uint4 raw[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-                raw[x] = real && 16 * part < a.d ? reinterpret_cast<const uint4*>(q)[x] : make_uint4(0, 0, 0, 0);
+                all[n][x] = real && 16 * part < a.d ? reinterpret_cast<const uint4*>(q)[x] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int n = 0; n < kTurns; ++n) {
+            const int r = n * (kWarpgroup / 8) + (tid >> 3);
+            const uint4* raw = all[n];
             const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(raw);
             float amax = 0.0f;
             bool number = true;
@@ -643,8 +693,108 @@ struct Softmax {
             }
         }
     }
-    static __device__ __noinline__ void scale_sums(uint32_t at, int d, float keep) {
-        for (int ch = 0; ch < d; ch += 16) {
+    // The references move to the largest of the scores from chunk h (32 tokens) on: (m, dr, log2 of what that multiplies the
+    // sums by, whether there was any).  The sums in TMEM (where there are any) and the weights of the chunks before
+    // are multiplied in place.  All is taken from differences of rounded products, so that scores whose last places are
+    // whole numbers still give the largest one's value.
+    static __device__ __noinline__ float4 move_references(uint32_t s_at, uint32_t o_at, const Scales* sc, float factor, float m,
+                                                          float dr, bool seen, int h0, int d) {
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int j = 2 * h0; j < kSteps; ++j) {
+            float s[16];
+            tc::tmem_ld16(s_at + 16 * j, s);
+            loaded16(s);
+            float most = s[0];
+#pragma unroll
+            for (int x = 1; x < 16; ++x) most = fmaxf(most, s[x]);
+            if (sc->mask >> j & 1) top = fmaxf(top, __fmul_rn(most, factor * sc->step[j].x));
+        }
+        const bool found = top > -INFINITY;
+        const float m_new = !found ? m : seen ? fmaxf(m, ceilf(top)) : ceilf(top);
+        float reach = -INFINITY;
+#pragma unroll 1
+        for (int j = 2 * h0; j < kSteps; ++j) {
+            float s[16];
+            tc::tmem_ld16(s_at + 16 * j, s);
+            loaded16(s);
+            float most = s[0];
+#pragma unroll
+            for (int x = 1; x < 16; ++x) most = fmaxf(most, s[x]);
+            const float2 st = sc->step[j];
+            if (sc->mask >> j & 1) reach = fmaxf(reach, __fsub_rn(__fmul_rn(most, factor * st.x), m_new) + st.y);
+        }
+        const float dr_old = dr + (seen ? m - m_new : 0.0f);
+        const bool moves = found && (!seen || reach > dr_old);
+        const float dr_new = moves ? ceilf(reach) : dr_old;
+        const float move = seen && moves ? dr_old - dr_new : 0.0f;
+        if (__any_sync(0xffffffffu, move != 0.0f)) {
+            const float keep = ex2(move);
+            tc::tmem_wait_st();                            // the weights stored so far
+            if (d > 0) scale_sums(o_at, d, keep);
+#pragma unroll 1
+            for (int h = 0; h < h0; ++h) {
+                float two[16];
+                uint32_t out[16];
+                tc::tmem_ld16(s_at + 16 * h, two);
+                loaded16(two);
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const uint32_t bits = __float_as_uint(two[x]);
+                    const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&bits));
+                    out[x] = half2_bits(w.x * keep, w.y * keep);
+                }
+                tc::tmem_st16(s_at + 16 * h, out);
+            }
+            tc::tmem_wait_st();
+        }
+        return make_float4(m_new, dr_new, move, found ? 1.0f : 0.0f);
+    }
+    // Weights from chunk h on where steps are missing, scores are beyond 2^22, or pages of values so small beside others that
+    // their weights are lost: the sum of weights by itself, which it returns.
+    static __device__ __noinline__ float far_weights(uint32_t at, const Scales* sc, float factor, float m, float dr, int h0) {
+        float l = 0.0f;
+#pragma unroll 1
+        for (int h = h0; h < 4; ++h) {
+            uint32_t out[16];
+            float s[32];
+            load32(at + 32 * h, s);
+            loaded16(s);
+            loaded16(s + 16);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float2 st = sc->step[2 * h + j];
+                const bool real = sc->mask >> (2 * h + j) & 1;
+                const float f = factor * st.x, lift = st.y - dr + kBits;
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const float z0 = __fsub_rn(__fmul_rn(s[16 * j + 2 * x], f), m);
+                    const float z1 = __fsub_rn(__fmul_rn(s[16 * j + 2 * x + 1], f), m);
+                    if (real) l += ex2(z0) + ex2(z1);
+                    out[8 * j + x] = real ? half2_bits(ex2(z0 + lift), ex2(z1 + lift)) : 0u;
+                }
+            }
+            tc::tmem_st16(at + 16 * h, out);
+        }
+        return l;
+    }
+    static __device__ __forceinline__ void scale_sums(uint32_t at, int d, float keep) {
+        int ch = 0;
+#pragma unroll 1
+        for (; ch + 32 <= d; ch += 32) {
+            float o[32];
+            load32(at + ch, o);
+            loaded16(o);
+            loaded16(o + 16);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                uint32_t out[16];
+#pragma unroll
+                for (int y = 0; y < 16; ++y) out[y] = __float_as_uint(o[16 * x + y] * keep);
+                tc::tmem_st16(at + ch + 16 * x, out);
+            }
+        }
+        if (ch < d) {
             float o[16];
             uint32_t out[16];
             tc::tmem_ld16(at + ch, o);
@@ -653,7 +803,6 @@ struct Softmax {
             for (int x = 0; x < 16; ++x) out[x] = __float_as_uint(o[x] * keep);
             tc::tmem_st16(at + ch, out);
         }
-        tc::tmem_wait_st();
     }
 
     __device__ __forceinline__ void piece(const PrefixPiece& p, const GroupWork& w) {
@@ -678,105 +827,71 @@ struct Softmax {
             wait(&c.small->s_full[stream], s_phase);
             tc::tc_fence_after();
             const Scales* sc = &c.small->scales[scale.slot];
-            const uint32_t mask = sc->mask;
-            // Scores are loaded twice, 32 tokens at a time: for the largest, then for the weights (128 registers of them all
-            // do not fit, and a load costs less than their way to memory and back).
-            float top = -INFINITY, xs[kSteps], lowest = INFINITY;
-            {
-                float s[2][32];
-                load32(s_at, s[0]);
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    float* now = s[h & 1];
-                    loaded16(now);
-                    loaded16(now + 16);
-                    if (h < 3) load32(s_at + 32 * (h + 1), s[(h + 1) & 1]);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        float most = now[16 * j];
-#pragma unroll
-                        for (int x = 1; x < 16; ++x) most = fmaxf(most, now[16 * j + x]);
-                        const float2 st = sc->step[2 * h + j];
-                        const bool real = mask >> (2 * h + j) & 1;
-                        xs[2 * h + j] = real ? most * (factor * st.x) : -INFINITY;
-                        if (real) lowest = fminf(lowest, st.y);
-                        top = fmaxf(top, xs[2 * h + j]);
-                    }
-                }
-            }
-            // The new m, and how far the largest weighted value is from it.
-            const bool found = top > -INFINITY;
-            const float m_new = !found ? m : seen ? fmaxf(m, ceilf(top)) : ceilf(top);
-            const float up = seen ? m - m_new : 0.0f;
-            float reach = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < kSteps; ++j) reach = fmaxf(reach, xs[j] - m_new + sc->step[j].y);
-            const float dr_old = dr + up;
-            const bool moves = found && (!seen || reach > dr_old + kFar);
-            const float dr_new = moves ? ceilf(reach) : dr_old;
-            const float move = seen && moves ? dr_old - dr_new : 0.0f;
-            if (k > 0 && k % kRun == 0) {
+            const bool fresh = k % kRun == 0;              // no sums in O
+            if (fresh && k > 0) {
                 wait(&c.small->o_done[stream], s_phase ^ 1);
                 tc::tc_fence_after();
                 if (!bad) add_run(o_at, run_at(row), a.d, k == kRun, shift);
                 shift = 0.0f;
-            } else if (__any_sync(0xffffffffu, move != 0.0f) && k > 0) {
-                wait(&c.small->o_done[stream], s_phase ^ 1);
+            }
+            const float lowest = sc->lowest;
+            auto near = [&]() { return fabsf(m) < kNear && dr - lowest < 90.0f; };
+            auto move = [&](int h) {
+                if (!fresh) wait(&c.small->o_done[stream], s_phase ^ 1);
                 tc::tc_fence_after();
-                if (!bad) scale_sums(o_at, a.d, ex2(move));
-            }
-            shift += move;
-            l *= ex2(up);
-            m = m_new;
-            dr = dr_new;
-            seen |= found;
-
-            // Weights, 32 tokens (16 registers) at a time: over the scores of 16 tokens that have been loaded.
-            const bool plain = __all_sync(0xffffffffu, fabsf(m) < 4194304.0f && dr - lowest < 90.0f);
-            float s[2][32];
-            load32(s_at, s[0]);
+                const float4 to = move_references(s_at, o_at, sc, factor, m, dr, seen, h, fresh || bad ? 0 : a.d);
+                l *= seen ? ex2(m - to.x) : 1.0f;
+                m = to.x;
+                dr = to.y;
+                shift += to.z;
+                seen |= to.w != 0.0f;
+            };
+            // One pass, 32 tokens at a time, under the references so far.  Sums of 16 weights, which the sum of all needs anyway, tell
+            // where a weight would be too large: then the references move first.
+            int h = 0;
+            if (sc->mask == (1u << kSteps) - 1 && __all_sync(0xffffffffu, seen && near())) {
+                bool moved = false;
+#pragma unroll 1
+                for (; h < 4; ++h) {
+                    float now[32];
+                    load32(s_at + 32 * h, now);
+                    const float4 st = *reinterpret_cast<const float4*>(&sc->step[2 * h]);
+                    const float f[2] = {factor * st.x, factor * st.z}, lv[2] = {st.y, st.w};
+                    uint32_t out[16];
+                    float sum[2];
+                    loaded16(now);
+                    loaded16(now + 16);
+#pragma unroll 1
+                    for (;;) {
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                float* now = s[h & 1];
-                loaded16(now);
-                loaded16(now + 16);
-                if (h < 3) load32(s_at + 32 * (h + 1), s[(h + 1) & 1]);
-                uint32_t out[16];
+                        for (int j = 0; j < 2; ++j) {
+                            const float less = (lv[j] - dr + kBits) - m;
+                            const uint64_t ff = f2_pack(f[j], f[j]), cc = f2_pack(less, less);
+                            uint64_t both = 0;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float2 st = sc->step[2 * h + j];
-                    const bool real = mask >> (2 * h + j) & 1;
-                    if (!real) {
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) out[8 * j + x] = 0;
-                    } else if (plain) {
-                        const float f = factor * st.x, less = (st.y - dr + kBits) - m;
-                        const uint64_t ff = f2_pack(f, f), cc = f2_pack(less, less);
-                        uint64_t sum = 0;
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) {
-                            const float2 e = f2_unpack(f2_fma(f2_pack(now[16 * j + 2 * x], now[16 * j + 2 * x + 1]), ff, cc));
-                            const float w0 = ex2(e.x), w1 = ex2(e.y);
-                            sum = x == 0 ? f2_pack(w0, w1) : add_pair(sum, f2_pack(w0, w1));
-                            out[8 * j + x] = half2_bits(w0, w1);
+                            for (int x = 0; x < 8; ++x) {
+                                const float2 e = f2_unpack(f2_fma(f2_pack(now[16 * j + 2 * x], now[16 * j + 2 * x + 1]), ff, cc));
+                                const float w0 = ex2(e.x), w1 = ex2(e.y);
+                                both = x == 0 ? f2_pack(w0, w1) : add_pair(both, f2_pack(w0, w1));
+                                out[8 * j + x] = half2_bits(w0, w1);
+                            }
+                            const float2 two = f2_unpack(both);
+                            sum[j] = two.x + two.y;
                         }
-                        const float2 both = f2_unpack(sum);
-                        l = fmaf(both.x + both.y, ex2(dr - kBits - st.y), l);
-                    } else {
-                        // Scores whose last places are whole numbers: differences of rounded products; and pages of values so
-                        // small beside others that their weights are lost: the sum of weights by itself.
-                        const float f = factor * st.x, lift = st.y - dr + kBits;
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) {
-                            const float z0 = __fsub_rn(__fmul_rn(now[16 * j + 2 * x], f), m);
-                            const float z1 = __fsub_rn(__fmul_rn(now[16 * j + 2 * x + 1], f), m);
-                            l += ex2(z0) + ex2(z1);
-                            out[8 * j + x] = half2_bits(ex2(z0 + lift), ex2(z1 + lift));
-                        }
+                        if (moved || !__any_sync(0xffffffffu, fmaxf(sum[0], sum[1]) > kMost)) break;
+                        move(h);
+                        moved = true;
+                        if (!__all_sync(0xffffffffu, near())) break;
                     }
+                    if (moved && !__all_sync(0xffffffffu, near())) break;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) l = fmaf(sum[j], ex2(dr - kBits - lv[j]), l);
+                    tc::tmem_st16(s_at + 16 * h, out);
                 }
-                tc::tmem_st16(s_at + 16 * h, out);
+            } else {
+                move(0);
             }
+            if (h < 4) l += far_weights(s_at, sc, factor, m, dr, h);
             tc::tmem_wait_st();
             tc::tc_fence_before();
             tc::mbar_arrive(&c.small->p_full[stream]);
@@ -843,12 +958,17 @@ struct Softmax {
         for (int ch = 0; ch < c.a.d; ch += 16) {
             float o[16];
             sums(ch, o);                                   // (by whole warps: from TMEM)
+            float4 v[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                float4 v = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                v[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
                 float m = M, dm = DM, l = L;
-                if (other) join_sums(v, m, dm, l, stat, other[(ch / 4 + x) * kRows]);
-                if (real) *reinterpret_cast<float4*>(to + ch + 4 * x) = v;
+                if (other) join_sums(v[x], m, dm, l, stat, other[(ch / 4 + x) * kRows]);
+            }
+            // (a thread has a row: whole sectors of 32 bytes at a time)
+            if (real) {
+                store8(to + ch, v[0], v[1]);
+                store8(to + ch + 8, v[2], v[3]);
             }
         }
         if (other) {
@@ -914,7 +1034,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!role.dead) role.piece(p, w);
             });
             role.finish();
-        } else if (threadIdx.x == 32 * kIssuerWarp) {
+        } else if (warp == kIssuerWarp) {
             Issuer role{cta};
             for_each_prefix_piece(a, plan, share, [&](const PrefixPiece& p, const GroupWork&) {
                 if (!role.dead) role.piece(p);
