@@ -12,13 +12,14 @@
 // What bounds it: 4 d operations a row and token on the tensor cores (q in two fp8 pieces costs what one bf16 product
 // does), with the exponentials and conversions beside them; under 128 rows, reading the codes.
 //
-// One CTA an SM takes items (group, head of keys, 256 rows): two streams of 128 rows, each with a softmax warpgroup whose
-// threads own a row (no shuffles), so that one stream's products run under the other's softmax. Keys and values are loaded and
+// One CTA an SM takes items (group, head of keys, 256 rows): two streams of 128 rows, each with softmax threads
+// that own a row (no shuffles), so that one stream's products run under the other's softmax. Keys and values are loaded and
 // converted once for both. Where 128 rows or fewer are left, both streams take them, the tiles of tokens in turn. Roles:
-//   8 softmax    scores from TMEM, weights back into the same columns
+//   16 softmax   scores from TMEM, weights back into the same columns: eight warps a stream, half of a tile's tokens each
 //   4 converters values from e4m3 to fp16
 //   1 issuer     S of a stream's next tile after the O of its last one: S and W share their columns
 //   1 loader     pages by TMA, 128-byte-swizzled rows, a box a page (of up to 128 tokens); their scales
+//   1 planner    the CTA's pieces, told to the others through shared memory
 // A row's reference moves when a score passes it by more than a factor of 128; it is a whole number, so that weights,
 // moves and the sum of weights l, which is taken from the same weights step by step, have no rounding of their own.
 //
@@ -49,18 +50,21 @@ constexpr int kTile = kTokens * 128;       // bytes of a tile's keys, or values
 constexpr int kKeySlots = 3, kRawSlots = 2, kValueSlots = 2;
 constexpr int kScaleSlots = 8;             // more than tiles that softmax may be behind the loader
 constexpr int kWarpgroup = 128;
-constexpr int kThreads = 512;
-constexpr int kConverterWarp = 8, kIssuerWarp = 12, kLoaderWarp = 13;
-// 128 registers a thread at launch: 256 x 168 + 256 x 88 = 512 x 128.
-constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
-static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= kThreads * 128, "registers at launch");
+constexpr int kStream = 256;               // softmax threads of a stream
+constexpr int kThreads = 768;
+constexpr int kConverterWarp = 16, kIssuerWarp = 20, kLoaderWarp = 21, kPlannerWarp = 22;
+constexpr int kPieceSlots = 4;
+constexpr int kPatience = 8;               // waits' limits that roles wait for one another's pieces
+// 80 registers a thread at launch: 512 x 96 + 256 x 48 = 768 x 80.
+constexpr int kSoftmaxRegs = 96, kOtherRegs = 48;
+static_assert(2 * kStream * kSoftmaxRegs + (kThreads - 2 * kStream) * kOtherRegs <= kThreads * 80, "registers at launch");
 constexpr int kItemCost = 4;               // what an item's start and end cost, in tiles of a stream
 constexpr int kLeastShare = 8;
 constexpr int kRun = 64;                   // tiles that O sums up
-// log2 of the largest weight at its reference; and what no 16 weights may sum up to, so that each is an fp16 number.
-constexpr float kBits = 7.0f, kMost = 60000.0f;
+constexpr float kBits = 7.0f, kFar = 8.0f; // log2 of the largest weight at its reference, and of how far above it
 constexpr float kNear = 4194304.0f;        // 2^22: below, scores have places behind the point
-constexpr int kBarBoth = 3;                // named barriers: 1 and 2 of a stream's threads, 3 of both
+// Named barriers: 1 to 8 of the two warps that have the same rows, 9 and 10 of a stream's, 11 of both streams'.
+constexpr int kBarRows = 1, kBarStream = 9, kBarBoth = 11;
 
 // Shared memory, from a 1024-byte boundary.
 constexpr int kQueriesAt = 0;                                      // [2 streams][2 pieces][128 rows][128 channels]
@@ -70,17 +74,32 @@ constexpr int kValuesAt = kRawAt + kRawSlots * kTile;              // [2 halves 
 constexpr int kValueTile = 2 * kTile;
 constexpr int kSmallAt = kValuesAt + kValueSlots * kValueTile;
 
+// What a CTA does next: a piece of an item. The planner writes these, so that the other roles' registers are free of the
+// walk through the list.
+struct PrefixPiece {
+    int g, hk;
+    int rows256;                           // which 256 rows of the group's
+    int two;                               // two streams of 128 rows, or one of 128 or fewer that both take
+    int from, to;                          // tiles; none: the end
+    int slot, whole;
+    int first_seq;                         // of the group,
+    int tokens;                            // its prefix,
+    int64_t rows;                          // and all its rows
+};
 struct Scales {
     alignas(16) float2 step[kSteps];       // of keys; log2 of that of values
     uint32_t mask;                         // steps that exist, a bit each
     float lowest;                          // of their values' logarithms
 };
 struct Small {
+    PrefixPiece piece[kPieceSlots];
     Scales scales[kScaleSlots];
     float factor[kPair];                   // of the scores, to powers of two
     float4 stat[kRows];                    // of the second stream's sums, where both have the same rows
+    float top[2][2][kRows], reach[2][2][kRows];   // what the halves of a stream tell each other
     uint64_t k_full[kKeySlots], k_empty[kKeySlots], raw_full[kRawSlots], raw_empty[kRawSlots], v_full[kValueSlots],
-        v_empty[kValueSlots], scale_full[kScaleSlots], s_full[2], p_full[2], o_done[2], q_full[2], drained;
+        v_empty[kValueSlots], scale_full[kScaleSlots], s_full[2], p_full[2], o_done[2], q_full[2], piece_full[kPieceSlots],
+        piece_empty[kPieceSlots], drained;
     uint32_t tmem;
 };
 constexpr int kSmem = kSmallAt + (int)sizeof(Small) + 1024;
@@ -148,9 +167,9 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
     return r;
 }
 
-__device__ __forceinline__ void store8(float* to, const float4& a, const float4& b) {
-    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "f"(a.x), "f"(a.y), "f"(a.z), "f"(a.w),
-                 "f"(b.x), "f"(b.y), "f"(b.z), "f"(b.w)
+__device__ __forceinline__ void store8(float* to, const float* v) {
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+                 "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                  : "memory");
 }
 // The two fp16 pairs of a word of four codes.
@@ -181,13 +200,18 @@ __device__ __forceinline__ bool elected() {
     return r != 0;
 }
 
-// tc::mbar_wait with a limit of the caller's, in microseconds.
+// tc::mbar_wait with a limit of the caller's, in microseconds, counted in cycles of 2 GHz.  (The global timer, which that one
+// reads before it polls, takes longer than most waits here.)
 __device__ __forceinline__ bool wait_up_to(uint64_t* bar, uint32_t parity, int limit) {
     if (tc::mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = tc::global_ns();
-    for (uint32_t i = 0; i < (1u << 30); ++i) {
+    long long t0 = 0;
+    for (uint32_t i = 1; i < (1u << 30); ++i) {
         if (tc::mbar_try_wait(bar, parity)) return true;
-        if ((i & 15u) == 15u && tc::global_ns() - t0 > 1000ull * limit) break;
+        if ((i & 63u) == 0) {
+            const long long now = clock64();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > 2000ll * limit) break;
+        }
     }
     return false;
 }
@@ -223,63 +247,44 @@ struct PrefixShare {
     int g;                                 // -1: nothing
 };
 
+// One warp calls it; its lanes sum up some groups' spans each.
 __device__ __forceinline__ PrefixShare find_prefix_share(const CacheAttention& a, const PrefixPlan& plan) {
-    __shared__ int64_t warp_sum_s[kThreads / 32];
-    __shared__ int64_t found_base;
-    __shared__ int found;
-    const int each = (a.n_groups + kThreads - 1) / kThreads;
-    const int g0 = threadIdx.x * each;
+    const int lane = threadIdx.x & 31;
+    const int each = (a.n_groups + 31) / 32, g0 = lane * each;
     int64_t mine = 0;
     for (int g = g0; g < g0 + each && g < a.n_groups; ++g) mine += group_work(a, plan, g).span * a.H_kv;
-    int64_t before = mine;
+    int64_t up = mine;
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, before, w);
-        if ((threadIdx.x & 31) >= w) before += x;
+        const int64_t x = __shfl_up_sync(0xffffffffu, up, w);
+        if (lane >= w) up += x;
     }
-    if ((threadIdx.x & 31) == 31) warp_sum_s[threadIdx.x >> 5] = before;
-    if (threadIdx.x == 0) found = -1;
-    __syncthreads();
-    int64_t total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < (int)(threadIdx.x >> 5)) before += warp_sum_s[w];
-        total += warp_sum_s[w];
-    }
-    before -= mine;
+    const int64_t total = __shfl_sync(0xffffffffu, up, 31);
     PrefixShare s;
     s.share = (total + gridDim.x - 1) / gridDim.x;
     if (s.share < kLeastShare) s.share = kLeastShare;
     s.begin = s.share * blockIdx.x;
     s.end = s.begin + s.share < total ? s.begin + s.share : total;
-    if (s.begin >= before && s.begin < before + mine) {
-        int64_t base = before;
+    int found = -1;
+    int64_t base = up - mine;
+    if (s.begin >= base && s.begin < up) {
         for (int g = g0; g < a.n_groups; ++g) {
             const int64_t w = group_work(a, plan, g).span * a.H_kv;
             if (s.begin < base + w) {
                 found = g;
-                found_base = base;
                 break;
             }
             base += w;
         }
     }
-    __syncthreads();
-    s.g = found;
-    s.base = found_base;
+    const uint32_t who = __ballot_sync(0xffffffffu, found >= 0);
+    const int from = who ? __ffs(who) - 1 : 0;
+    s.g = __shfl_sync(0xffffffffu, found, from);
+    s.base = __shfl_sync(0xffffffffu, base, from);
     return s;
 }
 
-struct PrefixPiece {
-    int g, hk;
-    int rows256;                           // which 256 rows of the group's
-    bool two;                              // two streams of 128 rows, or one of 128 or fewer that both take
-    int from, to;                          // tiles
-    int slot;
-    bool whole;
-};
-
-// Calls f(piece, work of its group) for each piece of the share; returns the entry of `joins` for the item that begins here
+// Calls f(piece) for each piece of the share; returns the entry of `joins` for the item that begins here
 // and ends in a later share.
 template <typename F>
 __device__ __forceinline__ int4 for_each_prefix_piece(const CacheAttention& a, const PrefixPlan& plan, const PrefixShare& s,
@@ -308,7 +313,10 @@ __device__ __forceinline__ int4 for_each_prefix_piece(const CacheAttention& a, c
         if (p.from < p.to) {
             p.whole = p.from == 0 && p.to == w.tiles;
             p.slot = at == s.begin ? 0 : 1;
-            f(p, w);
+            p.first_seq = w.range.x;
+            p.tokens = w.tokens;
+            p.rows = w.rows;
+            f(p);
             if (!p.whole && p.from == 0) join = make_int4(p.g, p.hk, (int)((item_end - 1) / s.share), 2 * p.rows256 + p.slot);
         }
         at = stop;
@@ -317,10 +325,10 @@ __device__ __forceinline__ int4 for_each_prefix_piece(const CacheAttention& a, c
 }
 
 // Row r of a group's rows, as a row of o.
-__device__ __forceinline__ int64_t prefix_row(const CacheAttention& a, const PrefixPlan& plan, const GroupWork& w, int hk,
+__device__ __forceinline__ int64_t prefix_row(const CacheAttention& a, const PrefixPlan& plan, int first_seq, int hk,
                                               int64_t r) {
     const int64_t i = r / plan.group;
-    return ((int64_t)w.range.x * a.T_q + i) * a.H_q + hk * plan.group + (int)(r - i * plan.group);
+    return ((int64_t)first_seq * a.T_q + i) * a.H_q + hk * plan.group + (int)(r - i * plan.group);
 }
 
 struct Cta {
@@ -346,6 +354,20 @@ struct Ring {
     }
 };
 
+// Calls f for each piece that the planner writes; whole warps.
+template <typename F>
+__device__ __forceinline__ void for_each_piece_told(const Cta& c, F f) {
+    Ring<kPieceSlots> ring;
+    for (;;) {
+        if (!__all_sync(0xffffffffu, wait_up_to(&c.small->piece_full[ring.slot], ring.phase, kPatience * c.plan.stall.wait_us))) return;
+        const PrefixPiece& p = c.small->piece[ring.slot];
+        if (p.from >= p.to) return;
+        f(p);
+        tc::mbar_arrive(&c.small->piece_empty[ring.slot]);
+        ring.next();
+    }
+}
+
 // ------------------------------------------------------------------ loader
 struct Loader {
     Cta c;
@@ -362,10 +384,11 @@ struct Loader {
         if (!__all_sync(0xffffffffu, wait_up_to(bar, parity, c.plan.stall.wait_us))) dead = true;
     }
 
-    __device__ __forceinline__ void piece(const PrefixPiece& p, const GroupWork& w) {
+    __device__ __forceinline__ void piece(const PrefixPiece& told) {
         const CacheAttention& a = c.a;
         const int lane = threadIdx.x & 31;
-        const int32_t* table = a.prefix_table + (int64_t)p.g * a.prefix_pages;
+        const struct { int hk, from, to, tokens; } p{told.hk, told.from, told.to, told.tokens};
+        const int32_t* table = a.prefix_table + (int64_t)told.g * a.prefix_pages;
         const int page_mask = (1 << a.page_shift) - 1;
         const int box = a.page_shift >= 7 ? kSteps : 1 << (a.page_shift - 4);   // steps that one copy brings
         const bool leads = lane < kSteps && (lane & (box - 1)) == 0;
@@ -373,7 +396,7 @@ struct Loader {
         // Lane k < 8: step k of a tile.
         auto page_of = [&](int tile) -> int {
             const int t = (tile * kSteps + lane) * kStep;
-            const int id = lane < kSteps && tile < p.to && t < w.tokens ? table[t >> a.page_shift] : -1;
+            const int id = lane < kSteps && tile < p.to && t < p.tokens ? table[t >> a.page_shift] : -1;
             return id >= 0 && id < a.n_pages ? id : -1;
         };
         auto scales_of = [&](int id, float& ks, float& vs) {
@@ -462,7 +485,7 @@ struct Converter {
     __device__ __forceinline__ void piece(const PrefixPiece& p) {
         const int tid = threadIdx.x - kConverterWarp * 32;
         const int row0 = tid >> 3, chunk = tid & 7;        // eight threads a token, 16 channels each
-        for (int tile = p.from; tile < p.to; ++tile, ++n) {
+        for (int left = p.to - p.from; left > 0; --left, ++n) {
             wait(&c.small->scale_full[scale.slot], scale.phase);
             wait(&c.small->raw_full[raw.slot], raw.phase);
             if (n >= kValueSlots) wait(&c.small->v_empty[v.slot], v.phase ^ 1);
@@ -470,18 +493,12 @@ struct Converter {
             const uint32_t mask = c.small->scales[scale.slot].mask;
             const uint8_t* from = c.sm + kRawAt + raw.slot * kTile;
             uint8_t* to = c.sm + kValuesAt + v.slot * kValueTile + (chunk >> 2) * kTile;
-            uint4 code[kSteps];
-#pragma unroll
-            for (int j = 0; j < kSteps; ++j) code[j] = *reinterpret_cast<const uint4*>(from + tc::sw128(j * kStep + row0, chunk));
-            if (mask != (1u << kSteps) - 1) {
-#pragma unroll
-                for (int j = 0; j < kSteps; ++j)
-                    if (!(mask >> j & 1)) code[j] = make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
+#pragma unroll 2
             for (int j = 0; j < kSteps; ++j) {
                 const int t = j * kStep + row0;
-                const uint32_t word[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
+                uint4 code = *reinterpret_cast<const uint4*>(from + tc::sw128(t, chunk));
+                if (!(mask >> j & 1)) code = make_uint4(0, 0, 0, 0);
+                const uint32_t word[4] = {code.x, code.y, code.z, code.w};
                 uint32_t half[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) word_to_half2x2(word[i], half[2 * i], half[2 * i + 1]);
@@ -528,12 +545,14 @@ struct Issuer {
         for (int x = 0; x < CHUNKS; ++x)
             mma_f8(d_tmem, q + (kTile >> 4) + 2 * x, keys + 2 * x, idesc(128, kTokens, 0, false), true);
     }
+    // Keys of unit u's tile, where it is the first to read them: waited for before what it has to wait for at last.
+    __device__ __forceinline__ void keys_of(int u, bool two) {
+        if (two && (u & 1)) return;
+        if (++tiles > c.plan.stall.tiles) dead = true;
+        wait(&c.small->k_full[k.slot], k.phase);
+    }
     __device__ __forceinline__ void scores(int u, bool two) {
         const int stream = u & 1;
-        if (!two || stream == 0) {
-            if (++tiles > c.plan.stall.tiles) dead = true;
-            wait(&c.small->k_full[k.slot], k.phase);
-        }
         // the stream's last products have read the weights that lie where the scores go
         if (u >= 2) wait(&c.small->o_done[stream], (s_phases >> stream & 1) ^ 1);
         if (dead) return;
@@ -555,8 +574,8 @@ struct Issuer {
     }
     __device__ __forceinline__ void values(int u, bool two) {
         const int stream = u & 1, nth = u >> 1;            // nth of the stream's units
-        wait(&c.small->p_full[stream], s_phases >> stream & 1);
         if (!two || stream == 0) wait(&c.small->v_full[v.slot], v.phase);
+        wait(&c.small->p_full[stream], s_phases >> stream & 1);
         if (dead) return;
         s_phases ^= 1u << stream;
         tc::tc_fence_after();
@@ -567,21 +586,27 @@ struct Issuer {
             mma_f16_ta(to, from, values, desc, nth % kRun != 0);
 #pragma unroll
             for (int x = 1; x < kSteps; ++x)               // 16 tokens a product
-                mma_f16_ta(to, from + 8 * x, values + x * (kStep * 128 >> 4), desc, true);
+                mma_f16_ta(to, from + 8 * x + (x >= kSteps / 2 ? 32 : 0), values + x * (kStep * 128 >> 4), desc, true);
             tc::mma_commit(&c.small->o_done[stream]);
             if (last) tc::mma_commit(&c.small->v_empty[v.slot]);
         }
         if (last) v.next();
     }
     __device__ __forceinline__ void piece(const PrefixPiece& p) {
-        const int units = (p.to - p.from) * (p.two ? 2 : 1);
+        const bool two = p.two;
+        const int units = (p.to - p.from) * (two ? 2 : 1);
         wait(&c.small->q_full[0], q_phase);
         wait(&c.small->q_full[1], q_phase);
         q_phase ^= 1;
-        for (int u = 0; u < 2 && u < units && !dead; ++u) scores(u, p.two);
+        for (int u = 0; u < 2 && u < units && !dead; ++u) {
+            keys_of(u, two);
+            scores(u, two);
+        }
         for (int u = 0; u < units && !dead; ++u) {
-            values(u, p.two);
-            if (u + 2 < units && !dead) scores(u + 2, p.two);
+            const bool more = u + 2 < units;
+            if (more) keys_of(u + 2, two);
+            values(u, two);
+            if (more && !dead) scores(u + 2, two);
         }
     }
     // Every product issued has ended, whether or not a wait gave up before, so that TMEM may go.
@@ -592,9 +617,23 @@ struct Issuer {
 };
 
 // ------------------------------------------------------------------ softmax
+// Whether any of the 64 threads at barrier `id` says yes.
+__device__ __forceinline__ bool vote_rows(bool yes, uint32_t id) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)yes), "r"(id)
+        : "memory");
+    return r != 0;
+}
+
+// A stream's two warpgroups: a thread has one row and half of a tile's tokens, then half of O's columns.  References are the
+// same in both halves.
 struct Softmax {
     Cta c;
-    int stream;
+    int stream, half;
     Ring<kScaleSlots> scale;
     uint32_t s_phase = 0;                  // of this stream's units
     bool bad = false;                      // a wait of this warp gave up: it waits no more, its numbers are none
@@ -603,30 +642,33 @@ struct Softmax {
         if (!bad && !__all_sync(0xffffffffu, wait_up_to(bar, parity, c.plan.stall.wait_us))) bad = true;
     }
 
-    // The stream's 128 queries: eight threads a row, 16 channels each.
-    __device__ __forceinline__ void load_queries(const PrefixPiece& p, const GroupWork& w) {
+    // The stream's 128 queries: eight threads a row, 16 channels each.  (A loop, the next row's loads under this one's
+    // work: unrolled, its instructions took longer to come than the queries.)
+    __device__ __forceinline__ void load_queries(const PrefixPiece& p) {
         const CacheAttention& a = c.a;
-        const int tid = threadIdx.x & (kWarpgroup - 1), part = tid & 7;
-        const int64_t first = (int64_t)p.rows256 * kPair + (p.two ? stream * kRows : 0);
+        const int tid = threadIdx.x & (kStream - 1), part = tid & 7;
+        constexpr int kStride = kStream / 8;
+        const int64_t first = (int64_t)p.rows256 * kPair + (p.two ? stream * kRows : 0), rows = p.rows;
+        const int64_t token0 = (int64_t)p.first_seq * a.T_q;
+        const int head0 = p.hk * c.plan.group;
         const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
         uint8_t* to = c.sm + kQueriesAt + 2 * stream * kTile;
-        constexpr int kTurns = kRows * 8 / kWarpgroup;
-        uint4 all[kTurns][2];                              // all loads before the first is used
-#pragma unroll
-        for (int n = 0; n < kTurns; ++n) {
-            const int64_t at = first + n * (kWarpgroup / 8) + (tid >> 3);
-            const bool real = at < w.rows;
+        auto load = [&](int r, uint4 (&raw)[2]) {
+            const int64_t at = first + r;
+            const bool real = r < kRows && at < rows;
             const int64_t i = real ? at / c.plan.group : 0;
-            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + ((int64_t)w.range.x * a.T_q + i) * a.q_stride +
-                                     (int64_t)(p.hk * c.plan.group + (real ? (int)(at - i * c.plan.group) : 0)) * a.d + 16 * part;
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (token0 + i) * a.q_stride +
+                                     (int64_t)(head0 + (real ? (int)(at - i * c.plan.group) : 0)) * a.d + 16 * part;
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-                all[n][x] = real && 16 * part < a.d ? reinterpret_cast<const uint4*>(q)[x] : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int n = 0; n < kTurns; ++n) {
-            const int r = n * (kWarpgroup / 8) + (tid >> 3);
-            const uint4* raw = all[n];
+                raw[x] = real && 16 * part < a.d ? reinterpret_cast<const uint4*>(q)[x] : make_uint4(0, 0, 0, 0);
+        };
+        uint4 next[2];
+        load(tid >> 3, next);
+#pragma unroll 1
+        for (int r = tid >> 3; r < kRows; r += kStride) {
+            uint4 raw[2] = {next[0], next[1]};
+            load(r + kStride, next);
             const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(raw);
             float amax = 0.0f;
             bool number = true;
@@ -676,10 +718,12 @@ struct Softmax {
         return reinterpret_cast<float4*>(c.plan.runs) + ((int64_t)blockIdx.x * 2 + stream) * 32 * kRows + row;
     }
 
-    // O, its products ended, goes to the sums of runs, which are 2^shift of what they were.  (`first`: there are none.)
-    static __device__ __noinline__ void add_run(uint32_t at, float4* runs, int d, bool first, float shift) {
+    // Columns [c0, c1) of O, its products ended, go to the sums of runs, which are 2^shift of what they were.  (`first`:
+    // there are none.)
+    static __device__ __noinline__ void add_run(uint32_t at, float4* runs, int c0, int c1, bool first, float shift) {
         const float keep = ex2(shift);
-        for (int ch = 0; ch < d; ch += 16) {
+#pragma unroll 1
+        for (int ch = c0; ch < c1; ch += 16) {
             float o[16];
             tc::tmem_ld16(at + ch, o);
             loaded16(o);
@@ -693,134 +737,78 @@ struct Softmax {
             }
         }
     }
-    // The references move to the largest of the scores from chunk h (32 tokens) on: (m, dr, log2 of what that multiplies the
-    // sums by, whether there was any).  The sums in TMEM (where there are any) and the weights of the chunks before
-    // are multiplied in place.  All is taken from differences of rounded products, so that scores whose last places are
-    // whole numbers still give the largest one's value.
-    static __device__ __noinline__ float4 move_references(uint32_t s_at, uint32_t o_at, const Scales* sc, float factor, float m,
-                                                          float dr, bool seen, int h0, int d) {
-        float top = -INFINITY;
+
+    // Columns [c0, c1) of O multiplied in place.
+    static __device__ __noinline__ void scale_sums(uint32_t at, int c0, int c1, float keep) {
 #pragma unroll 1
-        for (int j = 2 * h0; j < kSteps; ++j) {
-            float s[16];
-            tc::tmem_ld16(s_at + 16 * j, s);
-            loaded16(s);
-            float most = s[0];
+        for (int ch = c0; ch < c1; ch += 32) {             // (16 columns at the end are read twice, and one of the two kept)
+            const bool two = ch + 16 < c1;
+            float o[32];
+            tc::tmem_ld16(at + ch, *reinterpret_cast<float(*)[16]>(o));
+            tc::tmem_ld16(at + ch + (two ? 16 : 0), *reinterpret_cast<float(*)[16]>(o + 16));
+            loaded16(o);
+            loaded16(o + 16);
+            uint32_t out[32];
 #pragma unroll
-            for (int x = 1; x < 16; ++x) most = fmaxf(most, s[x]);
-            if (sc->mask >> j & 1) top = fmaxf(top, __fmul_rn(most, factor * sc->step[j].x));
+            for (int x = 0; x < 32; ++x) out[x] = __float_as_uint(o[x] * keep);
+            tc::tmem_st16(at + ch, *reinterpret_cast<uint32_t(*)[16]>(out));
+            if (two) tc::tmem_st16(at + ch + 16, *reinterpret_cast<uint32_t(*)[16]>(out + 16));
         }
-        const bool found = top > -INFINITY;
-        const float m_new = !found ? m : seen ? fmaxf(m, ceilf(top)) : ceilf(top);
-        float reach = -INFINITY;
-#pragma unroll 1
-        for (int j = 2 * h0; j < kSteps; ++j) {
-            float s[16];
-            tc::tmem_ld16(s_at + 16 * j, s);
-            loaded16(s);
-            float most = s[0];
-#pragma unroll
-            for (int x = 1; x < 16; ++x) most = fmaxf(most, s[x]);
-            const float2 st = sc->step[j];
-            if (sc->mask >> j & 1) reach = fmaxf(reach, __fsub_rn(__fmul_rn(most, factor * st.x), m_new) + st.y);
-        }
-        const float dr_old = dr + (seen ? m - m_new : 0.0f);
-        const bool moves = found && (!seen || reach > dr_old);
-        const float dr_new = moves ? ceilf(reach) : dr_old;
-        const float move = seen && moves ? dr_old - dr_new : 0.0f;
-        if (__any_sync(0xffffffffu, move != 0.0f)) {
-            const float keep = ex2(move);
-            tc::tmem_wait_st();                            // the weights stored so far
-            if (d > 0) scale_sums(o_at, d, keep);
-#pragma unroll 1
-            for (int h = 0; h < h0; ++h) {
-                float two[16];
-                uint32_t out[16];
-                tc::tmem_ld16(s_at + 16 * h, two);
-                loaded16(two);
-#pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    const uint32_t bits = __float_as_uint(two[x]);
-                    const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&bits));
-                    out[x] = half2_bits(w.x * keep, w.y * keep);
-                }
-                tc::tmem_st16(s_at + 16 * h, out);
-            }
-            tc::tmem_wait_st();
-        }
-        return make_float4(m_new, dr_new, move, found ? 1.0f : 0.0f);
     }
-    // Weights from chunk h on where steps are missing, scores are beyond 2^22, or pages of values so small beside others that
-    // their weights are lost: the sum of weights by itself, which it returns.
-    static __device__ __noinline__ float far_weights(uint32_t at, const Scales* sc, float factor, float m, float dr, int h0) {
+    // Weights where steps are missing, scores are beyond 2^22, or pages of values so small beside others that their weights
+    // are lost: the sum of weights by itself, which it returns.
+    static __device__ __noinline__ float far_weights(uint32_t at, const Scales* sc, int half, float factor, float m, float dr) {
         float l = 0.0f;
 #pragma unroll 1
-        for (int h = h0; h < 4; ++h) {
+        for (int h = 0; h < 2; ++h) {
             uint32_t out[16];
-            float s[32];
-            load32(at + 32 * h, s);
-            loaded16(s);
-            loaded16(s + 16);
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < 2; ++j) {
-                const float2 st = sc->step[2 * h + j];
-                const bool real = sc->mask >> (2 * h + j) & 1;
+                float s[16];
+                tc::tmem_ld16(at + 32 * h + 16 * j, s);
+                loaded16(s);
+                const float2 st = sc->step[4 * half + 2 * h + j];
+                const bool real = sc->mask >> (4 * half + 2 * h + j) & 1;
                 const float f = factor * st.x, lift = st.y - dr + kBits;
+                uint32_t eight[8];
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
-                    const float z0 = __fsub_rn(__fmul_rn(s[16 * j + 2 * x], f), m);
-                    const float z1 = __fsub_rn(__fmul_rn(s[16 * j + 2 * x + 1], f), m);
+                    const float z0 = __fsub_rn(__fmul_rn(s[2 * x], f), m);
+                    const float z1 = __fsub_rn(__fmul_rn(s[2 * x + 1], f), m);
                     if (real) l += ex2(z0) + ex2(z1);
-                    out[8 * j + x] = real ? half2_bits(ex2(z0 + lift), ex2(z1 + lift)) : 0u;
+                    eight[x] = real ? half2_bits(ex2(z0 + lift), ex2(z1 + lift)) : 0u;
+                }
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    out[x] = j == 0 ? eight[x] : out[x];
+                    out[8 + x] = eight[x];
                 }
             }
             tc::tmem_st16(at + 16 * h, out);
         }
         return l;
     }
-    static __device__ __forceinline__ void scale_sums(uint32_t at, int d, float keep) {
-        int ch = 0;
-#pragma unroll 1
-        for (; ch + 32 <= d; ch += 32) {
-            float o[32];
-            load32(at + ch, o);
-            loaded16(o);
-            loaded16(o + 16);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                uint32_t out[16];
-#pragma unroll
-                for (int y = 0; y < 16; ++y) out[y] = __float_as_uint(o[16 * x + y] * keep);
-                tc::tmem_st16(at + ch + 16 * x, out);
-            }
-        }
-        if (ch < d) {
-            float o[16];
-            uint32_t out[16];
-            tc::tmem_ld16(at + ch, o);
-            loaded16(o);
-#pragma unroll
-            for (int x = 0; x < 16; ++x) out[x] = __float_as_uint(o[x] * keep);
-            tc::tmem_st16(at + ch, out);
-        }
-    }
 
-    __device__ __forceinline__ void piece(const PrefixPiece& p, const GroupWork& w) {
+    __device__ __forceinline__ void piece(const PrefixPiece& p) {
         const CacheAttention& a = c.a;
-        const int row = threadIdx.x & (kWarpgroup - 1);
+        const int row = threadIdx.x & (kRows - 1);
+        const uint32_t id = kBarRows + 4 * stream + (row >> 5);
         const uint32_t lanes = (uint32_t)(row & 96) << 16;
-        const uint32_t s_at = c.tmem + lanes + 128 * stream, o_at = s_at + kTmemO;
-        load_queries(p, w);
+        // This thread's scores, then (from their first column on) its weights.
+        const uint32_t s_at = c.tmem + lanes + 128 * stream + 64 * half, o_at = c.tmem + lanes + 128 * stream + kTmemO;
+        const int middle = (a.d / 16 + 1) / 2 * 16, c0 = half ? middle : 0, c1 = half ? a.d : middle;
+        load_queries(p);
         tc::fence_async_smem();
-        tc::named_bar_sync(1 + stream, kWarpgroup);
-        if (threadIdx.x % kWarpgroup == 0) tc::mbar_arrive(&c.small->q_full[stream]);
+        tc::named_bar_sync(kBarStream + stream, kStream);
+        if (threadIdx.x % kStream == 0) tc::mbar_arrive(&c.small->q_full[stream]);
         const float factor = c.small->factor[stream * kRows + row];
 
         // m: the largest score so far, rounded up (or 0: none); weights are relative to m + dr.
         float m = 0.0f, dr = 0.0f, l = 0.0f, shift = 0.0f;
         bool seen = false;
-        const int tiles = p.to - p.from, units = p.two ? tiles : (tiles + 1 - stream) >> 1;
-        if (!p.two && stream) scale.next();
+        const bool two = p.two;
+        const int tiles = p.to - p.from, units = two ? tiles : (tiles + 1 - stream) >> 1;
+        if (!two && stream) scale.next();
 #pragma unroll 1
         for (int k = 0; k < units; ++k) {
             wait(&c.small->scale_full[scale.slot], scale.phase);
@@ -831,151 +819,181 @@ struct Softmax {
             if (fresh && k > 0) {
                 wait(&c.small->o_done[stream], s_phase ^ 1);
                 tc::tc_fence_after();
-                if (!bad) add_run(o_at, run_at(row), a.d, k == kRun, shift);
+                if (!bad) add_run(o_at, run_at(row), c0, c1, k == kRun, shift);
                 shift = 0.0f;
             }
-            const float lowest = sc->lowest;
-            auto near = [&]() { return fabsf(m) < kNear && dr - lowest < 90.0f; };
-            auto move = [&](int h) {
-                if (!fresh) wait(&c.small->o_done[stream], s_phase ^ 1);
-                tc::tc_fence_after();
-                const float4 to = move_references(s_at, o_at, sc, factor, m, dr, seen, h, fresh || bad ? 0 : a.d);
-                l *= seen ? ex2(m - to.x) : 1.0f;
-                m = to.x;
-                dr = to.y;
-                shift += to.z;
-                seen |= to.w != 0.0f;
-            };
-            // One pass, 32 tokens at a time, under the references so far.  Sums of 16 weights, which the sum of all needs anyway, tell
-            // where a weight would be too large: then the references move first.
-            int h = 0;
-            if (sc->mask == (1u << kSteps) - 1 && __all_sync(0xffffffffu, seen && near())) {
-                bool moved = false;
-#pragma unroll 1
-                for (; h < 4; ++h) {
+            // Scores are loaded twice, 32 tokens at a time: for the largest, then for the weights.
+            const uint32_t mine = sc->mask >> (kSteps / 2 * half);
+            float xs[kSteps / 2], top = -INFINITY, reach = -INFINITY;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float now[32];
+                load32(s_at + 32 * h, now);
+                const float4 st = *reinterpret_cast<const float4*>(&sc->step[kSteps / 2 * half + 2 * h]);
+                loaded16(now);
+                loaded16(now + 16);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float most = now[16 * j];
+#pragma unroll
+                    for (int x = 1; x < 15; x += 2) most = fmaxf(fmaxf(most, now[16 * j + x]), now[16 * j + x + 1]);
+                    most = fmaxf(most, now[16 * j + 15]);
+                    const float x = mine >> (2 * h + j) & 1 ? __fmul_rn(most, factor * (j ? st.z : st.x)) : -INFINITY;
+                    xs[2 * h + j] = x;
+                    top = fmaxf(top, x);
+                    reach = fmaxf(reach, (x - m) + (j ? st.w : st.y));   // (m first: it may have no places to add to)
+                }
+            }
+            // Where a weight would be too large, all references of the two warps' rows move to the largest so far.
+            if (vote_rows(reach - dr > kFar || (!seen && top > -INFINITY), id)) {
+                c.small->top[stream][half][row] = top;
+                tc::named_bar_sync(id, 64);
+                top = fmaxf(top, c.small->top[stream][half ^ 1][row]);
+                const bool found = top > -INFINITY;
+                const float m_new = !found ? m : seen ? fmaxf(m, ceilf(top)) : ceilf(top);
+                // (differences of rounded products: scores whose last places are whole numbers still give the largest
+                // one's value)
+                reach = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < kSteps / 2; ++j) reach = fmaxf(reach, __fsub_rn(xs[j], m_new) + sc->step[kSteps / 2 * half + j].y);
+                c.small->reach[stream][half][row] = reach;
+                tc::named_bar_sync(id, 64);
+                reach = fmaxf(reach, c.small->reach[stream][half ^ 1][row]);
+                const float dr_old = dr + (seen ? m - m_new : 0.0f);
+                const bool moves = found && (!seen || reach > dr_old);
+                const float dr_new = moves ? ceilf(reach) : dr_old;
+                const float move = seen && moves ? dr_old - dr_new : 0.0f;
+                if (!fresh && __any_sync(0xffffffffu, move != 0.0f)) {
+                    wait(&c.small->o_done[stream], s_phase ^ 1);
+                    tc::tc_fence_after();
+                    if (!bad) scale_sums(o_at, c0, c1, ex2(move));
+                }
+                l *= seen ? ex2(m - m_new) : 1.0f;
+                shift += move;
+                m = m_new;
+                dr = dr_new;
+                seen |= found;
+            }
+            // (the same in both halves)
+            const bool near = __all_sync(0xffffffffu, fabsf(m) < kNear && dr - sc->lowest < 90.0f);
+            if (near && sc->mask == (1u << kSteps) - 1) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
                     float now[32];
                     load32(s_at + 32 * h, now);
-                    const float4 st = *reinterpret_cast<const float4*>(&sc->step[2 * h]);
-                    const float f[2] = {factor * st.x, factor * st.z}, lv[2] = {st.y, st.w};
+                    const float4 st = *reinterpret_cast<const float4*>(&sc->step[kSteps / 2 * half + 2 * h]);
                     uint32_t out[16];
-                    float sum[2];
                     loaded16(now);
                     loaded16(now + 16);
-#pragma unroll 1
-                    for (;;) {
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const float less = (lv[j] - dr + kBits) - m;
-                            const uint64_t ff = f2_pack(f[j], f[j]), cc = f2_pack(less, less);
-                            uint64_t both = 0;
+                    for (int j = 0; j < 2; ++j) {
+                        const float f = factor * (j ? st.z : st.x), lv = j ? st.w : st.y, less = (lv - dr + kBits) - m;
+                        const uint64_t ff = f2_pack(f, f), cc = f2_pack(less, less);
+                        uint64_t both = 0;
 #pragma unroll
-                            for (int x = 0; x < 8; ++x) {
-                                const float2 e = f2_unpack(f2_fma(f2_pack(now[16 * j + 2 * x], now[16 * j + 2 * x + 1]), ff, cc));
-                                const float w0 = ex2(e.x), w1 = ex2(e.y);
-                                both = x == 0 ? f2_pack(w0, w1) : add_pair(both, f2_pack(w0, w1));
-                                out[8 * j + x] = half2_bits(w0, w1);
-                            }
-                            const float2 two = f2_unpack(both);
-                            sum[j] = two.x + two.y;
+                        for (int x = 0; x < 8; ++x) {
+                            const float2 e = f2_unpack(f2_fma(f2_pack(now[16 * j + 2 * x], now[16 * j + 2 * x + 1]), ff, cc));
+                            const float w0 = ex2(e.x), w1 = ex2(e.y);
+                            both = x == 0 ? f2_pack(w0, w1) : add_pair(both, f2_pack(w0, w1));
+                            out[8 * j + x] = half2_bits(w0, w1);
                         }
-                        if (moved || !__any_sync(0xffffffffu, fmaxf(sum[0], sum[1]) > kMost)) break;
-                        move(h);
-                        moved = true;
-                        if (!__all_sync(0xffffffffu, near())) break;
+                        const float2 two = f2_unpack(both);
+                        l = fmaf(two.x + two.y, ex2(dr - kBits - lv), l);
                     }
-                    if (moved && !__all_sync(0xffffffffu, near())) break;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) l = fmaf(sum[j], ex2(dr - kBits - lv[j]), l);
                     tc::tmem_st16(s_at + 16 * h, out);
                 }
             } else {
-                move(0);
+                l += far_weights(s_at, sc, half, factor, m, dr);
             }
-            if (h < 4) l += far_weights(s_at, sc, factor, m, dr, h);
             tc::tmem_wait_st();
             tc::tc_fence_before();
             tc::mbar_arrive(&c.small->p_full[stream]);
             s_phase ^= 1;
             scale.next();
-            if (!p.two && 2 * k + stream + 1 < tiles) scale.next();
+            if (!two && 2 * k + stream + 1 < tiles) scale.next();
         }
         if (units > 0) wait(&c.small->o_done[stream], s_phase ^ 1);
         tc::tc_fence_after();
 
-        float M = seen ? m : kLowest, DM = -dr - (kWeightBits - kBits), L = bad ? NAN : l;
-        if (!seen) DM = 0.0f;
-        const bool runs = units > kRun;
+        // The end: both halves' sums of weights, and each half's columns.
+        c.small->reach[stream][half][row] = bad ? NAN : l;
+        tc::named_bar_sync(kBarStream + stream, kStream);
+        const float L = c.small->reach[stream][0][row] + c.small->reach[stream][1][row];
+        const float M = seen ? m : kLowest, DM = seen ? -dr - (kWeightBits - kBits) : 0.0f;
+        const bool runs = units > kRun, none = units == 0;
         const float keep = ex2(shift);
         auto sums = [&](int ch, float (&o)[16]) {
-            if (units == 0 || bad) {
-#pragma unroll
-                for (int x = 0; x < 16; ++x) o[x] = bad ? NAN : 0.0f;
-                return;
-            }
             tc::tmem_ld16(o_at + ch, o);
             loaded16(o);
-            if (!runs) return;
+            if (runs) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const float4 r = run_at(row)[(ch / 4 + x) * kRows];
-                o[4 * x] = fmaf(r.x, keep, o[4 * x]);
-                o[4 * x + 1] = fmaf(r.y, keep, o[4 * x + 1]);
-                o[4 * x + 2] = fmaf(r.z, keep, o[4 * x + 2]);
-                o[4 * x + 3] = fmaf(r.w, keep, o[4 * x + 3]);
+                for (int x = 0; x < 4; ++x) {
+                    const float4 r = run_at(row)[(ch / 4 + x) * kRows];
+                    o[4 * x] = fmaf(r.x, keep, o[4 * x]);
+                    o[4 * x + 1] = fmaf(r.y, keep, o[4 * x + 1]);
+                    o[4 * x + 2] = fmaf(r.z, keep, o[4 * x + 2]);
+                    o[4 * x + 3] = fmaf(r.w, keep, o[4 * x + 3]);
+                }
+            }
+            if (bad || none) {
+#pragma unroll
+                for (int x = 0; x < 16; ++x) o[x] = bad ? NAN : 0.0f;
             }
         };
-        if (!p.two) {
-            // Both streams' sums of the same rows: the second's through the queries' place, whose products have ended.
-            tc::named_bar_sync(kBarBoth, kPair);
-            float4* other = reinterpret_cast<float4*>(c.sm + kQueriesAt) + row;
+        // Where both streams have the same rows, the second's sums go through the queries' place, whose products have ended.
+        float4* other = two ? nullptr : reinterpret_cast<float4*>(c.sm + kQueriesAt) + row;
+        float4 stat = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (!two) {
+            tc::named_bar_sync(kBarBoth, 2 * kStream);
             if (stream == 1) {
-                for (int ch = 0; ch < a.d; ch += 16) {
+#pragma unroll 1
+                for (int ch = c0; ch < c1; ch += 16) {
                     float o[16];
                     sums(ch, o);
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
                         other[(ch / 4 + x) * kRows] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
                 }
-                c.small->stat[row] = make_float4(M, DM, L, 0.0f);
+                if (half == 0) c.small->stat[row] = make_float4(M, DM, L, 0.0f);
             }
-            tc::named_bar_sync(kBarBoth, kPair);
-            if (stream == 0) write(p, w, row, M, DM, L, sums, other, c.small->stat[row]);
-            tc::named_bar_sync(kBarBoth, kPair);
-        } else {
-            write(p, w, stream * kRows + row, M, DM, L, sums, nullptr, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+            tc::named_bar_sync(kBarBoth, 2 * kStream);
+            stat = c.small->stat[row];
         }
-        tc::tc_fence_before();                             // the next piece's products may overwrite the sums
-    }
-
-    // The piece's row r: its sums, with those of `other` where there are any, to what the row carries or to the share's slot.
-    template <typename F>
-    __device__ __forceinline__ void write(const PrefixPiece& p, const GroupWork& w, int r, float M, float DM, float L, F sums,
-                                          const float4* other, float4 stat) {
-        const int64_t at = (int64_t)p.rows256 * kPair + r;
-        const bool real = at < w.rows;
-        const int64_t out = !real ? 0 : p.whole ? prefix_row(c.a, c.plan, w, p.hk, at) : ((int64_t)blockIdx.x * 2 + p.slot) * kPair + r;
-        float* to = (p.whole ? c.a.carry_sums : c.plan.sums) + out * c.plan.D;
-        for (int ch = 0; ch < c.a.d; ch += 16) {
-            float o[16];
-            sums(ch, o);                                   // (by whole warps: from TMEM)
-            float4 v[4];
+        if (two || stream == 0) {
+            // To what the row carries, or to the share's slot.
+            const int r = (two ? stream * kRows : 0) + row;
+            const int64_t at = (int64_t)p.rows256 * kPair + r;
+            const bool real = at < p.rows;
+            const int64_t out = !real ? 0 : p.whole ? prefix_row(a, c.plan, p.first_seq, p.hk, at) : ((int64_t)blockIdx.x * 2 + p.slot) * kPair + r;
+            float* to = (p.whole ? a.carry_sums : c.plan.sums) + out * c.plan.D;
+            // (join_sums' factors, once)
+            const float m_all = other ? fmaxf(M, stat.x) : M, dm_all = other ? fminf(DM + (m_all - M), stat.y + (m_all - stat.x)) : DM;
+            const float mine = other ? ex2(M - m_all + (dm_all - DM)) : 1.0f, its = other ? ex2(stat.x - m_all + (dm_all - stat.y)) : 0.0f;
+#pragma unroll 1
+            for (int ch = c0; ch < c1; ch += 16) {
+                float o[16];
+                sums(ch, o);                               // (by whole warps: from TMEM)
+                if (other) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                v[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-                float m = M, dm = DM, l = L;
-                if (other) join_sums(v[x], m, dm, l, stat, other[(ch / 4 + x) * kRows]);
+                    for (int x = 0; x < 4; ++x) {
+                        const float4 y = other[(ch / 4 + x) * kRows];
+                        o[4 * x] = o[4 * x] * mine + y.x * its;
+                        o[4 * x + 1] = o[4 * x + 1] * mine + y.y * its;
+                        o[4 * x + 2] = o[4 * x + 2] * mine + y.z * its;
+                        o[4 * x + 3] = o[4 * x + 3] * mine + y.w * its;
+                    }
+                }
+                // (a thread has a row: whole sectors of 32 bytes at a time)
+                if (real) {
+                    store8(to + ch, o);
+                    store8(to + ch + 8, o + 8);
+                }
             }
-            // (a thread has a row: whole sectors of 32 bytes at a time)
-            if (real) {
-                store8(to + ch, v[0], v[1]);
-                store8(to + ch + 8, v[2], v[3]);
-            }
+            const float l_all = other ? L * ex2(M - m_all) + stat.z * ex2(stat.x - m_all) : L;
+            if (real && half == 0) (p.whole ? a.carry_stats : c.plan.stats)[out] = make_float4(m_all, dm_all, l_all, 0.0f);
         }
-        if (other) {
-            float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            join_sums(none, M, DM, L, stat, none);
-        }
-        if (real) (p.whole ? c.a.carry_stats : c.plan.stats)[out] = make_float4(M, DM, L, 0.0f);
+        if (!two) tc::named_bar_sync(kBarBoth, 2 * kStream);   // before the queries' place is theirs again
+        tc::tc_fence_before();                             // the next piece's products may overwrite the sums
     }
 };
 
@@ -1001,9 +1019,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_init(&small->v_empty[i], 1);
         }
         for (int i = 0; i < kScaleSlots; ++i) tc::mbar_init(&small->scale_full[i], 1);
+        for (int i = 0; i < kPieceSlots; ++i) {
+            tc::mbar_init(&small->piece_full[i], 1);
+            tc::mbar_init(&small->piece_empty[i], 32 * kPlannerWarp);   // every thread of the roles before the planner
+        }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&small->s_full[i], 1);
-            tc::mbar_init(&small->p_full[i], kWarpgroup);
+            tc::mbar_init(&small->p_full[i], kStream);
             tc::mbar_init(&small->o_done[i], 1);
             tc::mbar_init(&small->q_full[i], 1);
         }
@@ -1014,32 +1036,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    const PrefixShare share = find_prefix_share(a, plan);
     const Cta cta{a, plan, sm, small, small->tmem};
     if (warp < kConverterWarp) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        Softmax role{cta, warp >> 2};
-        const int4 join = for_each_prefix_piece(a, plan, share, [&](const PrefixPiece& p, const GroupWork& w) { role.piece(p, w); });
-        if (threadIdx.x == 0) plan.joins[blockIdx.x] = join;
+        Softmax role{cta, warp >> 3, warp >> 2 & 1};
+        for_each_piece_told(cta, [&](const PrefixPiece& p) { role.piece(p); });
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp < kIssuerWarp) {
             Converter role{cta};
-            for_each_prefix_piece(a, plan, share, [&](const PrefixPiece& p, const GroupWork&) {
+            for_each_piece_told(cta, [&](const PrefixPiece& p) {
                 if (!role.dead) role.piece(p);
             });
         } else if (warp == kLoaderWarp) {
             Loader role{cta, &k_map, &v_map};
-            for_each_prefix_piece(a, plan, share, [&](const PrefixPiece& p, const GroupWork& w) {
-                if (!role.dead) role.piece(p, w);
+            for_each_piece_told(cta, [&](const PrefixPiece& p) {
+                if (!role.dead) role.piece(p);
             });
             role.finish();
         } else if (warp == kIssuerWarp) {
             Issuer role{cta};
-            for_each_prefix_piece(a, plan, share, [&](const PrefixPiece& p, const GroupWork&) {
+            for_each_piece_told(cta, [&](const PrefixPiece& p) {
                 if (!role.dead) role.piece(p);
             });
             role.finish();
+        } else if (warp == kPlannerWarp) {
+            const PrefixShare share = find_prefix_share(a, plan);
+            Ring<kPieceSlots> ring;
+            auto tell = [&](const PrefixPiece& p) {
+                if (ring.again)
+                    __all_sync(0xffffffffu, wait_up_to(&small->piece_empty[ring.slot], ring.phase ^ 1, kPatience * plan.stall.wait_us));
+                if (elected()) {
+                    small->piece[ring.slot] = p;
+                    tc::mbar_arrive(&small->piece_full[ring.slot]);
+                }
+                __syncwarp();
+                ring.next();
+            };
+            const int4 join = for_each_prefix_piece(a, plan, share, tell);
+            PrefixPiece end = {};
+            tell(end);
+            if (elected()) plan.joins[blockIdx.x] = join;
         }
     }
     __syncwarp();
@@ -1077,7 +1114,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) prefix_join_kernel(const Cache
             join_sums(o, M, DM, L, s, x);
         }
     }
-    const int64_t out = prefix_row(a, plan, w, join.y, at);
+    const int64_t out = prefix_row(a, plan, w.range.x, join.y, at);
     if (ch < a.d) *reinterpret_cast<float4*>(a.carry_sums + out * plan.D + ch) = o;
     if (lane == 0) a.carry_stats[out] = make_float4(M, DM, L, 0.0f);
 }
