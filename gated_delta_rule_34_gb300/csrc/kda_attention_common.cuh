@@ -222,6 +222,13 @@ inline int64_t most_steps(const CacheAttention& a) {
     return seen < held ? seen : held;
 }
 
+// kRest: the steps that sequences are taken to have beyond their prefix, by the widths of the two tables (all of them,
+// where these say nothing).  Only whether items are cut goes by it.
+inline int64_t rest_steps(const CacheAttention& a) {
+    const int64_t rest = (int64_t)(a.table_pages > a.prefix_pages ? a.table_pages - a.prefix_pages : a.table_pages);
+    return (rest << a.page_shift) / kStep;
+}
+
 // Whether one CTA an item is faster than equal shares of all items' steps.  Cutting costs each CTA a second start and
 // end and a kernel that joins, together the time of `cutting` steps; whole items cost what the longest takes beyond
 // the average load of the CTAs, where lengths are even from 0 to the longest: cap - items cap / (2 ctas) steps.
@@ -426,7 +433,7 @@ cudaError_t run_attention_prefix_tc(const CacheAttention& a, void* workspace, cu
 // the work out (0: each item is one CTA's), and the launch.
 bool attention_tc_takes(const CacheAttention& a, bool bf16);
 attn::Plan attention_tc_plan(const CacheAttention& a);
-int64_t attention_tc_grid(const CacheAttention& a, const attn::Plan& plan, int num_sms);
+int64_t attention_tc_grid(const CacheAttention& a, const attn::Plan& plan, int num_sms, attn::Part part = attn::kAll);
 cudaError_t run_attention_tc(const CacheAttention& a, void* workspace, cudaStream_t stream, int num_sms);
 cudaError_t run_attention_tc_rest(const CacheAttention& a, void* workspace, cudaStream_t stream, int num_sms);
 

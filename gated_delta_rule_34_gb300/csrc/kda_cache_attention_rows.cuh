@@ -828,7 +828,7 @@ template <Part P>
 int64_t share_grid(const CacheAttention& a, const Plan& plan, int64_t most) {
     const int64_t cap = P == kPrefix ? ((int64_t)a.prefix_pages << a.page_shift) / kStep : most_steps(a);
     const int64_t pairs = pairs_of<P>(a, plan), items = pairs * a.H_kv;
-    if (whole_items_pay(cap, items, most, 32, 128) || pairs > kMaxScan) return 0;
+    if (whole_items_pay(P == kRest ? rest_steps(a) : cap, items, most, 32, 128) || pairs > kMaxScan) return 0;
     const int64_t useful = (items * (cap + plan.item_cost) + kMinShare - 1) / kMinShare;
     return useful < most ? useful : most;
 }

@@ -831,10 +831,10 @@ attn::Plan attention_tc_plan(const CacheAttention& a) {
 // 16 tiles (2,048 tokens), 32 items 32 us whole and 23 cut, 128 items 32 and 37, 512 items 86 and 101, 2,048 items 294 and 343;
 // 32 tiles, 256 items 76 and 86 us, lengths that differ 72 and 66.  Very few items are cut from 5 tiles on (8 items of 8
 // tiles: 21 us whole, 17 cut).
-int64_t attention_tc_grid(const CacheAttention& a, const attn::Plan& plan, int num_sms) {
+int64_t attention_tc_grid(const CacheAttention& a, const attn::Plan& plan, int num_sms, attn::Part part) {
     const int64_t cap = most_steps(a), items = (int64_t)a.B * plan.row_tiles * a.H_kv, most = (int64_t)num_sms * kCtas;
     const bool few = 10 * items < most;
-    if (whole_items_pay(cap, items, most, 13 * kTileSteps, (few ? 4 : 32) * kTileSteps) ||
+    if (whole_items_pay(part == kRest ? rest_steps(a) : cap, items, most, 13 * kTileSteps, (few ? 4 : 32) * kTileSteps) ||
         (int64_t)a.B * plan.row_tiles > kMaxScan)
         return 0;
     const int64_t useful = (items * (cap + plan.item_cost) + kMinShare - 1) / kMinShare;
@@ -851,7 +851,7 @@ template <Part P>
 cudaError_t launch_tc(const CacheAttention& a, void* workspace, cudaStream_t stream, int num_sms) {
     Plan plan = attention_tc_plan(a);
     plan.stall = stall;
-    const int64_t grid = attention_tc_grid(a, plan, num_sms);
+    const int64_t grid = attention_tc_grid(a, plan, num_sms, P);
     if (grid == 0) {
         const int64_t items = (int64_t)a.B * plan.row_tiles * a.H_kv;
         cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<true, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);

@@ -17,7 +17,7 @@
 // converted once for both. Where 128 rows or fewer are left, both streams take them, the tiles of tokens in turn. Roles:
 //   16 softmax   scores from TMEM, weights back into the same columns: eight warps a stream, half of a tile's tokens each
 //   4 converters values from e4m3 to fp16
-//   1 issuer     S of a stream's next tile after the O of its last one: S and W share their columns
+//   1 issuer     S of a stream's next tile after the O of its last one, since S and W share their columns
 //   1 loader     pages by TMA, 128-byte-swizzled rows, a box a page (of up to 128 tokens); their scales
 //   1 planner    the CTA's pieces, told to the others through shared memory
 // A row's reference moves when a score passes it by more than a factor of 128; it is a whole number, so that weights,
@@ -121,20 +121,27 @@ struct PrefixPlan {
 constexpr uint32_t idesc(uint32_t M, uint32_t N, uint32_t a_format, bool b_mn) {
     return (1u << 4) | (a_format << 7) | ((b_mn ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
+// Shared-memory descriptors by their lower words (address and the stride along the 128-byte rows); the upper words are
+// constant: 1024 bytes from eight rows to the next, version 1, 128-byte swizzle.
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) { return (addr >> 4 & 0x3FFFu) | lbo >> 4 << 16; }
 // fp8 (a_format 0 e4m3, 1 e5m2; B e4m3), both from shared memory.
-__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t desc, bool accumulate) {
+template <bool ADD>
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t desc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a), "l"(b), "r"(desc),
-        "r"((uint32_t)accumulate)
+        "{\n\t.reg .b64 da, db;\n\t.reg .pred p;\n\t"
+        "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem), "r"(a), "r"(b), "r"(desc),
+        "n"(kDescHigh), "n"(ADD ? 1 : 0)
         : "memory");
 }
 // fp16, A from TMEM.
-__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t desc, bool accumulate) {
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t desc, bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(desc),
-        "r"((uint32_t)accumulate)
+        "{\n\t.reg .b64 db;\n\t.reg .pred p;\n\t"
+        "mov.b64 db, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem), "r"(a_tmem), "r"(b), "r"(desc),
+        "r"((uint32_t)accumulate), "n"(kDescHigh)
         : "memory");
 }
 // 32 columns of the warp's 32 lanes, a lane a thread.
@@ -200,18 +207,37 @@ __device__ __forceinline__ bool elected() {
     return r != 0;
 }
 
-// tc::mbar_wait with a limit of the caller's, in microseconds, counted in cycles of 2 GHz.  (The global timer, which that one
-// reads before it polls, takes longer than most waits here.)
+// tc::mbar_wait with a limit of the caller's, in microseconds, counted in cycles of 2 GHz.  A try may rest for 10 us before it
+// says no, so that waiting warps take no issue slots from working ones.
+__device__ __forceinline__ bool try_long(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(10000u)
+        : "memory");
+    return ok != 0;
+}
+// Without a rest.
+__device__ __forceinline__ bool has_come(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool wait_up_to(uint64_t* bar, uint32_t parity, int limit) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
-    long long t0 = 0;
-    for (uint32_t i = 1; i < (1u << 30); ++i) {
-        if (tc::mbar_try_wait(bar, parity)) return true;
-        if ((i & 63u) == 0) {
-            const long long now = clock64();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > 2000ll * limit) break;
-        }
+    if (try_long(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (uint32_t i = 0; i < (1u << 30); ++i) {
+        if (try_long(bar, parity)) return true;
+        if (clock64() - t0 > 2000ll * limit) break;
     }
     return false;
 }
@@ -339,6 +365,19 @@ struct Cta {
     uint32_t tmem;
 };
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// An arrival for a whole warp: what its lanes did before is done.  (Arrivals of single lanes at one barrier follow one
+// another.)
+__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
+}
+
 // A ring's next slot and the parity of its use.
 template <int N>
 struct Ring {
@@ -352,6 +391,11 @@ struct Ring {
             again = true;
         }
     }
+    __device__ __forceinline__ void skip(int n) {
+        const int at = slot + n % N;
+        phase ^= (uint32_t)(n / N + at / N) & 1u;
+        slot = at % N;
+    }
 };
 
 // Calls f for each piece that the planner writes; whole warps.
@@ -363,7 +407,7 @@ __device__ __forceinline__ void for_each_piece_told(const Cta& c, F f) {
         const PrefixPiece& p = c.small->piece[ring.slot];
         if (p.from >= p.to) return;
         f(p);
-        tc::mbar_arrive(&c.small->piece_empty[ring.slot]);
+        arrive_warp(&c.small->piece_empty[ring.slot]);
         ring.next();
     }
 }
@@ -510,8 +554,8 @@ struct Converter {
                 *reinterpret_cast<uint4*>(to + tc::sw128(t, c0 + 1 - late)) = second;
             }
             tc::fence_async_smem();
-            tc::mbar_arrive(&c.small->v_full[v.slot]);
-            tc::mbar_arrive(&c.small->raw_empty[raw.slot]);
+            arrive_warp(&c.small->v_full[v.slot]);
+            arrive_warp(&c.small->raw_empty[raw.slot]);
             raw.next();
             v.next();
             scale.next();
@@ -520,94 +564,131 @@ struct Converter {
 };
 
 // ------------------------------------------------------------------ issuer
-// Units of a piece: (tile, stream), in the order in which their products are issued.  Two streams take every tile, one
-// after the other; one item of 128 rows has its tiles taken by the streams in turn.  Unit u is stream u & 1's either way.
+// A unit is a stream's tile: O += W V of it, then, once these products have read W, S of the stream's next tile,
+// which goes where W lies.  Both streams' units are taken as their weights come, each to its end: so one stream's
+// products run under the other's softmax, and not both under neither.  (An issuer a stream: both did the same at the
+// same time, 218 us for 256 sequences behind 32,768 tokens against 206.)
 struct Issuer {
     Cta c;
-    Ring<kKeySlots> k;
-    Ring<kValueSlots> v;
-    uint32_t s_phases = 0;                 // a bit a stream: parity of the unit whose weights are waited for next
+    Ring<kKeySlots> k[2];                  // of each stream's next unit
+    Ring<kValueSlots> v[2];
+    bool k_here[2] = {false, false}, v_here[2] = {false, false};   // their tiles have been seen to be there
+    uint32_t phase[2] = {0, 0};            // of each stream's weights
     uint32_t q_phase = 0;
     int tiles = 0;
     bool dead = false;
 
-    // All lanes call everything, and agree; one of them issues.
+    // All lanes call everything, and agree; one of them issues.  (With one thread alone a product took 105 cycles to issue,
+    // its descriptors moved to uniform registers one by one; the product takes 64.)
     __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
         if (!dead && !__all_sync(0xffffffffu, wait_up_to(bar, parity, c.plan.stall.wait_us))) dead = true;
     }
-    // Products that follow one another without a loop's instructions between them: each takes 64 cycles, and one thread
-    // issues them all.
     template <int CHUNKS>
-    static __device__ __forceinline__ void score_products(uint32_t d_tmem, uint64_t q, uint64_t keys) {
+    static __device__ __forceinline__ void score_products(uint32_t d_tmem, uint32_t q, uint32_t keys) {
+        mma_f8<false>(d_tmem, q, keys, idesc(128, kTokens, 1, false));
 #pragma unroll
-        for (int x = 0; x < CHUNKS; ++x) mma_f8(d_tmem, q + 2 * x, keys + 2 * x, idesc(128, kTokens, 1, false), x > 0);
+        for (int x = 1; x < CHUNKS; ++x) mma_f8<true>(d_tmem, q + 2 * x, keys + 2 * x, idesc(128, kTokens, 1, false));
 #pragma unroll
         for (int x = 0; x < CHUNKS; ++x)
-            mma_f8(d_tmem, q + (kTile >> 4) + 2 * x, keys + 2 * x, idesc(128, kTokens, 0, false), true);
+            mma_f8<true>(d_tmem, q + (kTile >> 4) + 2 * x, keys + 2 * x, idesc(128, kTokens, 0, false));
     }
-    // Keys of unit u's tile, where it is the first to read them: waited for before what it has to wait for at last.
-    __device__ __forceinline__ void keys_of(int u, bool two) {
-        if (two && (u & 1)) return;
-        if (++tiles > c.plan.stall.tiles) dead = true;
-        wait(&c.small->k_full[k.slot], k.phase);
+    // A tile that both streams read is given back by both; one that only one does, by that one twice.
+    static __device__ __forceinline__ void give_back(uint64_t* bar, bool two) {
+        tc::mma_commit(bar);
+        if (!two) tc::mma_commit(bar);
     }
-    __device__ __forceinline__ void scores(int u, bool two) {
-        const int stream = u & 1;
-        // the stream's last products have read the weights that lie where the scores go
-        if (u >= 2) wait(&c.small->o_done[stream], (s_phases >> stream & 1) ^ 1);
+    template <int STREAM>
+    __device__ __forceinline__ void scores(bool two, bool later) {
+        if (tiles++ / 2 >= c.plan.stall.tiles) dead = true;
+        const int slot = k[STREAM].slot;
+        if (!k_here[STREAM]) wait(&c.small->k_full[slot], k[STREAM].phase);
+        if (later) wait(&c.small->o_done[STREAM], phase[STREAM] ^ 1);
         if (dead) return;
         tc::tc_fence_after();
-        const uint64_t keys = tc::desc_sw128(smem_u32(c.sm + kKeysAt + k.slot * kTile));
-        const uint64_t q = tc::desc_sw128(smem_u32(c.sm + kQueriesAt + 2 * stream * kTile));
-        const uint32_t to = c.tmem + 128 * stream;
-        const bool last = !two || stream == 1;             // that reads the keys
+        const uint32_t base = smem_u32(c.sm), keys = desc_low(base + kKeysAt + slot * kTile, 16);
+        const uint32_t q = desc_low(base + kQueriesAt + 2 * STREAM * kTile, 16), to = c.tmem + 128 * STREAM;
         const int chunks = (c.a.d + 31) / 32;              // 32 channels a product
         if (elected()) {
             if (chunks == 4) score_products<4>(to, q, keys);
             else if (chunks == 3) score_products<3>(to, q, keys);
             else if (chunks == 2) score_products<2>(to, q, keys);
             else score_products<1>(to, q, keys);
-            tc::mma_commit(&c.small->s_full[stream]);
-            if (last) tc::mma_commit(&c.small->k_empty[k.slot]);
+            tc::mma_commit(&c.small->s_full[STREAM]);
+            give_back(&c.small->k_empty[slot], two);
         }
-        if (last) k.next();
+        __syncwarp();
+        k[STREAM].next();
+        if (!two) k[STREAM].next();
     }
-    __device__ __forceinline__ void values(int u, bool two) {
-        const int stream = u & 1, nth = u >> 1;            // nth of the stream's units
-        if (!two || stream == 0) wait(&c.small->v_full[v.slot], v.phase);
-        wait(&c.small->p_full[stream], s_phases >> stream & 1);
+    // `fresh`: O has no sums yet.  The weights have come.
+    template <int STREAM>
+    __device__ __forceinline__ void values(bool two, bool fresh) {
+        const int slot = v[STREAM].slot;
+        if (!v_here[STREAM]) wait(&c.small->v_full[slot], v[STREAM].phase);
         if (dead) return;
-        s_phases ^= 1u << stream;
         tc::tc_fence_after();
-        const uint64_t values = tc::desc_sw128_mn(smem_u32(c.sm + kValuesAt + v.slot * kValueTile), kTile, 1024);
-        const uint32_t from = c.tmem + 128 * stream, to = from + kTmemO, desc = idesc(128, c.a.d, 0, true);
-        const bool last = !two || stream == 1;             // that reads the values
+        const uint32_t values = desc_low(smem_u32(c.sm) + kValuesAt + slot * kValueTile, kTile);
+        const uint32_t from = c.tmem + 128 * STREAM, to = from + kTmemO, desc = idesc(128, c.a.d, 0, true);
         if (elected()) {
-            mma_f16_ta(to, from, values, desc, nth % kRun != 0);
+            mma_f16_ta(to, from, values, desc, !fresh);
 #pragma unroll
             for (int x = 1; x < kSteps; ++x)               // 16 tokens a product
                 mma_f16_ta(to, from + 8 * x + (x >= kSteps / 2 ? 32 : 0), values + x * (kStep * 128 >> 4), desc, true);
-            tc::mma_commit(&c.small->o_done[stream]);
-            if (last) tc::mma_commit(&c.small->v_empty[v.slot]);
+            tc::mma_commit(&c.small->o_done[STREAM]);
+            give_back(&c.small->v_empty[slot], two);
         }
-        if (last) v.next();
+        __syncwarp();
+        phase[STREAM] ^= 1;
+        v[STREAM].next();
+        if (!two) v[STREAM].next();
+    }
+    template <int STREAM>
+    __device__ __forceinline__ bool unit(bool two, int done, int units) {
+        if (done == units || !__all_sync(0xffffffffu, has_come(&c.small->p_full[STREAM], phase[STREAM]))) return false;
+        values<STREAM>(two, done % kRun == 0);
+        if (done + 1 < units && !dead) scores<STREAM>(two, true);
+        look<STREAM>();
+        return true;
+    }
+    // Whether the next unit's tiles are there, asked while products run and not when they are needed.
+    template <int STREAM>
+    __device__ __forceinline__ void look() {
+        k_here[STREAM] = __all_sync(0xffffffffu, has_come(&c.small->k_full[k[STREAM].slot], k[STREAM].phase));
+        v_here[STREAM] = __all_sync(0xffffffffu, has_come(&c.small->v_full[v[STREAM].slot], v[STREAM].phase));
     }
     __device__ __forceinline__ void piece(const PrefixPiece& p) {
         const bool two = p.two;
-        const int units = (p.to - p.from) * (two ? 2 : 1);
+        const int n = p.to - p.from, n0 = two ? n : (n + 1) >> 1, n1 = two ? n : n >> 1;
         wait(&c.small->q_full[0], q_phase);
         wait(&c.small->q_full[1], q_phase);
         q_phase ^= 1;
-        for (int u = 0; u < 2 && u < units && !dead; ++u) {
-            keys_of(u, two);
-            scores(u, two);
+        Ring<kKeySlots> k_begin = k[0];
+        Ring<kValueSlots> v_begin = v[0];
+        if (!two) {                                        // the second stream's first tile is the second
+            k[1].next();
+            v[1].next();
         }
-        for (int u = 0; u < units && !dead; ++u) {
-            const bool more = u + 2 < units;
-            if (more) keys_of(u + 2, two);
-            values(u, two);
-            if (more && !dead) scores(u + 2, two);
+        k_here[0] = k_here[1] = v_here[0] = v_here[1] = false;
+        if (!dead) scores<0>(two, false);
+        if (n1 > 0 && !dead) scores<1>(two, false);
+        int d0 = 0, d1 = 0;
+        long long t0 = 0;
+        for (uint32_t idle = 0; (d0 < n0 || d1 < n1) && !dead;) {
+            const bool a = unit<0>(two, d0, n0);
+            d0 += a;
+            const bool b = !dead && unit<1>(two, d1, n1);
+            d1 += b;
+            if (a || b) {
+                idle = 0;
+            } else if ((++idle & 15u) == 0) {              // as in wait_up_to
+                if (idle == 16) t0 = clock64();
+                dead = __any_sync(0xffffffffu, clock64() - t0 > 2000ll * c.plan.stall.wait_us);
+            }
         }
+        k_begin.skip(n);
+        v_begin.skip(n);
+        k[0] = k[1] = k_begin;
+        v[0] = v[1] = v_begin;
     }
     // Every product issued has ended, whether or not a wait gave up before, so that TMEM may go.
     __device__ __forceinline__ void finish() {
@@ -834,10 +915,10 @@ struct Softmax {
                 loaded16(now + 16);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float most = now[16 * j];
+                    float some[5];
 #pragma unroll
-                    for (int x = 1; x < 15; x += 2) most = fmaxf(fmaxf(most, now[16 * j + x]), now[16 * j + x + 1]);
-                    most = fmaxf(most, now[16 * j + 15]);
+                    for (int x = 0; x < 5; ++x) some[x] = max3(now[16 * j + 3 * x], now[16 * j + 3 * x + 1], now[16 * j + 3 * x + 2]);
+                    const float most = fmaxf(max3(some[0], some[1], some[2]), max3(some[3], some[4], now[16 * j + 15]));
                     const float x = mine >> (2 * h + j) & 1 ? __fmul_rn(most, factor * (j ? st.z : st.x)) : -INFINITY;
                     xs[2 * h + j] = x;
                     top = fmaxf(top, x);
@@ -907,7 +988,7 @@ struct Softmax {
             }
             tc::tmem_wait_st();
             tc::tc_fence_before();
-            tc::mbar_arrive(&c.small->p_full[stream]);
+            arrive_warp(&c.small->p_full[stream]);
             s_phase ^= 1;
             scale.next();
             if (!two && 2 * k + stream + 1 < tiles) scale.next();
@@ -1008,24 +1089,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kKeySlots; ++i) {
             tc::mbar_init(&small->k_full[i], 1);
-            tc::mbar_init(&small->k_empty[i], 1);
+            tc::mbar_init(&small->k_empty[i], 2);
         }
         for (int i = 0; i < kRawSlots; ++i) {
             tc::mbar_init(&small->raw_full[i], 1);
-            tc::mbar_init(&small->raw_empty[i], kWarpgroup);
+            tc::mbar_init(&small->raw_empty[i], kWarpgroup / 32);
         }
         for (int i = 0; i < kValueSlots; ++i) {
-            tc::mbar_init(&small->v_full[i], kWarpgroup);
-            tc::mbar_init(&small->v_empty[i], 1);
+            tc::mbar_init(&small->v_full[i], kWarpgroup / 32);
+            tc::mbar_init(&small->v_empty[i], 2);
         }
         for (int i = 0; i < kScaleSlots; ++i) tc::mbar_init(&small->scale_full[i], 1);
         for (int i = 0; i < kPieceSlots; ++i) {
             tc::mbar_init(&small->piece_full[i], 1);
-            tc::mbar_init(&small->piece_empty[i], 32 * kPlannerWarp);   // every thread of the roles before the planner
+            tc::mbar_init(&small->piece_empty[i], kPlannerWarp);   // the warps of the roles before the planner
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&small->s_full[i], 1);
-            tc::mbar_init(&small->p_full[i], kStream);
+            tc::mbar_init(&small->p_full[i], kStream / 32);
             tc::mbar_init(&small->o_done[i], 1);
             tc::mbar_init(&small->q_full[i], 1);
         }

@@ -33,7 +33,7 @@ size_t cache_attention_shared_workspace_bytes(const CacheAttention& a, int num_s
     if (attention_prefix_tc_takes(a, true)) pieces = most(pieces, attention_prefix_tc_workspace_bytes(a, num_sms));
     if (attention_tc_takes(a, true)) {
         const attn::Plan plan = attention_tc_plan(a);
-        pieces = most(pieces, attention_piece_bytes(attention_tc_grid(a, plan, num_sms), plan.stored, 128));
+        pieces = most(pieces, attention_piece_bytes(attention_tc_grid(a, plan, num_sms, attn::kRest), plan.stored, 128));
     }
     // (a pool without pages holds nothing to share)
     return most(carry_bytes(a) + pieces, cache_attention_workspace_bytes(a, num_sms));
