@@ -109,7 +109,7 @@ def _declare(lib):
     lib.kda_cache_fork.restype = i32
     lib.kda_cache_compact.argtypes = [vp, vp, i64, vp, vp, i32, i32, vp, vp, vp, vp, vp]
     lib.kda_cache_compact.restype = i32
-    lib.kda_cache_pages_workspace_size.argtypes = [i64]
+    lib.kda_cache_pages_workspace_size.argtypes = [i64, i32]
     lib.kda_cache_pages_workspace_size.restype = sz
     lib.kda_static_workspace_status.argtypes = [vp, vp]
     lib.kda_static_workspace_status.restype = i32

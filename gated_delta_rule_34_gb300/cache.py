@@ -373,8 +373,8 @@ def cache_copy(cache: PagedCache, src, dst) -> PagedCache:
     _not_understood("cache_copy")
 
 
-def cache_pages_workspace_size(n_pages: int) -> int:
-    return int(lib().kda_cache_pages_workspace_size(n_pages))
+def cache_pages_workspace_size(n_pages: int, n_rows: int) -> int:
+    return int(lib().kda_cache_pages_workspace_size(n_pages, n_rows))
 
 
 def cache_resize(refs, block_table, rows, tokens, page: int, missing=None, workspace=None):

@@ -432,7 +432,7 @@ PyObject* cache_resize(PyObject*, PyObject* const* arg, Py_ssize_t n_args) {
     if (!integer32(arg[4], page)) return nullptr;
     List missing;
     Workspace ws;
-    if (!missing.read(arg[5], 1, index, *rows) || !ws.read(arg[6], pages_workspace_entry(table.n_pages), index, *rows))
+    if (!missing.read(arg[5], 1, index, *rows) || !ws.read(arg[6], pages_workspace_entry(table.n_pages, (int)table.table->size(0)), index, *rows))
         Py_RETURN_NONE;
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(index).stream();
     kda_status status;
@@ -463,7 +463,7 @@ PyObject* cache_fork(PyObject*, PyObject* const* arg, Py_ssize_t n_args) {
     List from, to, missing;
     Workspace ws;
     if (!from.read(arg[6], src->numel(), index, *src) || !to.read(arg[7], src->numel(), index, *src) ||
-        !missing.read(arg[8], 1, index, *src) || !ws.read(arg[9], pages_workspace_entry(table.n_pages), index, *src))
+        !missing.read(arg[8], 1, index, *src) || !ws.read(arg[9], pages_workspace_entry(table.n_pages, (int)table.table->size(0)), index, *src))
         Py_RETURN_NONE;
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(index).stream();
     kda_status status;

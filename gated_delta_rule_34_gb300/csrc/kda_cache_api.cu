@@ -378,8 +378,8 @@ static kda_status make_pages(kda::CachePages& p, int32_t* refs, int64_t n_pages,
     return KDA_OK;
 }
 
-size_t kda_cache_pages_workspace_size(int64_t n_pages) {
-    return n_pages < 0 || n_pages > INT32_MAX ? 0 : kda::cache_pages_workspace_bytes(n_pages);
+size_t kda_cache_pages_workspace_size(int64_t n_pages, int n_rows) {
+    return n_pages < 0 || n_pages > INT32_MAX || n_rows < 0 ? 0 : kda::cache_pages_workspace_bytes(n_pages, n_rows);
 }
 
 kda_status kda_cache_copy(void* k_codes, void* v_codes, float* k_scale, float* v_scale, const int32_t* src,
@@ -387,7 +387,8 @@ kda_status kda_cache_copy(void* k_codes, void* v_codes, float* k_scale, float* v
     KDA_REQUIRE(n >= 0, KDA_ERR_INVALID_ARG, "bad size n=%d", n);
     const kda_status st = check_pool(H_kv, d, n_pages, page, 0);
     if (st != KDA_OK) return st;
-    KDA_REQUIRE((int64_t)n * H_kv <= INT32_MAX / 16, KDA_ERR_UNSUPPORTED,
+    // (16 bytes a thread, 32 KB a work)
+    KDA_REQUIRE((int64_t)n * (((int64_t)H_kv * d * page) / 16384 + 1) <= INT32_MAX, KDA_ERR_UNSUPPORTED,
                 "too many pages and heads for one call (%d pages, %d heads)", n, H_kv);
     if (n == 0 || n_pages == 0) return ok();
     KDA_POINTER(k_codes, 16);
@@ -396,7 +397,8 @@ kda_status kda_cache_copy(void* k_codes, void* v_codes, float* k_scale, float* v
     KDA_POINTER(v_scale, 4);
     KDA_POINTER(src, 4);
     KDA_POINTER(dst, 4);
-    return launched(kda::run_cache_copy(k_codes, v_codes, k_scale, v_scale, src, dst, n, H_kv, d, n_pages, page, stream),
+    return launched(kda::run_cache_copy(k_codes, v_codes, k_scale, v_scale, src, dst, n, H_kv, d, n_pages, page, stream,
+                                        sm_count()),
                     "kda_cache_copy launch");
 }
 
@@ -412,7 +414,7 @@ kda_status kda_cache_resize(int32_t* refs, int64_t n_pages, int32_t* block_table
     }
     if (n_rows > 0 && table_pages > 0) KDA_POINTER(block_table, 4);
     if (n_pages > 0) KDA_POINTER(refs, 4);
-    st = check_workspace(kda::cache_pages_workspace_bytes(n_pages), workspace, workspace_bytes);
+    st = check_workspace(kda::cache_pages_workspace_bytes(n_pages, n_rows), workspace, workspace_bytes);
     if (st != KDA_OK) return st;
     if (!missing && (n == 0 || n_rows == 0 || table_pages == 0)) return ok();
     return launched(kda::run_cache_resize(p, rows, tokens, workspace, stream), "kda_cache_resize launch");
@@ -434,7 +436,7 @@ kda_status kda_cache_fork(int32_t* refs, int64_t n_pages, int32_t* block_table, 
     if (n_rows > 0) KDA_POINTER(lengths, 4);
     if (n_rows > 0 && table_pages > 0) KDA_POINTER(block_table, 4);
     if (n_pages > 0) KDA_POINTER(refs, 4);
-    st = check_workspace(kda::cache_pages_workspace_bytes(n_pages), workspace, workspace_bytes);
+    st = check_workspace(kda::cache_pages_workspace_bytes(n_pages, n_rows), workspace, workspace_bytes);
     if (st != KDA_OK) return st;
     if (!missing && n == 0) return ok();
     return launched(kda::run_cache_fork(p, lengths, src, dst, from_pages, to_pages, workspace, stream),

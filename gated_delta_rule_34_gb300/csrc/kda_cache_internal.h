@@ -84,7 +84,7 @@ struct CachePages {
     int n;                     // rows, or pairs of rows, that the call names
 };
 int cache_pages_most_rows();
-size_t cache_pages_workspace_bytes(int64_t n_pages);
+size_t cache_pages_workspace_bytes(int64_t n_pages, int n_rows);
 cudaError_t run_cache_resize(const CachePages& p, const int32_t* rows, const int32_t* tokens, void* workspace,
                              cudaStream_t stream);
 cudaError_t run_cache_fork(const CachePages& p, int32_t* lengths, const int32_t* src, const int32_t* dst, int32_t* from,
@@ -93,6 +93,7 @@ cudaError_t run_cache_compact(const int32_t* refs, int32_t* refs_out, int64_t n_
                               int32_t* table_out, int64_t entries, int32_t* map, int32_t* from, int32_t* to, int32_t* held,
                               cudaStream_t stream);
 cudaError_t run_cache_copy(void* k_codes, void* v_codes, float* k_scale, float* v_scale, const int32_t* src,
-                           const int32_t* dst, int n, int heads, int d, int64_t n_pages, int page, cudaStream_t stream);
+                           const int32_t* dst, int n, int heads, int d, int64_t n_pages, int page, cudaStream_t stream,
+                           int num_sms);
 
 }  // namespace kda

@@ -552,7 +552,7 @@ size_t kda_cache_attention_shared_workspace_size(int B, int T_q, int H_q, int H_
  * can be captured.  Layers that share a block table share refs; their pools' pages are copied layer by layer, by
  * kda_cache_copy with the lists of pages that kda_cache_fork and kda_cache_compact write.  Pages are taken lowest first in the order
  * of what asks, so results do not depend on timing.  An entry outside [0, n_pages) holds nothing.
- *   workspace  kda_cache_pages_workspace_size(n_pages) bytes, 256-byte aligned; contents on entry are ignored
+ *   workspace  kda_cache_pages_workspace_size() bytes, 256-byte aligned; contents on entry are ignored
  *   missing    nullable; device int32 [1] (written): pages that were wanted and not there
  * All tables, lists and counts are dense and apart from one another unless stated; at most 65536 rows or pairs a call,
  * and n * table_pages below 2^31.
@@ -597,7 +597,7 @@ kda_status kda_cache_fork(int32_t *refs, int64_t n_pages, int32_t *block_table, 
                           size_t workspace_bytes, cudaStream_t stream);
 
 /* Workspace bytes of kda_cache_resize and kda_cache_fork (0 for sizes they do not take). */
-size_t kda_cache_pages_workspace_size(int64_t n_pages);
+size_t kda_cache_pages_workspace_size(int64_t n_pages, int n_rows);
 
 /*
  * kda_cache_compact -- brings the held pages (refs > 0), `held` in number, to [0, held): the k-th of them from page

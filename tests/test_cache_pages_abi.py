@@ -22,7 +22,7 @@ def L():
     (dict(kc=None), INVALID), (dict(vc=P + 8), INVALID), (dict(ksc=P + 2), INVALID), (dict(vsc=None), INVALID),
     (dict(src=None), INVALID), (dict(dst=P + 1), INVALID), (dict(n=-1), INVALID), (dict(h=0), INVALID),
     (dict(d=24), UNSUPPORTED), (dict(d=144), UNSUPPORTED), (dict(page=48), UNSUPPORTED), (dict(pages=-1), INVALID),
-    (dict(pages=1 << 31), UNSUPPORTED), (dict(n=1 << 28, h=8), UNSUPPORTED), (dict(n=0), OK), (dict(n=0, src=None), OK),
+    (dict(pages=1 << 31), UNSUPPORTED), (dict(n=1 << 29, h=8), UNSUPPORTED), (dict(n=0), OK), (dict(n=0, src=None), OK),
     (dict(pages=0, kc=None), OK),
 ])
 def test_copy_refusals(L, kw, status):
@@ -42,7 +42,7 @@ ROWS = [(dict(refs=None), INVALID), (dict(table=P + 2), INVALID), (dict(pages=-1
     (dict(wide=0, missing=None, table=None), OK), (dict(n_rows=0, missing=None, table=None), OK),
 ])
 def test_resize_refusals(L, kw, status):
-    a = dict(refs=P, pages=100, table=P, n_rows=4, wide=8, rows=P, tokens=P, n=3, page=64, missing=P, ws=P, ws_bytes=512)
+    a = dict(refs=P, pages=100, table=P, n_rows=4, wide=8, rows=P, tokens=P, n=3, page=64, missing=P, ws=P, ws_bytes=1 << 19)
     a.update(kw)
     assert L.kda_cache_resize(*a.values(), None) == status
 
@@ -53,7 +53,7 @@ def test_resize_refusals(L, kw, status):
 ])
 def test_fork_refusals(L, kw, status):
     a = dict(refs=P, pages=100, table=P, n_rows=4, wide=8, lengths=P, src=P, dst=P, n=3, page=64, frm=P, to=P, missing=P,
-             ws=P, ws_bytes=512)
+             ws=P, ws_bytes=1 << 19)
     a.update(kw)
     assert L.kda_cache_fork(*a.values(), None) == status
 
@@ -95,10 +95,11 @@ def test_shared_workspace_size(L):
 
 
 def test_workspace_size(L):
-    assert kda.cache_pages_workspace_size(0) == 0
-    assert kda.cache_pages_workspace_size(1) == 256
-    assert kda.cache_pages_workspace_size(1000) == 4096
-    assert kda.cache_pages_workspace_size(-1) == kda.cache_pages_workspace_size(1 << 31) == 0
+    size = kda.cache_pages_workspace_size
+    assert size(0, 0) >= 4 * 65536 and size(0, 0) % 256 == 0   # (places of 65536 units of rows)
+    assert size(1000, 24) >= size(0, 0) + 4096 - 256
+    assert size((1 << 31) - 1, 5) > 1 << 33
+    assert size(-1, 4) == size(1 << 31, 4) == size(4, -1) == 0
 
 
 @pytest.mark.parametrize("name", ["cache_copy", "cache_resize", "cache_fork", "cache_compact", "cache_attention_shared"])

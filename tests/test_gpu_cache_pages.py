@@ -103,7 +103,8 @@ def scattered(rng, n_pages, n_rows, wide, fill, share=0.3):
     return refs, table
 
 
-SIZES = [(1, 1, 1), (7, 3, 5), (40, 9, 31), (100, 33, 32), (1000, 20, 257), (5000, 70, 300), (40001, 130, 300), (9000, 1, 9000), (300, 9001, 1)]
+# (lists of more than 1,024 rows go another way, and so do warps with more than 1,024 pages)
+SIZES = [(400_000, 6, 40), (1, 1, 1), (7, 3, 5), (40, 9, 31), (100, 33, 32), (1000, 20, 257), (5000, 70, 300), (40001, 130, 300), (9000, 1, 9000), (300, 9001, 1)]
 
 
 @pytest.mark.parametrize("n_pages, n_rows, wide", SIZES)
@@ -115,7 +116,7 @@ def test_resize(n_pages, n_rows, wide, page):
     plain = Plain(refs, table, page)
     t_refs, t_table = ints(refs), ints(table)
     for step in range(3):
-        n = min(rng.randint(1, n_rows + 2), 300)
+        n = rng.randint(1, n_rows + 2) if n_rows > 1024 else min(rng.randint(1, n_rows + 2), 300)
         rows = [rng.randint(-1, n_rows) for _ in range(n)]  # outside, and some of them twice
         tokens = [rng.choice([0, -5, 1, page, page + 1, rng.randint(0, wide * page + 40), 2 ** 31 - 1]) for _ in range(n)]
         missing = kda.cache_resize(t_refs, t_table, ints(rows), ints(tokens), page)
@@ -137,7 +138,7 @@ def test_resize_of_counts_that_do_not_match():
     assert refs.tolist() == [0, 0, 2] and table.tolist() == [[-1, -1, -1], [2, -1, -1]]
 
 
-@pytest.mark.parametrize("n_pages, n_rows, wide", [(12, 6, 3), (100, 33, 32), (3000, 70, 300), (300, 600, 2), (50, 8, 1)])
+@pytest.mark.parametrize("n_pages, n_rows, wide", [(12, 6, 3), (100, 33, 32), (3000, 70, 300), (300, 600, 2), (50, 8, 1), (4000, 5000, 3), (9000, 3000, 17)])
 def test_fork(n_pages, n_rows, wide):
     page = 32
     rng = random.Random(n_pages)
