@@ -566,8 +566,9 @@ struct Converter {
 // ------------------------------------------------------------------ issuer
 // A unit is a stream's tile: O += W V of it, then, once these products have read W, S of the stream's next tile,
 // which goes where W lies.  Both streams' units are taken as their weights come, each to its end: so one stream's
-// products run under the other's softmax, and not both under neither.  (An issuer a stream: both did the same at the
-// same time, 218 us for 256 sequences behind 32,768 tokens against 206.)
+// products run under the other's softmax, and not both under neither.  (An issuer a stream, or one that takes whatever products are
+// ready: the streams fall into step, both softmaxes at once and then all products; 23 to 34 us more for 256 sequences behind
+// 32,768 tokens.)
 struct Issuer {
     Cta c;
     Ring<kKeySlots> k[2];                  // of each stream's next unit
@@ -701,6 +702,7 @@ struct Issuer {
 // Whether any of the 64 threads at barrier `id` says yes.
 __device__ __forceinline__ bool vote_rows(bool yes, uint32_t id) {
     uint32_t r;
+    __syncwarp();
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
         "bar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
@@ -721,6 +723,7 @@ struct Softmax {
 
     __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
         if (!bad && !__all_sync(0xffffffffu, wait_up_to(bar, parity, c.plan.stall.wait_us))) bad = true;
+        __syncwarp();                                      // (what follows is done by whole warps)
     }
 
     // The stream's 128 queries: eight threads a row, 16 channels each.  (A loop, the next row's loads under this one's
@@ -1238,7 +1241,14 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-bool attention_prefix_tc_takes(const CacheAttention& a, bool bf16) { return bf16; }
+// Rows times tokens, over all heads, up to which the kernels for few rows are faster: a call of this one has 18 us before its first
+// product and after its last.  Measured both ways with 8 heads of keys (us, these kernels and those): d = 128, 512 tokens under 128
+// rows a head 22.6 and 16.8, under 1,024 44.6 and 46.7; 2,048 under 128 28.9 and 26.9, under 256 33.4 and 37.6; 8,192 under 32 29.7
+// and 30.0; 32,768 under 8 41.8 and 37.9, under 32 43.4 and 54.5; d = 64, 2,048 under 256 28.4 and 29.2, 8,192 under 32 27.5 and 22.7,
+// under 128 29.5 and 37.5.
+bool attention_prefix_tc_takes(const CacheAttention& a, bool bf16) {
+    return bf16 && (double)a.B * a.T_q * a.H_q * a.prefix_pages * (1 << a.page_shift) > 2097152.0;
+}
 
 size_t attention_prefix_tc_workspace_bytes(const CacheAttention& a, int num_sms) {
     const size_t grid = prefix_grid(a, num_sms), D = a.d <= 64 ? 64 : 128;
