@@ -643,18 +643,26 @@ struct Issuer {
         v[STREAM].next();
         if (!two) v[STREAM].next();
     }
+    // `done` units of this stream are, and `others` of the other's.  A stream is at most one unit ahead, and the second not at all
+    // where it has the odd tiles: then the slots that the unit's tiles, and all tiles before them, lie in were given back by products
+    // already issued, so that no wait here is for products that come after it, and a slot's barrier is at most one phase behind.
     template <int STREAM>
-    __device__ __forceinline__ bool unit(bool two, int done, int units) {
-        if (done == units || !__all_sync(0xffffffffu, has_come(&c.small->p_full[STREAM], phase[STREAM]))) return false;
+    static __device__ __forceinline__ bool in_turn(bool two, int done, int others) { return done <= others + (STREAM == 0 || two); }
+    template <int STREAM>
+    __device__ __forceinline__ bool unit(bool two, int done, int units, int others) {
+        if (done == units || !in_turn<STREAM>(two, done, others) ||
+            !__all_sync(0xffffffffu, has_come(&c.small->p_full[STREAM], phase[STREAM])))
+            return false;
         values<STREAM>(two, done % kRun == 0);
         if (done + 1 < units && !dead) scores<STREAM>(two, true);
-        look<STREAM>();
+        look<STREAM>(two);
         return true;
     }
-    // Whether the next unit's tiles are there, asked while products run and not when they are needed.
+    // Whether the next unit's tiles are there, asked while products run and not when they are needed.  (Keys where this stream
+    // has had every tile: what lay in the slot before may else be the other's, and still to come.)
     template <int STREAM>
-    __device__ __forceinline__ void look() {
-        k_here[STREAM] = __all_sync(0xffffffffu, has_come(&c.small->k_full[k[STREAM].slot], k[STREAM].phase));
+    __device__ __forceinline__ void look(bool two) {
+        k_here[STREAM] = two && __all_sync(0xffffffffu, has_come(&c.small->k_full[k[STREAM].slot], k[STREAM].phase));
         v_here[STREAM] = __all_sync(0xffffffffu, has_come(&c.small->v_full[v[STREAM].slot], v[STREAM].phase));
     }
     __device__ __forceinline__ void piece(const PrefixPiece& p) {
@@ -675,9 +683,9 @@ struct Issuer {
         int d0 = 0, d1 = 0;
         long long t0 = 0;
         for (uint32_t idle = 0; (d0 < n0 || d1 < n1) && !dead;) {
-            const bool a = unit<0>(two, d0, n0);
+            const bool a = unit<0>(two, d0, n0, d1);
             d0 += a;
-            const bool b = !dead && unit<1>(two, d1, n1);
+            const bool b = !dead && unit<1>(two, d1, n1, d0);
             d1 += b;
             if (a || b) {
                 idle = 0;

@@ -643,8 +643,9 @@ kda_status kda_selftest_bounded_wait(uint32_t *status, int arrive, cudaStream_t 
 
 /*
  * kda_selftest_attention_stall -- the same for kda_cache_attention with more
- * than 16 bf16 rows a head of more than 64 channels.  While set, every later
- * such call made on this thread stops short in each CTA: its loaders after
+ * than 16 bf16 rows a head of more than 64 channels, and for the prefixes of a
+ * kda_cache_attention_shared of many bf16 rows.  While set, every later such
+ * call made on this thread stops short in each CTA: its loaders after
  * `loads` tiles of 128 tokens, its products after `tiles` tiles; its waits
  * then run out after wait_us microseconds (1 to 2,000,000) instead of 2 s.
  * The call returns, with NaN where what is missing was needed, and the context

@@ -1,6 +1,7 @@
 """Attention of groups of sequences over a prefix that they share, against each sequence's attention over its own row in 64 bits."""
 import math
 import random
+import time
 
 import pytest
 import torch
@@ -10,6 +11,9 @@ import gated_delta_rule_34_gb300 as kda
 pytestmark = pytest.mark.gpu
 
 BF16, F32, F64 = torch.bfloat16, torch.float32, torch.float64
+# Which kernels a bf16 call runs follows from its sizes, the prefix table's among them: "wide" fills that up with entries that hold
+# nothing, until the kernel for many rows takes the call.
+KINDS = [BF16, "wide", F32]
 HALF_STEP = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
 DEV = "cuda"
 
@@ -25,6 +29,9 @@ class Case:
     def __init__(self, seed, T_q, hq, hk, d, page, dtype, groups, before=(), after=(), spread=3, extra_pages=0):
         g = torch.Generator().manual_seed(seed)
         shared = [s for s, _ in groups]
+        rows = sum(len(own) for _, own in groups) + len(before) + len(after)
+        wide_extra = 2 ** 21 // max(1, rows * T_q * hq * page) + 1 if dtype == "wide" else 0
+        dtype = BF16 if dtype == "wide" else dtype
         lengths, cu, of = list(before), [len(before)], [None] * len(before)
         for i, (s, own) in enumerate(groups):
             lengths += [0 if n is None else max(0, s + n) for n in own]
@@ -35,7 +42,7 @@ class Case:
         pages = lambda n: -(-n // page)  # noqa: E731
         n_pages = sum(pages(s) for s in shared) + sum(pages(n) for n in lengths) + 2
         ids = iter(torch.randperm(n_pages, generator=g).tolist())
-        wide_prefix = max([pages(s) for s in shared] + [0]) + extra_pages
+        wide_prefix = max([pages(s) for s in shared] + [0]) + extra_pages + wide_extra
         wide = max([pages(n) for n in lengths] + [1]) + extra_pages
         prefix = [[next(ids) for _ in range(pages(s))] for s in shared]
         rows = []
@@ -72,23 +79,23 @@ class Case:
         numbers, 2^-21), below fp16's normal range 2^-31 of the row's reference a token; exponentials 2^-21, again 2^-20 for the joining's
         factors; sums 2^-24 (n / 16 + 64); products of 64 tiles cut off by at most 512 steps 2^-23 of the sum, 2^-14.  All of
         that twice, for the division; half a step of the output's type."""
-        q, d = self.q.cpu().double(), self.d
+        q, d = self.q.double(), self.d
         scale = 1 / math.sqrt(d) if scale is None else scale
         B, t_q, hq, _ = q.shape
         hk = self.pool.k.shape[1]
-        values = {n: getattr(self.pool, n).cpu().float().double() * getattr(self.pool, n + "_scale").cpu().double()[:, :, None, None] for n in "kv"}
+        values = {n: getattr(self.pool, n).float().double() * getattr(self.pool, n + "_scale").double()[:, :, None, None] for n in "kv"}
         worst = 0.0
         for b in range(B):
             length = min(int(self.lengths[b]), self.table.shape[1] * self.page)
-            at = torch.arange(max(length, 0))
-            ids = self.table[b].cpu().long()[at // self.page] if length > 0 else at
+            at = torch.arange(max(length, 0), device=DEV)
+            ids = self.table[b].long()[at // self.page] if length > 0 else at
             held = (ids >= 0) & (ids < values["k"].shape[0])
             at, ids = at[held], ids[held]
             for h in range(hk):
                 rows = slice(h * hq // hk, (h + 1) * hq // hk)
                 qq = q[b, :, rows]                         # [t_q, group, d]
                 k, v = (values[n][ids, h, at % self.page] for n in "kv")
-                unseen = at > (length - t_q + torch.arange(t_q))[:, None]
+                unseen = at > (length - t_q + torch.arange(t_q, device=DEV))[:, None]
                 k, v = k.nan_to_num(0.0), v.nan_to_num(0.0)
                 s = scale * torch.einsum("igd,td->igt", qq, k)
                 s = s.masked_fill(unseen[:, None], -math.inf)
@@ -96,16 +103,16 @@ class Case:
                 w = torch.exp(s - want_lse[..., None]).nan_to_num(0.0)
                 want = w @ v
                 weight = w @ v.abs()
-                size = (abs(scale) * torch.einsum("igd,td->igt", qq.abs(), k.abs())).amax(-1) if len(at) else torch.zeros(t_q, qq.shape[1], dtype=F64)
+                size = (abs(scale) * torch.einsum("igd,td->igt", qq.abs(), k.abs())).amax(-1) if len(at) else torch.zeros(t_q, qq.shape[1], dtype=F64, device=DEV)
                 lost = abs(scale) * 2.0 ** -22 * qq.abs().amax(-1) * (k.abs().sum(-1).max() if len(at) else 0.0)
-                vs = getattr(self.pool, "v_scale").cpu().double()[ids, h] if len(at) else torch.zeros(0, dtype=F64)
-                floor = ((w * vs).amax(-1) if len(at) else torch.zeros_like(size))[..., None] * ((v.abs() / vs[:, None]).sum(0) if len(at) else torch.zeros(d, dtype=F64))
+                vs = self.pool.v_scale.double()[ids, h] if len(at) else torch.zeros(0, dtype=F64, device=DEV)
+                floor = ((w * vs).amax(-1) if len(at) else torch.zeros_like(size))[..., None] * ((v.abs() / vs[:, None]).sum(0) if len(at) else torch.zeros(d, dtype=F64, device=DEV))
                 score = 2.0 ** -24 * (2 * d + 8) * size + lost
                 n = max(length, 1)
                 step = (2.0 ** -11 if self.q.dtype == BF16 else 2.0 ** -21) + 2.0 ** -20 + 2.0 ** -24 * (n / 16 + 64) + \
                     (2.0 ** -14 if self.q.dtype == BF16 else 0.0)
                 tol = HALF_STEP[self.q.dtype] * want.abs() + 2 * (score + step)[..., None] * weight + 2.0 ** -31 * floor + 1e-30
-                got, got_lse = o[b, :, rows].cpu().double(), lse[b, :, rows].cpu().double()
+                got, got_lse = o[b, :, rows].double(), lse[b, :, rows].double()
                 empty = want_lse == -math.inf
                 assert not bool(got[empty].any()) and bool((got_lse[empty] == -math.inf).all())
                 err = ((got - want).abs() / tol)[~empty]
@@ -139,13 +146,13 @@ SIZES = [  # T_q, hq, hk, d, page, groups
 ]
 
 
-@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dtype", KINDS)
 @pytest.mark.parametrize("T_q, hq, hk, d, page, groups", SIZES)
 def test_sizes(dtype, T_q, hq, hk, d, page, groups):
     both(Case(d + hq, T_q, hq, hk, d, page, dtype, groups))
 
 
-@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dtype", KINDS)
 @pytest.mark.parametrize("T_q, group, d", [(1, 2, 64), (1, 8, 128), (3, 4, 128), (12, 3, 80)])
 def test_places_not_in_use_and_sequences_that_do_not_see_all(dtype, T_q, group, d):
     """Lengths of 0 (their rows of the table hold nothing), shorter than the prefix, the newest query's token the prefix's last."""
@@ -153,20 +160,44 @@ def test_places_not_in_use_and_sequences_that_do_not_see_all(dtype, T_q, group, 
     both(Case(1, T_q, 2 * group, 2, d, 32, dtype, groups, before=[5, 0, 100], after=[0, 33]))
 
 
-@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dtype", KINDS)
 def test_groups_of_all_sizes(dtype):
     groups = [(32 * (1 + i % 3), [1 + (i * j) % 40 for j in range(i)]) for i in (0, 1, 2, 3, 5, 8, 13, 21)]
     both(Case(2, 1, 12, 2, 64, 32, dtype, groups, before=[40], extra_pages=3))
 
 
-@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dtype", KINDS)
 @pytest.mark.parametrize("d, hq, B", [(128, 8, 3), (64, 4, 40), (128, 32, 20), (96, 4, 130)])
 def test_long(dtype, d, hq, B):
     """Long enough to be cut many times over."""
     both(Case(3, 1, hq, 1, d, 64, dtype, [(9001, [1 + 13 * i for i in range(B)])]))
 
 
-@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("hk, group, T_q, d, page, n", [(16, 16, 16, 64, 32, 30000), (19, 8, 32, 128, 128, 26001)])
+def test_long_for_every_processor(hk, group, T_q, d, page, n):
+    """Many rows of many heads: each processor walks more tiles of one prefix than it adds up in one place."""
+    both(Case(14, T_q, hk * group, hk, d, page, BF16, [(n, [T_q, T_q + 3, T_q + 90])], spread=1))
+
+
+@pytest.mark.parametrize("slow", [slice(0, 8), slice(8, 16)])
+def test_halves_of_different_speeds(slow):
+    """Scores beyond 2^22 take a longer way: 128 of 256 rows that are worked on side by side have them, for many tiles."""
+    case = Case(18, 1, 256, 16, 64, 64, BF16, [(20000, [1 + i for i in range(16)])], spread=0)
+    case.q[slow] *= 2.0 ** 24
+    want = both(case)
+    for _ in range(20):
+        assert all(torch.equal(a, b) for a, b in zip(case.run(), want))
+
+
+@pytest.mark.parametrize("dtype", [BF16, "wide"])
+def test_prefixes_of_every_length_around_a_tile(dtype):
+    """Ends inside, at and behind a tile of 128 tokens, and inside a page; the prefix's last page whole or not."""
+    groups = [(s, [1 + (s + i) % 7 for i in range(2 + s % 3)]) for s in (1, 31, 32, 127, 128, 129, 159, 160, 161, 255, 256, 257, 288, 300)]
+    both(Case(15, 1, 8, 2, 64, 32, dtype, groups))
+    both(Case(16, 1, 4, 1, 128, 256, dtype, groups))
+
+
+@pytest.mark.parametrize("dtype", KINDS)
 @pytest.mark.parametrize("n", [3, 150])
 def test_pages_not_held(dtype, n):
     case = Case(4, 2, 4, 2, 64, 16, dtype, [(400, [2 + i % 30 for i in range(n)])])
@@ -181,23 +212,23 @@ def test_pages_not_held(dtype, n):
     assert bool((lse[1] == -math.inf).all())
 
 
-@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dtype", KINDS)
 @pytest.mark.parametrize("n", [2, 70])
 @pytest.mark.parametrize("factor", [1.0, 40.0, 1e-3])
 def test_uneven_scales(dtype, n, factor):
     """Pages whose values differ by 2^60 in size, one after another; large scores, tiny queries."""
     case = Case(5, 1, 4, 2, 64, 16, dtype, [(16 * 30, [1 + i % 40 for i in range(n)])])
     order = torch.randperm(30, generator=torch.Generator().manual_seed(1)).float().to(DEV)
-    case.pool.v_scale[case.prefix_table[0].long()] = torch.exp2(2 * order - 30)[:, None]
+    case.pool.v_scale[case.prefix_table[0, :30].long()] = torch.exp2(2 * order - 30)[:, None]
     case.q *= factor
     both(case)
-    case.pool.k_scale[case.prefix_table[0].long()] = torch.exp2(order - 15)[:, None]
+    case.pool.k_scale[case.prefix_table[0, :30].long()] = torch.exp2(order - 15)[:, None]
     both(case, scale=1e-4)
     both(case, scale=-1e-4)
     both(case, scale=0.0)
 
 
-@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dtype", KINDS)
 @pytest.mark.parametrize("n", [2, 70])
 def test_extreme_queries(dtype, n):
     """Far outside fp16's range, rows of zeros, rows without a number."""
@@ -218,7 +249,7 @@ def test_extreme_queries(dtype, n):
     assert bool(((o.float() - clean.float()).abs() <= 2.0 ** -6 * clean.float().abs().max())[~mine].all())
 
 
-@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dtype", KINDS)
 @pytest.mark.parametrize("n", [2, 70])
 def test_infinite_queries(dtype, n):
     """A channel of -inf against keys of one sign makes every score -inf: 0 and -inf.  +inf, or keys of both signs: no number."""
@@ -241,7 +272,7 @@ def test_infinite_queries(dtype, n):
     assert bool(torch.isnan(o).all()) and bool(torch.isnan(lse).all())
 
 
-@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dtype", KINDS)
 @pytest.mark.parametrize("n", [2, 70])
 def test_nan_in_the_prefix_reaches_its_channel_only(dtype, n):
     case = Case(8, 1, 4, 2, 64, 32, dtype, [(160, [1 + i % 40 for i in range(n)] + [-130])])
@@ -257,9 +288,10 @@ def test_nan_in_the_prefix_reaches_its_channel_only(dtype, n):
     assert bool(torch.isfinite(lse[:n, 0, 2:]).all()) and bool(torch.isfinite(o[n]).all())
 
 
-@pytest.mark.parametrize("dtype, T_q, d", [(BF16, 1, 64), (BF16, 2, 128), (F32, 1, 128), (BF16, 40, 80)])
+@pytest.mark.parametrize("dtype, T_q, d", [(BF16, 1, 64), (BF16, 2, 128), (F32, 1, 128), (BF16, 40, 80), ("wide", 1, 64), ("wide", 40, 80)])
 def test_strides_buffers_and_another_stream(dtype, T_q, d):
     case = Case(9, T_q, 6, 2, d, 16, dtype, [(100, [T_q + i for i in range(9)]), (33, [T_q, 50])])
+    dtype = case.q.dtype
     o, lse = both(case)
     fused = torch.full((11, T_q, 10 * d), math.nan, dtype=dtype, device=DEV)
     fused[..., : 6 * d] = case.q.flatten(2)
@@ -280,7 +312,7 @@ def test_strides_buffers_and_another_stream(dtype, T_q, d):
     assert bool((guard[:256] == 0xA5).all()) and bool((guard[256 + need:] == 0xA5).all())
 
 
-@pytest.mark.parametrize("dtype, T_q, hq, d", [(BF16, 1, 4, 64), (BF16, 1, 16, 128), (BF16, 6, 16, 128), (F32, 1, 4, 128)])
+@pytest.mark.parametrize("dtype, T_q, hq, d", [(BF16, 1, 4, 64), (BF16, 6, 16, 128), ("wide", 1, 4, 64), ("wide", 1, 16, 128), ("wide", 6, 16, 128), (F32, 1, 4, 128)])
 def test_graph_with_lengths_that_change(dtype, T_q, hq, d):
     """One captured graph, replayed as sequences grow, places come and go, groups change; two graphs with one workspace."""
     case = Case(10, T_q, hq, 2, d, 32, dtype, [(300, [T_q + 40] * 12), (64, [T_q + 60, 90])], after=[50])
@@ -336,13 +368,37 @@ def test_malformed_groups_stay_in_the_buffers():
     torch.cuda.synchronize()
 
 
+@pytest.fixture
+def stall():
+    yield kda.selftest_attention_stall
+    kda.selftest_attention_stall()
+
+
+@pytest.mark.parametrize("sequences", [40, 20])            # 160 rows a head, and 80: a stream of them, or both take one
+@pytest.mark.parametrize("loads, tiles", [(0, 1 << 24), (1, 1 << 24), (1 << 24, 0)])
+def test_bounded_waits_run_out(stall, sequences, loads, tiles):
+    """Loads that stop, or products that do, with a limit of 3 ms: the call returns without numbers, and the next is right."""
+    case = Case(17, 1, 8, 2, 64, 64, "wide", [(50000, [1 + i for i in range(sequences)])])
+    want, want_lse = case.run()
+    torch.cuda.synchronize()
+    stall(loads, tiles, 3000)
+    start = time.perf_counter()
+    o, lse = case.run()
+    torch.cuda.synchronize()
+    assert time.perf_counter() - start < 20
+    assert bool(torch.isnan(o).all()) and bool(torch.isnan(lse).all())
+    stall()
+    o, lse = case.run()
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
 def test_refusals():
     case = Case(13, 1, 4, 2, 64, 16, BF16, [(64, [5, 60, 7])])
     a = dict(q=case.q, cache=case.pool, block_table=case.table, lengths=case.lengths, prefix_table=case.prefix_table,
              prefix_lengths=case.shared, cu_groups=case.cu)
     for change, error, match in [
             (dict(prefix_lengths=ints([1, 2])), ValueError, "prefix_lengths"), (dict(cu_groups=ints([0])), ValueError, "cu_groups"),
-            (dict(prefix_table=case.prefix_table.long()), TypeError, "prefix_table"), (dict(q=case.q.half()), TypeError, ""),
+            (dict(prefix_table=case.prefix_table.long()), TypeError, "prefix_table"), (dict(q=case.q.half()), TypeError, None),
             (dict(lengths=ints([1])), ValueError, "lengths"), (dict(scale=math.inf), kda.KDAError, "finite"),
             (dict(workspace=torch.empty(256, dtype=torch.uint8, device=DEV)), kda.KDAError, "workspace"),
             (dict(prefix_table=ints([[0]] * 4), prefix_lengths=ints([1] * 4), cu_groups=ints([0, 1, 2, 3, 3])), kda.KDAError, "more groups")]:
