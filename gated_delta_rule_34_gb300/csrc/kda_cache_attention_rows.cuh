@@ -782,12 +782,18 @@ int padded_d(const CacheAttention& a) { return a.d <= 64 ? 64 : 128; }
 
 // Calls f with the shape for these queries: as many rows a warp as registers allow
 // before warps have to share tokens.  (More than 16 bf16 rows of more than 64 channels
-// are the other kernel's: attention_tc_takes.)
+// are the other kernels': attention_tc_takes.)
 template <Part P, typename T, int D, typename F>
 auto by_rows(const CacheAttention& a, F f) {
     const int64_t rows = rows_of<P>(a);
     if (rows <= 8) return f(Shape<T, D, 1, 1>{});
     if constexpr (sizeof(T) == 2 && D == 128) {
+        // The rest behind a prefix is short, and 32 rows a CTA of two warps a group have fewer starts and ends: 40 sequences of
+        // 256 rows a head, 128 tokens each, 141 us with the prefix, 161 with 16 rows a CTA, 137 with 64 of four warps; 32 rows, 42,
+        // 45 and 47.  (Four tiles of rows a warp: slower than either.)
+        if constexpr (P == kRest) {
+            if (rows > 16) return f(Shape<T, D, 2, 2>{});
+        }
         return f(Shape<T, D, 2, 1>{});
     } else {
         constexpr int MOST = sizeof(T) == 4 ? 2 : 4;

@@ -24,6 +24,12 @@ bool nothing_shared(const CacheAttention& a) { return a.n_groups == 0 || a.prefi
 
 size_t most(size_t x, size_t y) { return x > y ? x : y; }
 
+// The rest of more rows a head than 16: the tensor cores' kernel from 1,024 tokens on that the tables have room for behind a prefix.
+// Its start and end take longer than a short rest.  Measured both ways with the prefix of 512 tokens (us, this and the few-row kernel,
+// 8 heads of 128 channels): 40 sequences of 32 rows a head 63 and 42 (128 tokens), 82 and 74 (1,024), 129 and 139 (4,096); of
+// 256 rows 247 and 141, 335 and 286, 425 and 452 (2,048), 611 and 808 (4,096); 4 of 256 rows 47 and 40, 59 and 65, 107 and 112.
+bool rest_is_long(const CacheAttention& a, bool bf16) { return attention_tc_takes(a, bf16) && attn::rest_steps(a) > 1024 / attn::kStep; }
+
 }  // namespace
 
 size_t cache_attention_shared_workspace_bytes(const CacheAttention& a, int num_sms) {
@@ -31,7 +37,7 @@ size_t cache_attention_shared_workspace_bytes(const CacheAttention& a, int num_s
     // the two passes' pieces follow one another in the same place
     size_t pieces = most(attention_prefix_rows_workspace_bytes(a, num_sms), attention_rest_rows_workspace_bytes(a, num_sms));
     if (attention_prefix_tc_takes(a, true)) pieces = most(pieces, attention_prefix_tc_workspace_bytes(a, num_sms));
-    if (attention_tc_takes(a, true)) {
+    if (rest_is_long(a, true)) {
         const attn::Plan plan = attention_tc_plan(a);
         pieces = most(pieces, attention_piece_bytes(attention_tc_grid(a, plan, num_sms, attn::kRest), plan.stored, 128));
     }
@@ -48,7 +54,7 @@ cudaError_t run_cache_attention_shared(CacheAttention a, bool bf16, void* worksp
     cudaError_t e = attention_prefix_tc_takes(a, bf16) ? run_attention_prefix_tc(a, pieces, stream, num_sms)
                                                        : run_attention_prefix_rows(a, bf16, pieces, stream, num_sms);
     if (e != cudaSuccess) return e;
-    if (attention_tc_takes(a, bf16)) return run_attention_tc_rest(a, pieces, stream, num_sms);
+    if (rest_is_long(a, bf16)) return run_attention_tc_rest(a, pieces, stream, num_sms);
     return run_attention_rest_rows(a, bf16, pieces, stream, num_sms);
 }
 

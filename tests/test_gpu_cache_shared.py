@@ -26,7 +26,7 @@ class Case:
     """groups: (shared tokens, [tokens of each sequence beyond them]); negative: that many tokens short of the prefix;
     None: a place not in use."""
 
-    def __init__(self, seed, T_q, hq, hk, d, page, dtype, groups, before=(), after=(), spread=3, extra_pages=0):
+    def __init__(self, seed, T_q, hq, hk, d, page, dtype, groups, before=(), after=(), spread=3, extra_pages=0, room=0):
         g = torch.Generator().manual_seed(seed)
         shared = [s for s, _ in groups]
         rows = sum(len(own) for _, own in groups) + len(before) + len(after)
@@ -43,7 +43,7 @@ class Case:
         n_pages = sum(pages(s) for s in shared) + sum(pages(n) for n in lengths) + 2
         ids = iter(torch.randperm(n_pages, generator=g).tolist())
         wide_prefix = max([pages(s) for s in shared] + [0]) + extra_pages + wide_extra
-        wide = max([pages(n) for n in lengths] + [1]) + extra_pages
+        wide = max([pages(n) for n in lengths] + [1]) + extra_pages + pages(room)
         prefix = [[next(ids) for _ in range(pages(s))] for s in shared]
         rows = []
         for n, o in zip(lengths, of):
@@ -195,6 +195,15 @@ def test_prefixes_of_every_length_around_a_tile(dtype):
     groups = [(s, [1 + (s + i) % 7 for i in range(2 + s % 3)]) for s in (1, 31, 32, 127, 128, 129, 159, 160, 161, 255, 256, 257, 288, 300)]
     both(Case(15, 1, 8, 2, 64, 32, dtype, groups))
     both(Case(16, 1, 4, 1, 128, 256, dtype, groups))
+
+
+@pytest.mark.parametrize("T_q, hq, hk, d, page, groups", [
+    (5, 8, 2, 128, 64, [(64, [5, 6, 300]), (200, [5, 70])]), (40, 4, 2, 80, 16, [(33, [40, 75, 41]), (16, [0, None, -3])]),
+    (33, 16, 2, 128, 32, [(140, [33, 34, 2600])]), (3, 14, 2, 112, 16, [(130, [3, 90]), (16, [4] * 9), (47, [3, 1500])])])
+@pytest.mark.parametrize("room", [0, 2000])
+def test_rests_with_room_for_more(T_q, hq, hk, d, page, groups, room):
+    """Which kernel takes the rest of more than 16 rows a head follows from the room behind the prefix."""
+    both(Case(19, T_q, hq, hk, d, page, BF16, groups, before=[50], after=[0], room=room))
 
 
 @pytest.mark.parametrize("dtype", KINDS)
