@@ -387,8 +387,8 @@ kda_status kda_cache_copy(void* k_codes, void* v_codes, float* k_scale, float* v
     KDA_REQUIRE(n >= 0, KDA_ERR_INVALID_ARG, "bad size n=%d", n);
     const kda_status st = check_pool(H_kv, d, n_pages, page, 0);
     if (st != KDA_OK) return st;
-    // (16 bytes a thread, 32 KB a work)
-    KDA_REQUIRE((int64_t)n * (((int64_t)H_kv * d * page) / 16384 + 1) <= INT32_MAX, KDA_ERR_UNSUPPORTED,
+    // (32 KB a work, or some pairs: less than all threads' places below 2^31)
+    KDA_REQUIRE(((int64_t)n + 4096) * (((int64_t)H_kv * d * page) / 16384 + 1) <= INT32_MAX, KDA_ERR_UNSUPPORTED,
                 "too many pages and heads for one call (%d pages, %d heads)", n, H_kv);
     if (n == 0 || n_pages == 0) return ok();
     KDA_POINTER(k_codes, 16);

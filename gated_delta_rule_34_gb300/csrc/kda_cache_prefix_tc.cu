@@ -259,7 +259,7 @@ __device__ __forceinline__ GroupWork group_work(const CacheAttention& a, const P
     GroupWork w;
     w.range = group_range(a, g, a.B);
     w.tokens = shared_tokens(a, g, w.range);
-    w.tiles = (w.tokens + kTokens - 1) / kTokens;
+    w.tiles = (int)(((int64_t)w.tokens + kTokens - 1) / kTokens);   // (tokens may be close to 2^31)
     w.rows = (int64_t)(w.range.y - w.range.x) * a.T_q * plan.group;
     const int left = (int)(w.rows % kPair);
     w.pairs = (int)(w.rows / kPair) + (left > kRows);
@@ -439,8 +439,8 @@ struct Loader {
         const uint32_t box_bytes = box * kStep * 128;
         // Lane k < 8: step k of a tile.
         auto page_of = [&](int tile) -> int {
-            const int t = (tile * kSteps + lane) * kStep;
-            const int id = lane < kSteps && tile < p.to && t < p.tokens ? table[t >> a.page_shift] : -1;
+            const uint32_t t = (uint32_t)(tile * kSteps + lane) * kStep;
+            const int id = lane < kSteps && tile < p.to && t < (uint32_t)p.tokens ? table[t >> a.page_shift] : -1;
             return id >= 0 && id < a.n_pages ? id : -1;
         };
         auto scales_of = [&](int id, float& ks, float& vs) {

@@ -348,6 +348,39 @@ def test_graph_with_lengths_that_change(dtype, T_q, hq, d):
         case.lengths.copy_(ints(full))
 
 
+@pytest.mark.parametrize("dtype, d", [(BF16, 128), ("wide", 128), ("wide", 64), (F32, 128)])
+def test_pages_beyond_four_gigabytes(dtype, d):
+    case = Case(20, 1, 8, 4, d, 256, dtype, [(700, [1 + i for i in range(6)]), (300, [4, 9])])
+    want = both(case)
+    small, n, more = case.pool, case.pool.k.shape[0], (1 << 32) // (4 * 256 * d) + 100
+    case.pool = kda.cache_new(more + n, 4, 256, d)
+    for a, b in zip(case.pool, small):
+        a.view(torch.uint8 if a.element_size() == 1 else F32)[more:].copy_(b.view(torch.uint8 if b.element_size() == 1 else F32))
+    for t in (case.table, case.prefix_table):
+        t.copy_(torch.where(t >= 0, t + more, t))
+    assert all(torch.equal(a, b) for a, b in zip(case.run(), want))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_nearly_two_to_the_31_tokens_mostly_not_held(dtype):
+    """The tables' largest sizes, some pages here and there: as attention over these alone."""
+    g = torch.Generator(device=DEV).manual_seed(21)
+    page, wide, n = 256, (1 << 23) - 1, 7
+    pool = kda.cache_new(n, 1, page, 64)
+    randn = lambda *shape: torch.randn(shape, generator=g, device=DEV).to(dtype)  # noqa: E731
+    kda.cache_write(pool, randn(1, n * page, 1, 64), randn(1, n * page, 1, 64), torch.arange(n, device=DEV, dtype=torch.int32)[None], ints([0]))
+    places = torch.tensor([0, 12345, 4000001, 8388600, wide - 3, wide - 2, wide - 1], device=DEV)
+    table = torch.full((2, wide), -1, dtype=torch.int32, device=DEV)
+    table[:, places] = torch.arange(n, device=DEV, dtype=torch.int32)
+    q = randn(2, 1, 2, 64)
+    prefix = table[:1, : wide - 1].contiguous()
+    o, lse = kda.cache_attention_shared(q, pool, table, ints([wide * page - 100] * 2), prefix, ints([(wide - 1) * page]), ints([0, 2]), return_lse=True)
+    alone, alone_lse = kda.cache_attention(q, pool, torch.arange(n, device=DEV, dtype=torch.int32).repeat(2, 1), ints([n * page - 100] * 2),
+                                           return_lse=True)
+    assert bool(((lse - alone_lse).abs() <= 2e-5).all())
+    assert bool(((o.float() - alone.float()).abs() <= HALF_STEP[dtype] * 2 * alone.float().abs() + 2.0 ** -9 * (1 if dtype == BF16 else 2.0 ** -6)).all())
+
+
 def test_no_groups_and_nothing_shared():
     """Without groups, or with nothing to share, it is cache_attention, bit for bit."""
     case = Case(11, 2, 4, 2, 64, 16, BF16, [(0, [5, 60]), (15, [7, 8])], after=[40])
@@ -365,9 +398,10 @@ def test_no_groups_and_nothing_shared():
     assert o.shape == (0, 2, 4, 64)
 
 
-def test_malformed_groups_stay_in_the_buffers():
-    case = Case(12, 1, 4, 2, 64, 16, BF16, [(64, [5, 60, 7]), (48, [7, 8])])
-    for cu in ([-5, 3, 99], [4, 2, 1], [2 ** 31 - 1, -2 ** 31, 5], [0, 0, 0], [5, 5, 5]):
+@pytest.mark.parametrize("dtype", KINDS)
+def test_malformed_groups_stay_in_the_buffers(dtype):
+    case = Case(12, 1, 4, 2, 64, 16, dtype, [(64, [5, 60, 7]), (48, [7, 8])])
+    for cu in ([0, 5, 0], [-5, 3, 99], [4, 2, 1], [2 ** 31 - 1, -2 ** 31, 5], [0, 0, 0], [5, 5, 5]):
         case.cu.copy_(ints(cu))
         o, lse = case.run()
         torch.cuda.synchronize()
