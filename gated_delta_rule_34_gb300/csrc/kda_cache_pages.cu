@@ -687,10 +687,12 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_pairs_kernel(con
     }
 }
 
-// One cluster, or one CTA where `work` (entries and counts to look through) is a few rounds of its threads.
+// One cluster, or one CTA where `work` (entries and counts to look through) is some rounds of its threads.  Resize and fork, us, one
+// CTA and a cluster of eight: of 2,560 7.9 and 8.5; 16,896 7.8 and 8.4, 12.4 and 13.4; 24,576 9.2 and 9.0, 13.7 and 13.4; 32,768
+// 11.8 and 9.0, 16.6 and 13.5.
 template <typename... P>
 cudaError_t launch_cluster(void (*kernel)(P...), int64_t work, cudaStream_t stream, typename as_given<P>::type... args) {
-    const unsigned ctas = work <= 8 * kThreads ? 1 : kCluster;
+    const unsigned ctas = work <= 20 * kThreads ? 1 : kCluster;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
@@ -740,8 +742,10 @@ size_t cache_pages_workspace_bytes(int64_t n_pages, int n_rows) {
     return ((size_t)(n_pages + n_rows + (int64_t)kCluster * kUnits + 2) * sizeof(int32_t) + 255) / 256 * 256;
 }
 
-// Entries from which rows are walked over the whole GPU.  Two calls each of 400 rows x 1,024 entries: 71 us in one cluster.
-constexpr int64_t kWide = 32768;
+// Entries up to which one cluster walks the rows too.  A resize that takes a page a row, us in the cluster and over the whole GPU:
+// 8 rows x 64 entries 8.4 and 10.6, 128 x 256 9.3 and 10.6, 64 x 1,024 9.9 and 11.0, 400 x 1,024 25.8 and 12.4; a fork of as many
+// rows: 13.4 and 14.3, 13.9 and 15.2, 14.6 and 15.4, 22.4 and 16.7.
+constexpr int64_t kWide = 65536;
 
 template <typename... P>
 cudaError_t launch_rows(void (*kernel)(P...), const Pages& a, cudaStream_t stream, typename as_given<P>::type... args) {
@@ -778,7 +782,8 @@ cudaError_t run_cache_fork(const CachePages& p, int32_t* lengths, const int32_t*
 cudaError_t run_cache_compact(const int32_t* refs, int32_t* refs_out, int64_t n_pages, const int32_t* table,
                               int32_t* table_out, int64_t entries, int32_t* map, int32_t* from, int32_t* to, int32_t* held,
                               cudaStream_t stream) {
-    cudaError_t e = launch_cluster(compact_kernel, n_pages, stream, refs, refs_out, n_pages, map, from, to, held);
+    // (the counts are looked through three times)
+    cudaError_t e = launch_cluster(compact_kernel, 3 * n_pages, stream, refs, refs_out, n_pages, map, from, to, held);
     if (e != cudaSuccess || entries == 0) return e;
     return launch_chained(remap_kernel, (unsigned)((entries + kRemapThreads - 1) / kRemapThreads), kRemapThreads, 0, stream,
                           table, table_out, entries, map, n_pages);

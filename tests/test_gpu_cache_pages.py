@@ -104,7 +104,8 @@ def scattered(rng, n_pages, n_rows, wide, fill, share=0.3):
 
 
 # (lists of more than 1,024 rows go another way, and so do warps with more than 1,024 pages)
-SIZES = [(400_000, 6, 40), (1, 1, 1), (7, 3, 5), (40, 9, 31), (100, 33, 32), (1000, 20, 257), (5000, 70, 300), (40001, 130, 300), (9000, 1, 9000), (300, 9001, 1)]
+SIZES = [(400_000, 6, 40), (1, 1, 1), (7, 3, 5), (40, 9, 31), (100, 33, 32), (1000, 20, 257), (5000, 70, 300), (40001, 130, 300), (9000, 1, 9000), (300, 9001, 1),
+         (30000, 300, 400), (20000, 1500, 90)]           # (and calls of more than 65,536 entries)
 
 
 @pytest.mark.parametrize("n_pages, n_rows, wide", SIZES)
@@ -138,7 +139,8 @@ def test_resize_of_counts_that_do_not_match():
     assert refs.tolist() == [0, 0, 2] and table.tolist() == [[-1, -1, -1], [2, -1, -1]]
 
 
-@pytest.mark.parametrize("n_pages, n_rows, wide", [(12, 6, 3), (100, 33, 32), (3000, 70, 300), (300, 600, 2), (50, 8, 1), (4000, 5000, 3), (9000, 3000, 17)])
+@pytest.mark.parametrize("n_pages, n_rows, wide", [(12, 6, 3), (100, 33, 32), (3000, 70, 300), (300, 600, 2), (50, 8, 1), (4000, 5000, 3), (9000, 3000, 17),
+                                                   (30000, 700, 300), (60000, 3000, 60)])
 def test_fork(n_pages, n_rows, wide):
     page = 32
     rng = random.Random(n_pages)
