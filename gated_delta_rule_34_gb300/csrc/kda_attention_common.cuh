@@ -223,7 +223,7 @@ inline int64_t most_steps(const CacheAttention& a) {
 }
 
 // kRest: the steps that sequences are taken to have beyond their prefix, by the widths of the two tables (all of them,
-// where these say nothing).  Only whether items are cut goes by it.
+// where these say nothing).  Whether items are cut, and which kernel takes them, goes by it.
 inline int64_t rest_steps(const CacheAttention& a) {
     const int64_t rest = (int64_t)(a.table_pages > a.prefix_pages ? a.table_pages - a.prefix_pages : a.table_pages);
     return (rest << a.page_shift) / kStep;
@@ -419,13 +419,12 @@ size_t attention_rest_rows_workspace_bytes(const CacheAttention& a, int num_sms)
 size_t attention_prefix_rows_workspace_bytes(const CacheAttention& a, int num_sms);
 cudaError_t run_attention_rows(const CacheAttention& a, bool bf16, void* workspace, cudaStream_t stream, int num_sms);
 cudaError_t run_attention_rest_rows(const CacheAttention& a, bool bf16, void* workspace, cudaStream_t stream, int num_sms);
-cudaError_t run_attention_prefix_rows(const CacheAttention& a, bool bf16, void* workspace, cudaStream_t stream, int num_sms);
+cudaError_t run_attention_prefix_rows(const CacheAttention& a, void* workspace, cudaStream_t stream, int num_sms);   // (fp32)
 
 // What kda_selftest_attention_stall has set on this thread.
 attn::Stall attention_stall();
 
 // The kernel for the prefixes of bf16 rows (kda_cache_prefix_tc.cu).
-bool attention_prefix_tc_takes(const CacheAttention& a, bool bf16);
 size_t attention_prefix_tc_workspace_bytes(const CacheAttention& a, int num_sms);
 cudaError_t run_attention_prefix_tc(const CacheAttention& a, void* workspace, cudaStream_t stream, int num_sms);
 

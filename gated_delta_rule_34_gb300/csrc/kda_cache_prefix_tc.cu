@@ -10,7 +10,10 @@
 //   O [128 rows x d]        += W [128 x 128] V                W from TMEM; V fp16, exact, converted once for 256 rows
 //
 // What bounds it: 4 d operations a row and token on the tensor cores (q in two fp8 pieces costs what one bf16 product
-// does), with the exponentials and conversions beside them; under 128 rows, reading the codes.
+// does), with the exponentials and conversions beside them; under 128 rows, reading the codes.  256 sequences of 4 rows a head, 8
+// heads of 128, behind 32,768 tokens: 147 us, where the products take 72; the tensor pipe runs 42% of it.  A stream's products are
+// 1,024 cycles a tile, two streams' tiles take 4,150: softmax 1,770, scores 1,100 (their operands take all that shared memory gives),
+// values 700, the rest hand-overs.
 //
 // One CTA an SM takes items (group, head of keys, 256 rows): two streams of 128 rows, each with softmax threads
 // that own a row (no shuffles), so that one stream's products run under the other's softmax. Keys and values are loaded and
@@ -1248,15 +1251,6 @@ int64_t prefix_grid(const CacheAttention& a, int num_sms) {
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
-
-// Rows times tokens, over all heads, up to which the kernels for few rows are faster: a call of this one has 18 us before its first
-// product and after its last.  Measured both ways with 8 heads of keys (us, these kernels and those): d = 128, 512 tokens under 128
-// rows a head 22.6 and 16.8, under 1,024 44.6 and 46.7; 2,048 under 128 28.9 and 26.9, under 256 33.4 and 37.6; 8,192 under 32 29.7
-// and 30.0; 32,768 under 8 41.8 and 37.9, under 32 43.4 and 54.5; d = 64, 2,048 under 256 28.4 and 29.2, 8,192 under 32 27.5 and 22.7,
-// under 128 29.5 and 37.5.
-bool attention_prefix_tc_takes(const CacheAttention& a, bool bf16) {
-    return bf16 && (double)a.B * a.T_q * a.H_q * a.prefix_pages * (1 << a.page_shift) > 2097152.0;
-}
 
 size_t attention_prefix_tc_workspace_bytes(const CacheAttention& a, int num_sms) {
     const size_t grid = prefix_grid(a, num_sms), D = a.d <= 64 ? 64 : 128;

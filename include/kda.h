@@ -523,10 +523,13 @@ size_t kda_cache_attention_workspace_size(int B, int T_q, int H_q, int H_kv, int
  *                   no access leaves the buffers.
  *   block_table     device int32 [B, table_pages]: each sequence's pages from its first token on, the prefix's among
  *                   them, as kda_cache_fork leaves them.
- * A sequence whose T_q queries all see all of the prefix takes it from prefix_table and the later tokens from its row of block_table;
- * any other (a shorter one, a place not in use with length 0) takes all from its row.  So where both
- * name the same pages, the results are those of kda_cache_attention but for the order of the sums.  Other arguments,
- * roundings, rows that see nothing and waits as there.
+ * A sequence whose T_q queries all see all of the prefix may take it from prefix_table and the later tokens from its row of
+ * block_table; any other (a shorter one, a place not in use with length 0) takes all from its row, and so do all sequences where
+ * the sizes leave too little to share: B - n_groups times what the prefix table has room for, less than about 96 MB of codes. So the two
+ * must name the same pages, and the results are those of kda_cache_attention but for the order of the sums.
+ * Other arguments, rows that see nothing and waits as there, and roundings: fp32 queries as there; bf16 queries over a prefix
+ * exactly as two fp8 numbers, down to 2^-13 of their row's largest value, weights in fp16 (11 bits down to 2^-21 of the row's
+ * reference, lost below 2^-32 of it), sums of at most 64 tiles of 128 tokens as the products add them, then rounded additions.
  *   workspace  kda_cache_attention_shared_workspace_size() bytes, 256-byte aligned; contents on entry are ignored
  */
 kda_status kda_cache_attention_shared(const void *q, int64_t q_stride, const void *k_codes,

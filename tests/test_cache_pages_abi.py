@@ -79,8 +79,8 @@ def test_compact_refusals(L, kw, status):
     (dict(B=0, groups=0), OK), (dict(T_q=0), OK), (dict(lse=P + 1), INVALID),
 ])
 def test_shared_refusals(L, kw, status):
-    a = dict(q=P, qs=1024, kc=P, vc=P, ksc=P, vsc=P, table=P, wide=8, lengths=P, prefix=P, prefix_pages=4, prefix_len=P, cu=P,
-             groups=2, o=P, lse=None, B=2, T_q=1, hq=8, hkv=2, d=128, pages=100, page=64, scale=1.0, dtype=1, ws=P,
+    a = dict(q=P, qs=1024, kc=P, vc=P, ksc=P, vsc=P, table=P, wide=8, lengths=P, prefix=P, prefix_pages=4000, prefix_len=P, cu=P,
+             groups=1, o=P, lse=None, B=2, T_q=1, hq=8, hkv=2, d=128, pages=100, page=64, scale=1.0, dtype=1, ws=P,
              ws_bytes=1 << 40)
     a.update(kw)
     assert L.kda_cache_attention_shared(*a.values(), None) == status
@@ -89,8 +89,9 @@ def test_shared_refusals(L, kw, status):
 def test_shared_workspace_size(L):
     size = kda.cache_attention_shared_workspace_size
     rows = 4 * 3 * 8
-    assert size(4, 3, 8, 2, 128, 64, 10, 5, 2) >= rows * (16 + 512)
-    assert size(4, 3, 8, 2, 128, 64, 10, 0, 2) == size(4, 3, 8, 2, 128, 64, 10, 5, 0) == kda.cache_attention_workspace_size(4, 3, 8, 2, 128, 64, 10)
+    assert size(4, 3, 8, 2, 128, 64, 10, 2000, 2) >= rows * (16 + 512)
+    # nothing to share, or too little
+    assert size(4, 3, 8, 2, 128, 64, 10, 0, 2) == size(4, 3, 8, 2, 128, 64, 10, 5, 2) == size(4, 3, 8, 2, 128, 64, 10, 5, 0) == kda.cache_attention_workspace_size(4, 3, 8, 2, 128, 64, 10)
     assert size(4, 3, 8, 3, 128, 64, 10, 5, 2) == size(4, 3, 8, 2, 128, 64, 10, 5, 5) == size(0, 3, 8, 2, 128, 64, 10, 5, 0) == 0
 
 

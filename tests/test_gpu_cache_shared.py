@@ -11,9 +11,18 @@ import gated_delta_rule_34_gb300 as kda
 pytestmark = pytest.mark.gpu
 
 BF16, F32, F64 = torch.bfloat16, torch.float32, torch.float64
-# Which kernels a bf16 call runs follows from its sizes, the prefix table's among them: "wide" fills that up with entries that hold
-# nothing, until the kernel for many rows takes the call.
-KINDS = [BF16, "wide", F32]
+# Whether prefixes are taken by themselves follows from the sizes, the prefix table's width among them: WIDE fills that up with
+# entries that hold nothing, until they are.
+WIDE, WIDE32 = "wide", "wide fp32"
+KINDS = [BF16, F32, WIDE, WIDE32]
+ROOM = 96 << 20                            # bytes of codes that sharing saves
+
+
+def room(sequences, groups, rows, hk, d):
+    """Tokens of prefix tables that are enough."""
+    return ROOM // (max(1, sequences - groups) * hk * -(-rows // 32) * 2 * (64 if d <= 64 else 128)) + 1
+
+
 HALF_STEP = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
 DEV = "cuda"
 
@@ -26,12 +35,12 @@ class Case:
     """groups: (shared tokens, [tokens of each sequence beyond them]); negative: that many tokens short of the prefix;
     None: a place not in use."""
 
-    def __init__(self, seed, T_q, hq, hk, d, page, dtype, groups, before=(), after=(), spread=3, extra_pages=0, room=0):
+    def __init__(self, seed, T_q, hq, hk, d, page, dtype, groups, before=(), after=(), spread=3, extra_pages=0, more=0):
         g = torch.Generator().manual_seed(seed)
         shared = [s for s, _ in groups]
         rows = sum(len(own) for _, own in groups) + len(before) + len(after)
-        wide_extra = 2 ** 21 // max(1, rows * T_q * hq * page) + 1 if dtype == "wide" else 0
-        dtype = BF16 if dtype == "wide" else dtype
+        wide_extra = room(rows, len(groups), T_q * hq // hk, hk, d) // page + 1 if dtype in (WIDE, WIDE32) else 0
+        dtype = {WIDE: BF16, WIDE32: F32}.get(dtype, dtype)
         lengths, cu, of = list(before), [len(before)], [None] * len(before)
         for i, (s, own) in enumerate(groups):
             lengths += [0 if n is None else max(0, s + n) for n in own]
@@ -43,7 +52,7 @@ class Case:
         n_pages = sum(pages(s) for s in shared) + sum(pages(n) for n in lengths) + 2
         ids = iter(torch.randperm(n_pages, generator=g).tolist())
         wide_prefix = max([pages(s) for s in shared] + [0]) + extra_pages + wide_extra
-        wide = max([pages(n) for n in lengths] + [1]) + extra_pages + pages(room)
+        wide = max([pages(n) for n in lengths] + [1]) + extra_pages + pages(more)
         prefix = [[next(ids) for _ in range(pages(s))] for s in shared]
         rows = []
         for n, o in zip(lengths, of):
@@ -189,7 +198,16 @@ def test_halves_of_different_speeds(slow):
         assert all(torch.equal(a, b) for a, b in zip(case.run(), want))
 
 
-@pytest.mark.parametrize("dtype", [BF16, "wide"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T_q, hq, hk, d, n, tokens", [(1, 32, 8, 128, 100, 900), (3, 16, 16, 80, 60, 600), (1, 16, 16, 48, 90, 1000), (40, 16, 4, 128, 20, 1100),
+                                                       (2, 32, 32, 64, 40, 1111)])
+def test_many_sequences_behind_a_short_prefix(dtype, T_q, hq, hk, d, n, tokens):
+    """Sharing pays, and no item is cut."""
+    assert room(n, 1, T_q * hq // hk, hk, d) <= tokens // 32 * 32
+    both(Case(22, T_q, hq, hk, d, 32, dtype, [(tokens, [T_q + i % 37 for i in range(n)])]))
+
+
+@pytest.mark.parametrize("dtype", [WIDE, WIDE32])
 def test_prefixes_of_every_length_around_a_tile(dtype):
     """Ends inside, at and behind a tile of 128 tokens, and inside a page; the prefix's last page whole or not."""
     groups = [(s, [1 + (s + i) % 7 for i in range(2 + s % 3)]) for s in (1, 31, 32, 127, 128, 129, 159, 160, 161, 255, 256, 257, 288, 300)]
@@ -200,10 +218,10 @@ def test_prefixes_of_every_length_around_a_tile(dtype):
 @pytest.mark.parametrize("T_q, hq, hk, d, page, groups", [
     (5, 8, 2, 128, 64, [(64, [5, 6, 300]), (200, [5, 70])]), (40, 4, 2, 80, 16, [(33, [40, 75, 41]), (16, [0, None, -3])]),
     (33, 16, 2, 128, 32, [(140, [33, 34, 2600])]), (3, 14, 2, 112, 16, [(130, [3, 90]), (16, [4] * 9), (47, [3, 1500])])])
-@pytest.mark.parametrize("room", [0, 2000])
-def test_rests_with_room_for_more(T_q, hq, hk, d, page, groups, room):
+@pytest.mark.parametrize("more", [0, 2000])
+def test_rests_with_room_for_more(T_q, hq, hk, d, page, groups, more):
     """Which kernel takes the rest of more than 16 rows a head follows from the room behind the prefix."""
-    both(Case(19, T_q, hq, hk, d, page, BF16, groups, before=[50], after=[0], room=room))
+    both(Case(19, T_q, hq, hk, d, page, WIDE, groups, before=[50], after=[0], more=more))
 
 
 @pytest.mark.parametrize("dtype", KINDS)
@@ -297,7 +315,7 @@ def test_nan_in_the_prefix_reaches_its_channel_only(dtype, n):
     assert bool(torch.isfinite(lse[:n, 0, 2:]).all()) and bool(torch.isfinite(o[n]).all())
 
 
-@pytest.mark.parametrize("dtype, T_q, d", [(BF16, 1, 64), (BF16, 2, 128), (F32, 1, 128), (BF16, 40, 80), ("wide", 1, 64), ("wide", 40, 80)])
+@pytest.mark.parametrize("dtype, T_q, d", [(BF16, 1, 64), (BF16, 2, 128), (WIDE32, 1, 128), (BF16, 40, 80), (WIDE, 1, 64), (WIDE, 40, 80), (WIDE32, 5, 64)])
 def test_strides_buffers_and_another_stream(dtype, T_q, d):
     case = Case(9, T_q, 6, 2, d, 16, dtype, [(100, [T_q + i for i in range(9)]), (33, [T_q, 50])])
     dtype = case.q.dtype
@@ -321,7 +339,7 @@ def test_strides_buffers_and_another_stream(dtype, T_q, d):
     assert bool((guard[:256] == 0xA5).all()) and bool((guard[256 + need:] == 0xA5).all())
 
 
-@pytest.mark.parametrize("dtype, T_q, hq, d", [(BF16, 1, 4, 64), (BF16, 6, 16, 128), ("wide", 1, 4, 64), ("wide", 1, 16, 128), ("wide", 6, 16, 128), (F32, 1, 4, 128)])
+@pytest.mark.parametrize("dtype, T_q, hq, d", [(BF16, 1, 4, 64), (BF16, 6, 16, 128), (WIDE, 1, 4, 64), (WIDE, 1, 16, 128), (WIDE, 6, 16, 128), (F32, 1, 4, 128), (WIDE32, 1, 4, 128), (WIDE32, 8, 16, 64)])
 def test_graph_with_lengths_that_change(dtype, T_q, hq, d):
     """One captured graph, replayed as sequences grow, places come and go, groups change; two graphs with one workspace."""
     case = Case(10, T_q, hq, 2, d, 32, dtype, [(300, [T_q + 40] * 12), (64, [T_q + 60, 90])], after=[50])
@@ -348,7 +366,7 @@ def test_graph_with_lengths_that_change(dtype, T_q, hq, d):
         case.lengths.copy_(ints(full))
 
 
-@pytest.mark.parametrize("dtype, d", [(BF16, 128), ("wide", 128), ("wide", 64), (F32, 128)])
+@pytest.mark.parametrize("dtype, d", [(BF16, 128), (WIDE, 128), (WIDE, 64), (WIDE32, 128)])
 def test_pages_beyond_four_gigabytes(dtype, d):
     case = Case(20, 1, 8, 4, d, 256, dtype, [(700, [1 + i for i in range(6)]), (300, [4, 9])])
     want = both(case)
@@ -421,7 +439,7 @@ def stall():
 @pytest.mark.parametrize("loads, tiles", [(0, 1 << 24), (1, 1 << 24), (1 << 24, 0)])
 def test_bounded_waits_run_out(stall, sequences, loads, tiles):
     """Loads that stop, or products that do, with a limit of 3 ms: the call returns without numbers, and the next is right."""
-    case = Case(17, 1, 8, 2, 64, 64, "wide", [(50000, [1 + i for i in range(sequences)])])
+    case = Case(17, 1, 8, 2, 64, 64, WIDE, [(50000, [1 + i for i in range(sequences)])])
     want, want_lse = case.run()
     torch.cuda.synchronize()
     stall(loads, tiles, 3000)
@@ -436,7 +454,7 @@ def test_bounded_waits_run_out(stall, sequences, loads, tiles):
 
 
 def test_refusals():
-    case = Case(13, 1, 4, 2, 64, 16, BF16, [(64, [5, 60, 7])])
+    case = Case(13, 1, 4, 2, 64, 16, WIDE, [(64, [5, 60, 7])])
     a = dict(q=case.q, cache=case.pool, block_table=case.table, lengths=case.lengths, prefix_table=case.prefix_table,
              prefix_lengths=case.shared, cu_groups=case.cu)
     for change, error, match in [
@@ -482,7 +500,7 @@ def test_a_served_run(dtype, heads, kv_heads, d):
         assert int(kda.cache_resize(refs, table, everyone, lengths, page)) == 0
         kda.cache_write(pool, randn(rows, new, kv_heads, d), randn(rows, new, kv_heads, d), table, start)
         q = randn(rows, new, heads, d)
-        prefix = table[4:5, : prompt // page].contiguous()
+        prefix = torch.nn.functional.pad(table[4:5, : prompt // page], (0, room(rows, 1, new * heads // kv_heads, kv_heads, d) // page + 1), value=-1)
         o, lse = kda.cache_attention_shared(q, pool, table, lengths, prefix, held, ints([0, rows]), return_lse=True)
         alone, alone_lse = kda.cache_attention(q, pool, table, lengths, return_lse=True)
         assert bool(((lse - alone_lse).abs()[alive] <= 2e-5).all())
