@@ -76,6 +76,7 @@ __device__ __forceinline__ int shared_tokens(const CacheAttention& a, int g, int
 // kRest: how many of sequence b's tokens its rows carry the sums of.  All of them must see all of the prefix; a
 // sequence whose rows do not attends over all of its own table.
 __device__ __forceinline__ int carried_tokens(const CacheAttention& a, int b, int len) {
+    if (a.prefix_pages == 0) return 0;
     int g = 0, end = a.n_groups;                           // the last group that starts at b or before
     while (end - g > 1) {
         const int mid = (g + end) >> 1;
@@ -419,7 +420,7 @@ size_t attention_rest_rows_workspace_bytes(const CacheAttention& a, int num_sms)
 size_t attention_prefix_rows_workspace_bytes(const CacheAttention& a, int num_sms);
 cudaError_t run_attention_rows(const CacheAttention& a, bool bf16, void* workspace, cudaStream_t stream, int num_sms);
 cudaError_t run_attention_rest_rows(const CacheAttention& a, bool bf16, void* workspace, cudaStream_t stream, int num_sms);
-cudaError_t run_attention_prefix_rows(const CacheAttention& a, void* workspace, cudaStream_t stream, int num_sms);   // (fp32)
+cudaError_t run_attention_prefix_rows(const CacheAttention& a, bool bf16, void* workspace, cudaStream_t stream, int num_sms);
 
 // What kda_selftest_attention_stall has set on this thread.
 attn::Stall attention_stall();

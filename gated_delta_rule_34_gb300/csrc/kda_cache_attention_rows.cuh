@@ -804,9 +804,7 @@ auto by_rows(const CacheAttention& a, F f) {
 }
 template <Part P, typename F>
 auto by_shape(const CacheAttention& a, bool bf16, F f) {
-    if constexpr (P != kPrefix) {                          // (bf16 rows' prefixes are kda_cache_prefix_tc.cu's)
-        if (bf16) return padded_d(a) == 64 ? by_rows<P, __nv_bfloat16, 64>(a, f) : by_rows<P, __nv_bfloat16, 128>(a, f);
-    }
+    if (bf16) return padded_d(a) == 64 ? by_rows<P, __nv_bfloat16, 64>(a, f) : by_rows<P, __nv_bfloat16, 128>(a, f);
     return padded_d(a) == 64 ? by_rows<P, float, 64>(a, f) : by_rows<P, float, 128>(a, f);
 }
 

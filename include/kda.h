@@ -525,7 +525,7 @@ size_t kda_cache_attention_workspace_size(int B, int T_q, int H_q, int H_kv, int
  *                   them, as kda_cache_fork leaves them.
  * A sequence whose T_q queries all see all of the prefix may take it from prefix_table and the later tokens from its row of
  * block_table; any other (a shorter one, a place not in use with length 0) takes all from its row, and so do all sequences where
- * the sizes leave too little to share: B - n_groups times what the prefix table has room for, less than about 96 MB of codes. So the two
+ * the sizes (B - n_groups, the rows, what the prefix table has room for) leave too little to share, 96 MB of codes or less. So the two
  * must name the same pages, and the results are those of kda_cache_attention but for the order of the sums.
  * Other arguments, rows that see nothing and waits as there, and roundings: fp32 queries as there; bf16 queries over a prefix
  * exactly as two fp8 numbers, down to 2^-13 of their row's largest value, weights in fp16 (11 bits down to 2^-21 of the row's

@@ -11,16 +11,19 @@ import gated_delta_rule_34_gb300 as kda
 pytestmark = pytest.mark.gpu
 
 BF16, F32, F64 = torch.bfloat16, torch.float32, torch.float64
-# Whether prefixes are taken by themselves follows from the sizes, the prefix table's width among them: WIDE fills that up with
+# Whether prefixes are taken by themselves follows from the sizes, the prefix table's width among them: "wide" fills that up with
 # entries that hold nothing, until they are.
 WIDE, WIDE32 = "wide", "wide fp32"
 KINDS = [BF16, F32, WIDE, WIDE32]
-ROOM = 96 << 20                            # bytes of codes that sharing saves
 
 
-def room(sequences, groups, rows, hk, d):
-    """Tokens of prefix tables that are enough."""
-    return ROOM // (max(1, sequences - groups) * hk * -(-rows // 32) * 2 * (64 if d <= 64 else 128)) + 1
+def room(dtype, sequences, groups, rows, hk, d):
+    """Tokens of prefix tables that are enough (fp32 rows that fill their tiles by themselves: none are)."""
+    d = 64 if d <= 64 else 128
+    tile = 10 if rows <= 8 else 16 if rows <= 16 else 32 if rows <= 32 else -(-rows // 64) * 64
+    reads = -(-rows // 32) if dtype == BF16 else (tile - rows) / 8
+    saved = reads * (sequences - groups) * hk * 2 * d
+    return int(((96 << 20) + (1 if dtype == BF16 else 6) * sequences * rows * hk * 8 * d) / saved) + 1 if saved > 0 else 0
 
 
 HALF_STEP = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
@@ -39,8 +42,8 @@ class Case:
         g = torch.Generator().manual_seed(seed)
         shared = [s for s, _ in groups]
         rows = sum(len(own) for _, own in groups) + len(before) + len(after)
-        wide_extra = room(rows, len(groups), T_q * hq // hk, hk, d) // page + 1 if dtype in (WIDE, WIDE32) else 0
-        dtype = {WIDE: BF16, WIDE32: F32}.get(dtype, dtype)
+        wide, dtype = dtype in (WIDE, WIDE32), {WIDE: BF16, WIDE32: F32}.get(dtype, dtype)
+        wide_extra = room(dtype, rows, len(groups), T_q * hq // hk, hk, d) // page + 1 if wide else 0
         lengths, cu, of = list(before), [len(before)], [None] * len(before)
         for i, (s, own) in enumerate(groups):
             lengths += [0 if n is None else max(0, s + n) for n in own]
@@ -199,12 +202,18 @@ def test_halves_of_different_speeds(slow):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("T_q, hq, hk, d, n, tokens", [(1, 32, 8, 128, 100, 900), (3, 16, 16, 80, 60, 600), (1, 16, 16, 48, 90, 1000), (40, 16, 4, 128, 20, 1100),
+@pytest.mark.parametrize("T_q, hq, hk, d, n, tokens", [(1, 32, 8, 128, 120, 900), (3, 16, 16, 80, 60, 600), (1, 16, 16, 48, 90, 1000), (38, 16, 4, 128, 30, 1900),
                                                        (2, 32, 32, 64, 40, 1111)])
 def test_many_sequences_behind_a_short_prefix(dtype, T_q, hq, hk, d, n, tokens):
     """Sharing pays, and no item is cut."""
-    assert room(n, 1, T_q * hq // hk, hk, d) <= tokens // 32 * 32
+    assert 0 < room(dtype, n, 1, T_q * hq // hk, hk, d) <= tokens // 32 * 32
     both(Case(22, T_q, hq, hk, d, 32, dtype, [(tokens, [T_q + i % 37 for i in range(n)])]))
+
+
+@pytest.mark.parametrize("T_q, hq, hk, d", [(1, 4, 2, 128), (2, 16, 2, 64), (1, 8, 1, 96), (1, 2, 2, 16)])
+def test_groups_of_few_rows(T_q, hq, hk, d):
+    """bf16 prefixes on the kernels for few rows: up to 16 rows a group, or 32 of 64 channels."""
+    both(Case(23, T_q, hq, hk, d, 32, WIDE, [(700 + 90 * i, [T_q + 7 * i, T_q + 50]) for i in range(5)], after=[0, 20]))
 
 
 @pytest.mark.parametrize("dtype", [WIDE, WIDE32])
@@ -500,7 +509,7 @@ def test_a_served_run(dtype, heads, kv_heads, d):
         assert int(kda.cache_resize(refs, table, everyone, lengths, page)) == 0
         kda.cache_write(pool, randn(rows, new, kv_heads, d), randn(rows, new, kv_heads, d), table, start)
         q = randn(rows, new, heads, d)
-        prefix = torch.nn.functional.pad(table[4:5, : prompt // page], (0, room(rows, 1, new * heads // kv_heads, kv_heads, d) // page + 1), value=-1)
+        prefix = torch.nn.functional.pad(table[4:5, : prompt // page], (0, room(dtype, rows, 1, new * heads // kv_heads, kv_heads, d) // page + 1), value=-1)
         o, lse = kda.cache_attention_shared(q, pool, table, lengths, prefix, held, ints([0, rows]), return_lse=True)
         alone, alone_lse = kda.cache_attention(q, pool, table, lengths, return_lse=True)
         assert bool(((lse - alone_lse).abs()[alive] <= 2e-5).all())
