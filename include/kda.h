@@ -554,7 +554,8 @@ size_t kda_cache_attention_shared_workspace_size(int B, int T_q, int H_q, int H_
  * The calls below keep refs and one table [n_rows, table_pages] in step, on the device: nothing is read back, so they
  * can be captured.  Layers that share a block table share refs; their pools' pages are copied layer by layer, by
  * kda_cache_copy with the lists of pages that kda_cache_fork and kda_cache_compact write.  Pages are taken lowest first in the order
- * of what asks, so results do not depend on timing.  An entry outside [0, n_pages) holds nothing.
+ * of what asks, so results do not depend on timing.  An entry outside [0, n_pages) holds nothing.  Calls that
+ * share counts, tables or a workspace follow one another (one stream, or events between two).
  *   workspace  kda_cache_pages_workspace_size() bytes, 256-byte aligned; contents on entry are ignored
  *   missing    nullable; device int32 [1] (written): pages that were wanted and not there
  * All tables, lists and counts are dense and apart from one another unless stated; at most 65536 rows or pairs a call,

@@ -375,6 +375,27 @@ def test_graph_with_lengths_that_change(dtype, T_q, hq, d):
         case.lengths.copy_(ints(full))
 
 
+def test_calls_at_once():
+    """Two streams' calls, each with its workspace, beside attention over each row alone."""
+    cases = [Case(24 + i, T_q, hq, 2, d, 32, WIDE, [(3000 + 500 * i, [T_q + 3 * j for j in range(40)])]) for i, (T_q, hq, d) in enumerate([(1, 16, 128), (9, 8, 80)])]
+    want = [both(c) for c in cases]
+    alone = kda.cache_attention(cases[1].q, cases[1].pool, cases[1].table, cases[1].lengths)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for stream, case in zip(streams, cases):
+            with torch.cuda.stream(stream):
+                got.append(case.run())
+        with torch.cuda.stream(streams[2]):
+            got.append(kda.cache_attention(cases[1].q, cases[1].pool, cases[1].table, cases[1].lengths))
+    torch.cuda.synchronize()
+    for i in range(0, len(got), 3):
+        for (o, lse), (wo, wl) in zip(got[i: i + 2], want):
+            assert torch.equal(o, wo) and torch.equal(lse, wl)
+        assert torch.equal(got[i + 2], alone)
+
+
 @pytest.mark.parametrize("dtype, d", [(BF16, 128), (WIDE, 128), (WIDE, 64), (WIDE32, 128)])
 def test_pages_beyond_four_gigabytes(dtype, d):
     case = Case(20, 1, 8, 4, d, 256, dtype, [(700, [1 + i for i in range(6)]), (300, [4, 9])])
