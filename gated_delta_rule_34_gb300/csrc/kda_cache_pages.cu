@@ -632,7 +632,8 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_parts_kernel(con
             for (int k = 0; k < kCopyLoads; ++k) {
                 const int at = begin + k * kCopyThreads, kv = at >= a.vectors;
                 if (at < both)
-                    x[k] = __ldcs(reinterpret_cast<const uint4*>(kv ? a.codes[1] : a.codes[0]) + (int64_t)from * a.vectors + at - kv * a.vectors);
+                    x[k] = __ldcs(reinterpret_cast<const uint4*>(kv ? a.codes[1] : a.codes[0]) + (int64_t)from * a.vectors + at -
+                                  kv * a.vectors);
             }
 #pragma unroll
             for (int k = 0; k < kCopyLoads; ++k) {

@@ -1059,7 +1059,9 @@ struct Softmax {
             const int r = (two ? stream * kRows : 0) + row;
             const int64_t at = (int64_t)p.rows256 * kPair + r;
             const bool real = at < p.rows;
-            const int64_t out = !real ? 0 : p.whole ? prefix_row(a, c.plan, p.first_seq, p.hk, at) : ((int64_t)blockIdx.x * 2 + p.slot) * kPair + r;
+            const int64_t out = !real    ? 0
+                                : p.whole ? prefix_row(a, c.plan, p.first_seq, p.hk, at)
+                                          : ((int64_t)blockIdx.x * 2 + p.slot) * kPair + r;
             float* to = (p.whole ? a.carry_sums : c.plan.sums) + out * c.plan.D;
             // (join_sums' factors, once)
             const float m_all = other ? fmaxf(M, stat.x) : M, dm_all = other ? fminf(DM + (m_all - M), stat.y + (m_all - stat.x)) : DM;
@@ -1093,8 +1095,8 @@ struct Softmax {
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
-    prefix_tc_kernel(const __grid_constant__ CacheAttention a, const __grid_constant__ PrefixPlan plan, const __grid_constant__ CUtensorMap k_map,
-                     const __grid_constant__ CUtensorMap v_map) {
+    prefix_tc_kernel(const __grid_constant__ CacheAttention a, const __grid_constant__ PrefixPlan plan,
+                     const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Small* small = reinterpret_cast<Small*>(sm + kSmallAt);

@@ -79,7 +79,8 @@ size_t cache_attention_shared_workspace_bytes(const CacheAttention& a, int num_s
 
 cudaError_t run_cache_attention_shared(CacheAttention a, bool bf16, void* workspace, cudaStream_t stream, int num_sms) {
     if (!sharing_pays(a, bf16) || a.n_pages == 0) {
-        // Each sequence by itself: many rows of few tokens as the rest of more, with nothing carried.
+        // Each sequence by itself: many rows of few tokens as the rest of more, with nothing carried (40 of 260 rows, 96 tokens:
+        // 64 us, on the tensor cores' kernel 133; 576 tokens 183 and 198).
         a.prefix_pages = 0;
         if (attention_tc_takes(a, bf16) && !rest_is_long(a, bf16)) return run_attention_rest_rows(a, bf16, workspace, stream, num_sms);
         return run_cache_attention(a, bf16, workspace, stream, num_sms);
