@@ -51,8 +51,11 @@ class Plain:
 
     def fork(self, lengths, src, dst):
         copies, ask, missing = [(-1, -1)] * len(src), [], 0
+        seen, sources = set(), set(src)
         for i, (a, b) in enumerate(zip(src, dst)):
-            if not (0 <= a < len(self.table) and 0 <= b < len(self.table)) or b in dst[:i] or b in src:
+            earlier = b in seen
+            seen.add(b)
+            if not (0 <= a < len(self.table) and 0 <= b < len(self.table)) or earlier or b in sources:
                 continue
             n = min(max(lengths[a], 0), self.wide * self.page)
             full = n // self.page
@@ -105,7 +108,8 @@ def scattered(rng, n_pages, n_rows, wide, fill, share=0.3):
 
 # (lists of more than 1,024 rows go another way, and so do warps with more than 1,024 pages)
 SIZES = [(400_000, 6, 40), (1, 1, 1), (7, 3, 5), (40, 9, 31), (100, 33, 32), (1000, 20, 257), (5000, 70, 300), (40001, 130, 300), (9000, 1, 9000), (300, 9001, 1),
-         (30000, 300, 400), (20000, 1500, 90)]           # (and calls of more than 65,536 entries)
+         (30000, 300, 400), (20000, 1500, 90),           # (calls of more than 65,536 entries)
+         (200, 16000, 1), (3000, 8193, 2)]               # (more rows than one CTA counts, little else to look through)
 
 
 @pytest.mark.parametrize("n_pages, n_rows, wide", SIZES)
@@ -140,7 +144,7 @@ def test_resize_of_counts_that_do_not_match():
 
 
 @pytest.mark.parametrize("n_pages, n_rows, wide", [(12, 6, 3), (100, 33, 32), (3000, 70, 300), (300, 600, 2), (50, 8, 1), (4000, 5000, 3), (9000, 3000, 17),
-                                                   (30000, 700, 300), (60000, 3000, 60)])
+                                                   (30000, 700, 300), (60000, 3000, 60), (100, 19000, 1), (100, 16500, 0)])
 def test_fork(n_pages, n_rows, wide):
     page = 32
     rng = random.Random(n_pages)
