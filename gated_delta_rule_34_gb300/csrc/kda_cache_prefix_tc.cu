@@ -65,6 +65,7 @@ constexpr int kItemCost = 4;               // what an item's start and end cost,
 constexpr int kLeastShare = 8;
 constexpr int kRun = 64;                   // tiles that O sums up
 constexpr float kBits = 7.0f, kFar = 8.0f; // log2 of the largest weight at its reference, and of how far above it
+constexpr float kFarScore = 64.0f;         // and of how far a score may be above m: l is a sum of 2^(s - m)
 constexpr float kNear = 4194304.0f;        // 2^22: below, scores have places behind the point
 // Named barriers: 1 to 8 of the two warps that have the same rows, 9 and 10 of a stream's, 11 of both streams'.
 constexpr int kBarRows = 1, kBarStream = 9, kBarBoth = 11;
@@ -939,8 +940,9 @@ struct Softmax {
                     reach = fmaxf(reach, (x - m) + (j ? st.w : st.y));   // (m first: it may have no places to add to)
                 }
             }
-            // Where a weight would be too large, all references of the two warps' rows move to the largest so far.
-            if (vote_rows(reach - dr > kFar || (!seen && top > -INFINITY), id)) {
+            // Where a weight would be too large, by its page's values or (on pages of values far smaller than others) by its score
+            // alone, all references of the two warps' rows move to the largest so far.
+            if (vote_rows(reach - dr > kFar || top - m > kFarScore || (!seen && top > -INFINITY), id)) {
                 c.small->top[stream][half][row] = top;
                 tc::named_bar_sync(id, 64);
                 top = fmaxf(top, c.small->top[stream][half ^ 1][row]);
