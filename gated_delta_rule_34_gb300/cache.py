@@ -222,7 +222,8 @@ def cache_write(cache: PagedCache, k, v, block_table, start, cu_seqlens=None) ->
 
     k, v: [B, T, H_kv, d], or with cu_seqlens (int32 [N + 1]) packed [1, T_total, H_kv, d] (fp32 or
     bf16, tokens evenly spaced, heads dense); block_table: int32 [N, table_pages];
-    start: int32 [N], the position of each sequence's first new token.
+    start: int32 [N], the position of each sequence's first new token.  No page that is written to may have another
+    holder: a row cut inside a page that it shares parts from it first, see cache_fork.
     """
     done = _binding().cache_write(cache, k, v, block_table, start, cu_seqlens)
     if done is not None:
@@ -406,9 +407,13 @@ def cache_fork(refs, block_table, lengths, src, dst, page: int, from_pages=None,
     """Rows dst[i] of the block table become the sequences of rows src[i], through kda_cache_fork: full pages are shared, a
     partly filled last page is replaced by a free one.  In place; dst rows must hold nothing (cache_resize to 0 gives back).
 
-    refs, block_table, page: as in cache_resize; lengths: int32 [n_rows], tokens of each row (dst's are set); src, dst: int32 [n],
-    a source may stand in many pairs.  Returns (from_pages, to_pages, missing): the pages to copy, int32 [n], -1 where there is none
+    refs, block_table, page: as in cache_resize; lengths: int32 [n_rows], tokens of each row (dst's are set; with less for a source
+    than it has, the branch begins earlier); src, dst: int32 [n], a source may stand in many pairs.  Returns (from_pages, to_pages, missing): the pages to copy, int32 [n], -1 where there is none
     (cache_copy, for the pool of each layer that has this table), and int32 [1], pages wanted when the pool had no more.
+
+    A row taken back to a length inside a page that it shares must not be written to, for its other holders' sake.  It goes on as its
+    own fork: its lengths entry set, cache_fork to a row that holds nothing, cache_copy, then cache_resize of the old row to 0.  The
+    states of recurrent layers are the caller's to copy.
     """
     done = _binding().cache_fork(refs, block_table, lengths, src, dst, page, from_pages, to_pages, missing, workspace)
     if done is not None:

@@ -449,7 +449,8 @@ kda_status kda_rotary(const void *q, int64_t q_stride, void *q_out, int64_t q_ou
  * become 448, NaN stays NaN, and neither counts for the scale.  Writing is
  * appending: codes that lie behind the new tokens in their page do not follow
  * a scale that grew.
- * No two sequences may write to the same page in one call.  Malformed
+ * No two sequences may write to the same page in one call, and none to a page that
+ * another holds too (below, "Sequences that share pages").  Malformed
  * cu_seqlens are clamped into [0, T]: results are then unspecified, but no
  * access leaves the buffers.
  */
@@ -556,6 +557,10 @@ size_t kda_cache_attention_shared_workspace_size(int B, int T_q, int H_q, int H_
  * kda_cache_copy with the lists of pages that kda_cache_fork and kda_cache_compact write.  Pages are taken lowest first in the order
  * of what asks, so results do not depend on timing.  An entry outside [0, n_pages) holds nothing.  Calls that
  * share counts, tables or a workspace follow one another (one stream, or events between two).
+ * A page with more than one holder is not to be written to: kda_cache_write knows no counts, and would change its other holders'
+ * tokens, or round them again where the page's scale grows.  A fork has no such page to write to; a row that is taken back to a length
+ * inside a page that it shares has.  It parts from it by a fork: with its lengths[r] the new one, to a row that holds nothing, whose
+ * listed page is copied; then row r is resized to 0, and the sequence goes on in the other.
  *   workspace  kda_cache_pages_workspace_size() bytes, 256-byte aligned; contents on entry are ignored
  *   missing    nullable; device int32 [1] (written): pages that were wanted and not there
  * All tables, lists and counts are dense and apart from one another unless stated; at most 65536 rows or pairs a call,
@@ -586,11 +591,13 @@ kda_status kda_cache_resize(int32_t *refs, int64_t n_pages, int32_t *block_table
 /*
  * kda_cache_fork -- row dst[i] becomes the sequence of row src[i], of lengths[src[i]] tokens: its full pages are shared
  * (refs and one), a partly filled last page is replaced by a free one, the rest of the row holds nothing, and
- * lengths[dst[i]] is set.  What row dst[i] held is not given back (resize it to 0 first).  For each i
+ * lengths[dst[i]] is set.  What row dst[i] held is not given back (resize it to 0 first).  The states of recurrent layers beside
+ * this one are the caller's to copy: that of the token where row dst[i] begins (kda_chunk_prefill_checkpoints).  For each i
  *   from_pages[i], to_pages[i]  (written) the page to copy before the row's next token, and where to; -1 and -1
  *                               where there is none: full pages only, a last page that is not held, or no free page (the
  *                               row's entry is then -1 and counts as missing)
- *   lengths   device int32 [n_rows], clamped into [0, table_pages * page]
+ *   lengths   device int32 [n_rows], clamped into [0, table_pages * page]; what a source gives is what they say, so that a copy of
+ *             the sequences' own with less for a source branches from an earlier token
  *   src, dst  device int32 [n]; a source may stand in many pairs.  A pair is skipped where a row is outside the table,
  *             where dst[i] is an earlier pair's, or some pair's source.
  */
