@@ -320,7 +320,8 @@ def cache_attention_shared(q, cache: PagedCache, block_table, lengths, prefix_ta
     each sequence from its first token on, as cache_fork leaves them.  prefix_table: int32 [G, prefix_pages], the pages of each
     group's prefix; prefix_lengths: int32 [G], its tokens, of which whole pages are shared; cu_groups: int32 [G + 1], group g
     is sequences cu_groups[g] .. cu_groups[g + 1] - 1.  A sequence some of whose queries do not see all of the prefix attends
-    over its own row alone, and so do all where the sizes (by the prefix table's width) leave too little to share.
+    over its own row alone, and so do all where the sizes leave too little to share; these go by the prefix table's width, which had
+    better be no more than the longest prefix needs.
     """
     done = _binding().cache_attention_shared(q, cache, block_table, lengths, prefix_table, prefix_lengths, cu_groups, scale, out, lse,
                                              return_lse, workspace)

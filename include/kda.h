@@ -526,11 +526,19 @@ size_t kda_cache_attention_workspace_size(int B, int T_q, int H_q, int H_kv, int
  *                   them, as kda_cache_fork leaves them.
  * A sequence whose T_q queries all see all of the prefix may take it from prefix_table and the later tokens from its row of
  * block_table; any other (a shorter one, a place not in use with length 0) takes all from its row, and so do all sequences where
- * the sizes (B - n_groups, the rows, what the prefix table has room for) leave too little to share, 96 MB of codes or less. So the two
- * must name the same pages, and the results are those of kda_cache_attention but for the order of the sums.
- * Other arguments, rows that see nothing and waits as there, and roundings: fp32 queries as there; bf16 queries over a prefix
- * exactly as two fp8 numbers, down to 2^-13 of their row's largest value, weights in fp16 (11 bits down to 2^-21 of the row's
- * reference, lost below 2^-32 of it), sums of at most 64 tiles of 128 tokens as the products add them, then rounded additions.
+ * the sizes leave too little to share. So the two must name the same pages, and the results are those of kda_cache_attention but for
+ * the order of the sums and the roundings below.
+ *   The sizes are B - n_groups (places not in use count), the rows a head, and what the prefix table has room for, whatever
+ * prefix_lengths say: one no wider than the longest prefix serves best.  bf16: shared from 96 MB of codes (and as much as all rows'
+ * sums) on that would be read again, once for each 32 rows of each further sequence.  fp32, bound by its products: from 96 MB and six
+ * times the sums on, for each 8 rows that tiles of 8, 16, 32 or a multiple of 64 rows a head leave empty; so 16, 32 or a multiple of
+ * 64 rows a head never.
+ * Other arguments, rows that see nothing and waits as there, and roundings.  fp32 as there.  bf16 over shared prefixes, where groups
+ * have more than 16 rows a head on average (32 for up to 64 channels): queries as two fp8 numbers, exact down to 2^-13 of their row's
+ * largest value, smaller ones within 2^-21 of it; weights in fp16, 11 bits down to 2^-21 of the row's reference, lost below 2^-32 of it;
+ * sums of at most 64 tiles of 128 tokens as the products add them, then rounded additions.  All other bf16 rows as there: as those of at most
+ * 16 rows a head, but with more of more than 64 channels and room for more than 1,024 tokens (of the block table; behind shared prefixes
+ * of what it has beyond their table).
  *   workspace  kda_cache_attention_shared_workspace_size() bytes, 256-byte aligned; contents on entry are ignored
  */
 kda_status kda_cache_attention_shared(const void *q, int64_t q_stride, const void *k_codes,
