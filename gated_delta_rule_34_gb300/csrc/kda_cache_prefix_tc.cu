@@ -23,8 +23,9 @@
 //   1 issuer     S of a stream's next tile after the O of its last one, since S and W share their columns
 //   1 loader     pages by TMA, 128-byte-swizzled rows, a box a page (of up to 128 tokens); their scales
 //   1 planner    the CTA's pieces, told to the others through shared memory
-// A row's reference moves when a score passes it by more than a factor of 128; it is a whole number, so that weights,
-// moves and the sum of weights l, which is taken from the same weights step by step, have no rounding of their own.
+// A row's references, m of its scores and m + dr of its weights times their pages' scales of values, are whole numbers, so that
+// moving them rounds nothing.  A weight is 2^7 at most where they were set; they move when one would pass 2^15, or a score 2^64 times
+// 2^m.  l sums the exponentials in fp32, before they are rounded to the fp16 weights (11 bits) that meet the values.
 //
 // The products' sums are cut off, not rounded: every 64 tiles O goes to sums in the workspace by rounded additions.
 //
