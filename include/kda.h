@@ -500,6 +500,8 @@ kda_status kda_cache_read(const void *k_codes, const void *v_codes, const float 
  * to the row's largest w_t times its page's scale of v: what lies below 2^-36 of
  * that is lost (below 2^-30 with more than 16 bf16 rows a head, T_q * H_q / H_kv, of
  * more than 64 channels, whose products take the codes as they are).
+ * A w_t below 2^-100 of the row's largest counts too little or not at all, whatever
+ * its page's scale of v: that matters where scales in a row lie 2^100 and more apart.
  */
 kda_status kda_cache_attention(const void *q, int64_t q_stride, const void *k_codes,
                                const void *v_codes, const float *k_scale, const float *v_scale,
